@@ -15,6 +15,10 @@ library's gfx950 kernels.  The functions carry the C entry points' names:
                                                         recv_topk_weights)
   ep_combine_partitioned(y, layout, ...)            -> combined_x
   ep_combine_reduced(y, layout, topk_idx, ...)      -> combined_x
+  ep_expert_linear(x, w, layout, ...)               -> (out, checkpoint)
+  ep_expert_wgrad(dy, x, layout, ...)               -> (dw, db)
+  ep_expert_activation_backward(dh, pre, layout, ...) -> (dpre, h, dweights)
+  ep_moe_decode(x, topk_idx, topk_weights, w1, w2, ...) -> out
 
 Semantics follow the DeepEP v2 test page ("DeepEP test target API
 reference", sec. 2.1 dispatch, 2.2 combine, 3.1-3.2 the V1 layout tensors and
@@ -37,6 +41,8 @@ __all__ = ["load_library", "Layout", "ep_get_layout", "ep_get_layout_noalloc", "
            "ep_combine", "ep_cast_fp8", "logfmt_row_bytes", "ep_logfmt_encode",
            "ep_logfmt_decode", "ep_combine_logfmt",
            "ep_dispatch_partitioned", "ep_combine_partitioned", "ep_combine_reduced",
+           "ep_expert_linear",
+           "ep_expert_wgrad", "ep_expert_activation_backward", "ep_moe_decode",
            "worst_case_recv_rows", "ep_probe_dispatch_stores", "EpError", "EP_DEV_BAD_EXPERT", "EP_DEV_CAPACITY",
            "EP_DEV_RECV_OVERFLOW"]
 
@@ -767,4 +773,275 @@ def ep_combine_reduced(y: torch.Tensor, layout: Layout, topk_idx: torch.Tensor,
             _ptr(y), H, rows, _ptr(topk_idx), _ptr(topk_weights), _ptr(b0),
             _ptr(b1), ctypes.byref(params), ctypes.byref(ptrs), _ptr(out),
             1 if bf16_partials else 0, _stream(y.device))
+    return out
+
+
+# Activations of the expert operators: the function, and whether it is gated
+# (a row of pre-activations is then [gate | up] and the result half as wide).
+_ACTS = {"none": _abi.EP_ACT_NONE, "silu": _abi.EP_ACT_SILU, "gelu": _abi.EP_ACT_GELU,
+         "swiglu": _abi.EP_ACT_SWIGLU, "geglu": _abi.EP_ACT_GEGLU}
+_FP8_ROW_GROUP = 128
+_CHECKPOINT_GROUP = 32
+
+
+def _activation(name: str):
+    if name not in _ACTS:
+        raise ValueError(f"activation must be one of {sorted(_ACTS)}")
+    return _ACTS[name], name in ("swiglu", "geglu")
+
+
+def _check3(t: torch.Tensor, name: str, dtypes, shape):
+    _need_cuda(t, name)
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
+
+
+def _rows_and_scales(v, name):
+    """(tensor, scales or None) of bf16 rows or of e4m3 codes with UE8M0
+    scales per 128 channels, along the last dimension."""
+    if not isinstance(v, (tuple, list)):
+        _need_cuda(v, name)
+        if v.dtype != torch.bfloat16:
+            raise ValueError(f"{name} must be bf16, or (fp8 codes, UE8M0 scales)")
+        return v, None
+    codes, scales = v
+    _need_cuda(codes, name)
+    if not _is_fp8(codes):
+        raise ValueError(f"{name} must be bf16, or (fp8 codes, UE8M0 scales)")
+    if codes.shape[-1] % _FP8_ROW_GROUP:
+        raise ValueError(f"fp8 {name} needs a multiple of {_FP8_ROW_GROUP} channels")
+    if scales is None or scales.dtype != torch.uint8:
+        raise ValueError(f"{name}'s scales must be uint8 (scale_fmt='ue8m0')")
+    _check3(scales, f"{name} scales", _U8, (*codes.shape[:-1], codes.shape[-1] // _FP8_ROW_GROUP))
+    return codes, scales
+
+
+def ep_expert_linear(x: Union[torch.Tensor, Tuple[torch.Tensor, torch.Tensor]],
+                     w: Union[torch.Tensor, Tuple[torch.Tensor, torch.Tensor]], layout: Layout,
+                     bias: Optional[torch.Tensor] = None, activation: str = "none",
+                     residual: Optional[torch.Tensor] = None, transposed: bool = False,
+                     checkpoint: Union[bool, Tuple[torch.Tensor, torch.Tensor], None] = None,
+                     out: Optional[torch.Tensor] = None):
+    """The experts' matrix product over the receive rows, with its epilogue:
+    z[r] = w[e] x[r] + bias[e], out[r] = act(z[r]) + residual[r], e the expert
+    of row r.
+
+    x: bf16 [rows, K], or (e4m3 codes [rows, K], UE8M0 scales uint8
+    [rows, K/128]) as ep_dispatch(recv_fp8=True, scale_fmt="ue8m0") gives them.
+    w: the same type, [E, N, K] (scales [E, N, K/128]); with transposed=True
+    (bf16) [E, K, N], which is the data gradient on the forward weights.
+    bias: bf16 [E, N].  activation: "none", "silu", "gelu" (tanh form), or
+    "swiglu" / "geglu" on z = [gate | up].  residual: bf16 like out.
+    checkpoint=True (or the two buffers) also keeps z in 8 bits: (e4m3 codes
+    [rows, N], UE8M0 scales uint8 [rows, N/32]) for
+    ep_expert_activation_backward.  Returns (out bf16 [rows, N or N/2],
+    checkpoint or None).  Padding rows are left as they were."""
+    lib = load_library()
+    act, gated = _activation(activation)
+    x, x_scales = _rows_and_scales(x, "x")
+    w, w_scales = _rows_and_scales(w, "w")
+    if (x_scales is None) != (w_scales is None):
+        raise ValueError("x and w must both be bf16 or both be fp8")
+    if x.dim() != 2 or w.dim() != 3:
+        raise ValueError("x must be [rows, K] and w [E, N, K]")
+    rows, K = x.shape
+    E = layout.num_experts
+    N = w.shape[2] if transposed else w.shape[1]
+    _check3(w, "w", _F8 if w_scales is not None else _BF16, (E, K, N) if transposed else (E, N, K))
+    M = N // 2 if gated else N
+    dev = x.device
+    if bias is not None:
+        _check3(bias, "bias", _BF16, (E, N))
+    if residual is not None:
+        _check(residual, "residual", _BF16, M, min_rows=rows)
+    if out is None:
+        out = torch.empty((rows, M), dtype=torch.bfloat16, device=dev)
+    _check(out, "out", _BF16, M, min_rows=rows)
+    codes = scales = None
+    if isinstance(checkpoint, (tuple, list)):
+        codes, scales = checkpoint
+    elif checkpoint:
+        codes = torch.empty((rows, N), dtype=torch.float8_e4m3fn, device=dev)
+        scales = torch.empty((rows, N // _CHECKPOINT_GROUP), dtype=torch.uint8, device=dev)
+    if codes is not None:
+        if N % _CHECKPOINT_GROUP:
+            raise ValueError(f"a checkpoint needs a multiple of {_CHECKPOINT_GROUP} columns")
+        _check(codes, "checkpoint codes", _F8, N, min_rows=rows)
+        _check(scales, "checkpoint scales", _U8, N // _CHECKPOINT_GROUP, min_rows=rows)
+    params = layout.params
+    ptrs = layout.ptrs()
+    _launch("ep_expert_linear", dev, lib.ep_expert_linear,
+            [x_scales, w, w_scales, bias, residual, out, codes, scales, layout.status],
+            _ptr(x), _abi.EP_DTYPE_BF16 if x_scales is None else _abi.EP_DTYPE_FP8_E4M3_UE8M0,
+            _ptr(x_scales), _ptr(w), _ptr(w_scales), N, K, 1 if transposed else 0, _ptr(bias), act,
+            _ptr(residual), ctypes.byref(params), ctypes.byref(ptrs), rows, _ptr(out),
+            _ptr(codes), _ptr(scales), _stream(dev))
+    return out, (None if codes is None else (codes, scales))
+
+
+def ep_expert_wgrad(dy: torch.Tensor, x: Union[torch.Tensor, Tuple[torch.Tensor, torch.Tensor]],
+                    layout: Layout, bias_grad: bool = False, dtype: torch.dtype = torch.float32,
+                    accumulate: Optional[Sequence[Optional[torch.Tensor]]] = None,
+                    out: Optional[Sequence[Optional[torch.Tensor]]] = None):
+    """The experts' weight gradient over the receive rows: dw[e] = sum of
+    dy[r]^T x[r] over the rows of expert e, [E, N, K] in `dtype` (float32 or
+    bfloat16), and with bias_grad db[e] = sum of dy[r], float32 [E, N].
+
+    dy: bf16 [rows, N].  x: bf16 [rows, K], or (e4m3 codes, UE8M0 scales per
+    128 channels), the rows of an fp8 dispatch kept for the backward pass.
+    accumulate=(dw0, db0): gradients the new ones are added to (db0 None
+    without bias_grad); `out` may name the result buffers, the same tensors
+    included.  An expert without rows gets zeros (or its dw0).  Returns
+    (dw, db or None)."""
+    lib = load_library()
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("dtype must be float32 or bfloat16")
+    x, x_scales = _rows_and_scales(x, "x")
+    if x.dim() != 2 or dy.dim() != 2:
+        raise ValueError("dy must be [rows, N] and x [rows, K]")
+    rows, K = x.shape
+    N = dy.shape[1]
+    _check(dy, "dy", _BF16, N, rows=rows)
+    E = layout.num_experts
+    dev = dy.device
+    dw, db = (list(out) + [None, None])[:2] if out is not None else (None, None)
+    dw0, db0 = (list(accumulate) + [None, None])[:2] if accumulate is not None else (None, None)
+    if accumulate is not None and dw0 is None:
+        raise ValueError("accumulate needs the weight gradients to add to")
+    if (db is not None or db0 is not None) and not bias_grad:
+        raise ValueError("db is given without bias_grad")
+    if accumulate is not None and bias_grad and db0 is None:
+        raise ValueError("accumulate with bias_grad needs both gradients")
+    if dw is None:
+        dw = torch.empty((E, N, K), dtype=dtype, device=dev)
+    if bias_grad and db is None:
+        db = torch.empty((E, N), dtype=torch.float32, device=dev)
+    for name, t in (("dw", dw), ("accumulate dw", dw0)):
+        if t is not None:
+            _check3(t, name, (dtype,), (E, N, K))
+    for name, t in (("db", db), ("accumulate db", db0)):
+        if t is not None:
+            _check3(t, name, _F32, (E, N))
+    params = layout.params
+    ptrs = layout.ptrs()
+    _launch("ep_expert_wgrad", dev, lib.ep_expert_wgrad,
+            [x, x_scales, dw0, db0, dw, db, layout.status],
+            _ptr(dy), _ptr(x),
+            _abi.EP_DTYPE_BF16 if x_scales is None else _abi.EP_DTYPE_FP8_E4M3_UE8M0,
+            _ptr(x_scales), N, K, ctypes.byref(params), ctypes.byref(ptrs), rows, _ptr(dw0),
+            _ptr(db0), _ptr(dw), 1 if dtype == torch.bfloat16 else 0, _ptr(db), _stream(dev))
+    return dw, db
+
+
+def ep_expert_activation_backward(dh: torch.Tensor,
+                                  pre: Union[torch.Tensor, Tuple[torch.Tensor, torch.Tensor]],
+                                  layout: Layout, activation: str = "swiglu",
+                                  row_weights: Optional[torch.Tensor] = None,
+                                  out: Optional[Sequence[Optional[torch.Tensor]]] = None):
+    """The gradient through the experts' activation h = act(z).
+
+    pre: z, as the checkpoint of ep_expert_linear (e4m3 codes [rows, N], UE8M0
+    scales [rows, N/32]) or bf16 [rows, N].  dh: bf16 [rows, M] (M = N, N/2
+    gated), the gradient of row_weights[r] * h[r] (float32 [rows], ep_dispatch's
+    recv_topk_weights; 1 if None).  Returns (dpre bf16 [rows, N], row_weights *
+    h bf16 [rows, M], dweights float32 [rows] = sum of dh * h).  Padding rows
+    are left as they were; `out` may name the three buffers (None entries are
+    allocated)."""
+    lib = load_library()
+    act, gated = _activation(activation)
+    scales = None
+    if isinstance(pre, (tuple, list)):
+        pre, scales = pre
+    _need_cuda(pre, "pre")
+    if pre.dim() != 2:
+        raise ValueError("pre must be [rows, N]")
+    rows, N = pre.shape
+    M = N // 2 if gated else N
+    if scales is None:
+        _check(pre, "pre", _BF16, N)
+    else:
+        if N % _CHECKPOINT_GROUP:
+            raise ValueError(f"a checkpoint needs a multiple of {_CHECKPOINT_GROUP} columns")
+        _check(pre, "pre codes", _F8, N)
+        _check(scales, "pre scales", _U8, N // _CHECKPOINT_GROUP, rows=rows)
+    _check(dh, "dh", _BF16, M, rows=rows)
+    _check(row_weights, "row_weights", _F32, min_rows=rows)
+    dev = dh.device
+    dpre, h, dw = (list(out) + [None] * 3)[:3] if out is not None else (None, None, None)
+    if dpre is None:
+        dpre = torch.empty((rows, N), dtype=torch.bfloat16, device=dev)
+    if h is None:
+        h = torch.empty((rows, M), dtype=torch.bfloat16, device=dev)
+    if dw is None:
+        dw = torch.empty(rows, dtype=torch.float32, device=dev)
+    _check(dpre, "dpre", _BF16, N, min_rows=rows)
+    _check(h, "h", _BF16, M, min_rows=rows)
+    _check(dw, "dweights", _F32, min_rows=rows)
+    params = layout.params
+    ptrs = layout.ptrs()
+    _launch("ep_expert_activation_backward", dev, lib.ep_expert_activation_backward,
+            [pre, scales, row_weights, dpre, h, dw, layout.status],
+            _ptr(dh), _ptr(pre), _ptr(scales), N, act, _ptr(row_weights), ctypes.byref(params),
+            ctypes.byref(ptrs), rows, _ptr(dpre), _ptr(h), _ptr(dw), _stream(dev))
+    return dpre, h, dw
+
+
+def ep_moe_decode(x: torch.Tensor, topk_idx: torch.Tensor, topk_weights: Optional[torch.Tensor],
+                  w1: Union[torch.Tensor, Tuple[torch.Tensor, torch.Tensor]],
+                  w2: Union[torch.Tensor, Tuple[torch.Tensor, torch.Tensor]],
+                  activation: str = "swiglu", w1_bias: Optional[torch.Tensor] = None,
+                  w2_bias: Optional[torch.Tensor] = None,
+                  bias: Union[None, torch.Tensor, Tuple[torch.Tensor, torch.Tensor]] = None,
+                  status: Optional[torch.Tensor] = None,
+                  out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """A whole mixture-of-experts layer for a few tokens (at most 1024 (token,
+    expert) pairs), without a layout: out[t] = bias0 + bias1 + sum_k w[t,k] *
+    (w2[e] act(w1[e] x[t] + w1_bias[e]) + w2_bias[e]), e = topk_idx[t,k].
+
+    x: bf16 [T, H].  topk_idx: int64 [T, K], -1 = none.  topk_weights: float32
+    [T, K], or None for the plain sum.  w1: bf16 [E, N, H] (N = 2I for "swiglu"
+    and "geglu", gate rows first) and w2: bf16 [E, H, I]; or both (e4m3 codes,
+    UE8M0 scales uint8 per 128 channels).  w1_bias: bf16 [E, N], w2_bias: bf16
+    [E, H].  bias: up to two bf16 [T, H] tensors, as ep_combine's (a residual,
+    a shared expert's output).  status: int32 [1], gets EP_DEV_BAD_EXPERT when
+    an id is outside [-1, E).  Returns bf16 [T, H]."""
+    lib = load_library()
+    act, gated = _activation(activation)
+    w1, s1 = _rows_and_scales(w1, "w1")
+    w2, s2 = _rows_and_scales(w2, "w2")
+    if (s1 is None) != (s2 is None):
+        raise ValueError("w1 and w2 must both be bf16 or both be fp8")
+    if x.dim() != 2 or w1.dim() != 3 or w2.dim() != 3 or topk_idx.dim() != 2:
+        raise ValueError("x must be [T, H], topk_idx [T, K], w1 [E, N, H] and w2 [E, H, I]")
+    T, H = x.shape
+    E, N = w1.shape[:2]
+    inter = N // 2 if gated else N
+    kinds = _BF16 if s1 is None else _F8
+    _check(x, "x", _BF16, H)
+    _check3(w1, "w1", kinds, (E, 2 * inter if gated else N, H))
+    _check3(w2, "w2", kinds, (E, H, inter))
+    K = topk_idx.shape[1]
+    _check(topk_idx, "topk_idx", _I64, K, rows=T)
+    _check(topk_weights, "topk_weights", _F32, K, rows=T)
+    if w1_bias is not None:
+        _check3(w1_bias, "w1_bias", _BF16, (E, N))
+    if w2_bias is not None:
+        _check3(w2_bias, "w2_bias", _BF16, (E, H))
+    b0, b1 = _biases(bias, T, H)
+    dev = x.device
+    if status is not None:
+        _check(status, "status", (torch.int32,), rows=1)
+    if out is None:
+        out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+    _check(out, "out", _BF16, H, rows=T)
+    nbytes = int(lib.ep_moe_decode_workspace_bytes(T, K, inter))
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    _launch("ep_moe_decode", dev, lib.ep_moe_decode,
+            [topk_idx, topk_weights, w1, s1, w2, s2, w1_bias, w2_bias, b0, b1, status, out],
+            _ptr(x), _ptr(topk_idx), _ptr(topk_weights), T, K, E, H, inter,
+            _abi.EP_DTYPE_BF16 if s1 is None else _abi.EP_DTYPE_FP8_E4M3_UE8M0, _ptr(w1), _ptr(s1),
+            _ptr(w1_bias), _ptr(w2), _ptr(s2), _ptr(w2_bias), act, _ptr(b0), _ptr(b1), _ptr(ws),
+            nbytes, _ptr(status), _ptr(out), _stream(dev))
     return out

@@ -22,11 +22,18 @@ EP_DTYPE_FP8_E4M3 = 1
 EP_DTYPE_FP8_E4M3_POW2 = 2
 EP_DTYPE_FP8_E4M3_UE8M0 = 3
 
+EP_ACT_NONE = 0
+EP_ACT_SILU = 1
+EP_ACT_GELU = 2
+EP_ACT_SWIGLU = 3
+EP_ACT_GEGLU = 4
+
 EP_MAX_EXPERTS = 4096
 EP_MAX_PARTITIONS = 1024
 EP_MAX_TOPK = 256
 EP_MAX_SLOT_PARTITIONS = 64
 EP_MAX_HIDDEN = 1 << 20
+EP_MAX_DECODE_PAIRS = 1024
 
 # Every symbol include/ep.h declares.
 EXPORTS = ("ep_get_layout_workspace_bytes", "ep_worst_case_recv_rows", "ep_get_layout",
@@ -34,7 +41,8 @@ EXPORTS = ("ep_get_layout_workspace_bytes", "ep_worst_case_recv_rows", "ep_get_l
            "ep_dispatch", "ep_dispatch_with_layout", "ep_combine", "ep_dispatch_partitioned", "ep_combine_partitioned",
            "ep_combine_reduced", "ep_cast_fp8", "ep_logfmt_row_bytes", "ep_logfmt_encode",
            "ep_logfmt_decode", "ep_combine_logfmt", "ep_probe_dispatch_stores",
-           "ep_status_string")
+           "ep_expert_linear", "ep_expert_wgrad", "ep_expert_activation_backward",
+           "ep_moe_decode_workspace_bytes", "ep_moe_decode", "ep_status_string")
 
 
 class LayoutParams(ctypes.Structure):
@@ -117,6 +125,22 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.ep_probe_dispatch_stores.argtypes = [i32, ctypes.c_uint32, P(LayoutParams), P(LayoutPtrs),
                                              vp, i64, vp]
     lib.ep_probe_dispatch_stores.restype = ctypes.c_int
+    lib.ep_expert_linear.argtypes = [vp, ctypes.c_int, vp, vp, vp, i32, i32, ctypes.c_int, vp,
+                                     ctypes.c_int, vp, P(LayoutParams), P(LayoutPtrs), i64, vp,
+                                     vp, vp, vp]
+    lib.ep_expert_linear.restype = ctypes.c_int
+    lib.ep_expert_wgrad.argtypes = [vp, vp, ctypes.c_int, vp, i32, i32, P(LayoutParams),
+                                    P(LayoutPtrs), i64, vp, vp, vp, ctypes.c_int, vp, vp]
+    lib.ep_expert_wgrad.restype = ctypes.c_int
+    lib.ep_expert_activation_backward.argtypes = [vp, vp, vp, i32, ctypes.c_int, vp,
+                                                  P(LayoutParams), P(LayoutPtrs), i64, vp, vp, vp,
+                                                  vp]
+    lib.ep_expert_activation_backward.restype = ctypes.c_int
+    lib.ep_moe_decode_workspace_bytes.argtypes = [i32, i32, i32]
+    lib.ep_moe_decode_workspace_bytes.restype = sz
+    lib.ep_moe_decode.argtypes = [vp, vp, vp, i32, i32, i32, i32, i32, ctypes.c_int, vp, vp, vp, vp,
+                                  vp, vp, ctypes.c_int, vp, vp, vp, sz, vp, vp, vp]
+    lib.ep_moe_decode.restype = ctypes.c_int
     lib.ep_status_string.argtypes = [ctypes.c_int]
     lib.ep_status_string.restype = ctypes.c_char_p
     _lib = lib

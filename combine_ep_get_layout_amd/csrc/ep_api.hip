@@ -8,6 +8,7 @@
 #include <atomic>
 
 #include "../../include/ep.h"
+#include "ep_expert.h"
 #include "ep_internal.h"
 
 namespace {
@@ -517,6 +518,202 @@ int ep_combine_logfmt(const void *payload, int32_t hidden, int64_t num_y_rows,
     c.K = p->num_topk;
     c.hidden = hidden;
     return to_status(ep::launch_combine_logfmt(c, (hipStream_t)stream));
+}
+
+static bool aligned8(const void *p) { return ((uintptr_t)p & 7u) == 0; }
+
+static bool is_act(int act) { return act >= EP_ACT_NONE && act <= EP_ACT_GEGLU; }
+
+// Host checks the segmented expert operators share; fills the segments.
+static int segment_checks(const ep_layout_params *p, const ep_layout *layout, int64_t num_rows,
+                          ep::SegmentRows *seg) {
+    const int rc = check_params(p);
+    if (rc != EP_OK) return rc;
+    if (p->partition_major) return EP_ERR_INVALID_ARG;
+    if (!layout || !layout->num_tokens_per_expert || !layout->expert_offset || !layout->status)
+        return EP_ERR_INVALID_ARG;
+    if (num_rows < 0 || num_rows >= ((int64_t)1 << 31)) return EP_ERR_INVALID_ARG;
+    seg->counts = layout->num_tokens_per_expert;
+    seg->offsets = layout->expert_offset;
+    seg->status = layout->status;
+    seg->E = p->num_experts;
+    seg->num_rows = num_rows;
+    seg->pairs = (int64_t)p->num_tokens * p->num_topk;
+    return EP_OK;
+}
+
+int ep_expert_linear(const void *x, int x_dtype, const uint8_t *x_scales, const void *w,
+                     const uint8_t *w_scales, int32_t n, int32_t k, int transposed,
+                     const void *bias, int act, const void *residual,
+                     const ep_layout_params *p, const ep_layout *layout, int64_t num_rows,
+                     void *out, uint8_t *ckpt, uint8_t *ckpt_scales, void *stream) {
+    ep::LinearArgs a = {};
+    const int rc = segment_checks(p, layout, num_rows, &a.seg);
+    if (rc != EP_OK) return rc;
+    if (!is_act(act) || (transposed != 0 && transposed != 1)) return EP_ERR_INVALID_ARG;
+    if (x_dtype != EP_DTYPE_BF16 && x_dtype != EP_DTYPE_FP8_E4M3_UE8M0) return EP_ERR_INVALID_ARG;
+    const bool fp8 = x_dtype != EP_DTYPE_BF16;
+    if (n < 8 || k < 8 || n % (ep::act_gated(act) ? 16 : 8) != 0) return EP_ERR_INVALID_ARG;
+    if (k % (fp8 ? ep::kFp8Group : 8) != 0) return EP_ERR_INVALID_ARG;
+    if ((ckpt == nullptr) != (ckpt_scales == nullptr)) return EP_ERR_INVALID_ARG;
+    if (ckpt && n % (ep::act_gated(act) ? 64 : 32) != 0) return EP_ERR_INVALID_ARG;
+    if ((fp8 && transposed) || n > EP_MAX_HIDDEN || k > EP_MAX_HIDDEN) return EP_ERR_UNSUPPORTED;
+    if ((int64_t)n * k * (fp8 ? 1 : 2) >= ((int64_t)1 << 31)) return EP_ERR_UNSUPPORTED;
+    if (a.seg.pairs == 0 || num_rows == 0) return EP_OK;
+    if (!x || !aligned16(x) || !w || !aligned16(w) || !out || !aligned8(out))
+        return EP_ERR_INVALID_ARG;
+    if (fp8 && (!x_scales || !w_scales)) return EP_ERR_INVALID_ARG;
+    if (!aligned8(bias) || !aligned8(residual) || !aligned4(ckpt)) return EP_ERR_INVALID_ARG;
+    a.x = x;
+    a.x_scales = x_scales;
+    a.w = w;
+    a.w_scales = w_scales;
+    a.bias = bias;
+    a.residual = residual;
+    a.out = out;
+    a.ckpt = ckpt;
+    a.ckpt_scales = ckpt_scales;
+    a.n = n;
+    a.k = k;
+    a.act = act;
+    a.fp8 = fp8;
+    a.transposed = transposed == 1;
+    return to_status(ep::launch_expert_linear(a, (hipStream_t)stream));
+}
+
+int ep_expert_wgrad(const void *dy, const void *x, int x_dtype, const uint8_t *x_scales,
+                    int32_t n, int32_t k, const ep_layout_params *p, const ep_layout *layout,
+                    int64_t num_rows, const void *dw_in, const float *db_in, void *dw, int dw_bf16,
+                    float *db, void *stream) {
+    ep::WgradArgs a = {};
+    const int rc = segment_checks(p, layout, num_rows, &a.seg);
+    if (rc != EP_OK) return rc;
+    if (x_dtype != EP_DTYPE_BF16 && x_dtype != EP_DTYPE_FP8_E4M3_UE8M0) return EP_ERR_INVALID_ARG;
+    const bool fp8 = x_dtype != EP_DTYPE_BF16;
+    if (n < 8 || k < 8 || n % 8 != 0 || k % (fp8 ? ep::kFp8Group : 8) != 0)
+        return EP_ERR_INVALID_ARG;
+    if ((dw_bf16 != 0 && dw_bf16 != 1) || (db_in && !db)) return EP_ERR_INVALID_ARG;
+    if (n > EP_MAX_HIDDEN || k > EP_MAX_HIDDEN) return EP_ERR_UNSUPPORTED;
+    if (!dw || !aligned16(dw) || !aligned16(dw_in) || !aligned4(db) || !aligned4(db_in))
+        return EP_ERR_INVALID_ARG;
+    if (num_rows > 0 && a.seg.pairs > 0) {
+        if (!dy || !aligned16(dy) || !x || !aligned16(x)) return EP_ERR_INVALID_ARG;
+        if (fp8 && !x_scales) return EP_ERR_INVALID_ARG;
+    }
+    a.dy = dy;
+    a.x = x;
+    a.x_scales = x_scales;
+    a.dw_in = dw_in;
+    a.db_in = db_in;
+    a.dw = dw;
+    a.db = db;
+    a.n = n;
+    a.k = k;
+    a.fp8 = fp8;
+    a.bf16_out = dw_bf16 == 1;
+    return to_status(ep::launch_expert_wgrad(a, (hipStream_t)stream));
+}
+
+int ep_expert_activation_backward(const void *dh, const void *pre, const uint8_t *pre_scales,
+                                  int32_t n, int act, const float *row_weights,
+                                  const ep_layout_params *p, const ep_layout *layout,
+                                  int64_t num_rows, void *dpre, void *h_out, float *dweights,
+                                  void *stream) {
+    const int rc = check_params(p);
+    if (rc != EP_OK) return rc;
+    if (p->partition_major || !is_act(act)) return EP_ERR_INVALID_ARG;
+    if (!layout || !layout->expert_offset || !layout->status) return EP_ERR_INVALID_ARG;
+    if (num_rows < 0 || num_rows >= ((int64_t)1 << 31)) return EP_ERR_INVALID_ARG;
+    const bool gated = ep::act_gated(act);
+    const int unit = (pre_scales ? ep::kCheckpointGroup : 8) * (gated ? 2 : 1);
+    if (n < unit || n % unit != 0) return EP_ERR_INVALID_ARG;
+    if (n > EP_MAX_HIDDEN) return EP_ERR_UNSUPPORTED;
+    // rows the layout has no entry for hold no pair
+    const int64_t rows = num_rows < p->max_recv_rows ? num_rows : p->max_recv_rows;
+    if (rows == 0 || p->num_tokens == 0) return EP_OK;
+    if (!layout->src_of_slot || !dh || !aligned16(dh) || !pre || !dpre || !aligned16(dpre) ||
+        !aligned16(h_out) || !aligned4(row_weights) || !aligned4(dweights))
+        return EP_ERR_INVALID_ARG;
+    if (pre_scales ? !aligned8(pre) : !aligned16(pre)) return EP_ERR_INVALID_ARG;
+    ep::ActBackwardArgs a = {};
+    a.src_of_slot = layout->src_of_slot;
+    a.total_rows = layout->expert_offset + p->num_experts;
+    a.status = layout->status;
+    a.num_rows = rows;
+    a.dh = dh;
+    a.pre = pre;
+    a.pre_scales = pre_scales;
+    a.row_weights = row_weights;
+    a.dpre = dpre;
+    a.h = h_out;
+    a.dweights = dweights;
+    a.n = n;
+    a.m = gated ? n / 2 : n;
+    a.kind = ep::act_kind(act);
+    a.gated = gated;
+    return to_status(ep::launch_act_backward(a, (hipStream_t)stream));
+}
+
+size_t ep_moe_decode_workspace_bytes(int32_t num_tokens, int32_t num_topk, int32_t inter) {
+    if (num_tokens < 0 || num_topk < 1 || inter < 1 || inter > EP_MAX_HIDDEN) return 0;
+    const int64_t pairs = (int64_t)num_tokens * num_topk;
+    if (pairs > EP_MAX_DECODE_PAIRS) return 0;
+    return ((size_t)pairs * inter * 2 + 255) / 256 * 256 + 256;   // h, never empty
+}
+
+int ep_moe_decode(const void *x, const int64_t *topk_idx, const float *topk_weights,
+                  int32_t num_tokens, int32_t num_topk, int32_t num_experts, int32_t hidden,
+                  int32_t inter, int w_dtype, const void *w1, const uint8_t *w1_scales,
+                  const void *b1, const void *w2, const uint8_t *w2_scales, const void *b2,
+                  int act, const void *res0, const void *res1, void *workspace,
+                  size_t workspace_bytes, int32_t *status, void *out, void *stream) {
+    if (num_tokens < 0 || num_topk < 1 || num_experts < 1 || hidden < 8 || inter < 8 ||
+        !is_act(act))
+        return EP_ERR_INVALID_ARG;
+    if (w_dtype != EP_DTYPE_BF16 && w_dtype != EP_DTYPE_FP8_E4M3_UE8M0) return EP_ERR_INVALID_ARG;
+    const bool fp8 = w_dtype != EP_DTYPE_BF16;
+    const int unit = fp8 ? ep::kFp8Group : 8;
+    if (hidden % unit != 0 || inter % unit != 0) return EP_ERR_INVALID_ARG;
+    const int64_t pairs = (int64_t)num_tokens * num_topk;
+    if (pairs > EP_MAX_DECODE_PAIRS || num_experts > EP_MAX_EXPERTS || hidden > EP_MAX_HIDDEN ||
+        inter > EP_MAX_HIDDEN)
+        return EP_ERR_UNSUPPORTED;
+    if (num_tokens == 0) return EP_OK;
+    if (!x || !aligned16(x) || !topk_idx || !w1 || !aligned16(w1) || !w2 || !aligned16(w2) ||
+        !out || !aligned16(out))
+        return EP_ERR_INVALID_ARG;
+    if (((uintptr_t)topk_idx & 7u) != 0 || !aligned4(topk_weights) || !aligned4(status))
+        return EP_ERR_INVALID_ARG;
+    if (fp8 && (!w1_scales || !w2_scales)) return EP_ERR_INVALID_ARG;
+    if (!aligned16(res0) || !aligned16(res1)) return EP_ERR_INVALID_ARG;
+    if ((((uintptr_t)b1 | (uintptr_t)b2) & 1u) != 0) return EP_ERR_INVALID_ARG;
+    if (!workspace || !aligned16(workspace) ||
+        workspace_bytes < ep_moe_decode_workspace_bytes(num_tokens, num_topk, inter))
+        return EP_ERR_WORKSPACE;
+    ep::MoeDecodeArgs a = {};
+    a.x = x;
+    a.topk_idx = topk_idx;
+    a.topk_weights = topk_weights;
+    a.w1 = w1;
+    a.w2 = w2;
+    a.w1_scales = w1_scales;
+    a.w2_scales = w2_scales;
+    a.bias1 = b1;
+    a.bias2 = b2;
+    a.res0 = res0;
+    a.res1 = res1;
+    a.h = workspace;
+    a.out = out;
+    a.status = status;
+    a.T = num_tokens;
+    a.K = num_topk;
+    a.E = num_experts;
+    a.H = hidden;
+    a.I = inter;
+    a.kind = ep::act_kind(act);
+    a.gated = ep::act_gated(act);
+    a.fp8 = fp8;
+    return to_status(ep::launch_moe_decode(a, (hipStream_t)stream));
 }
 
 const char *ep_status_string(int code) {

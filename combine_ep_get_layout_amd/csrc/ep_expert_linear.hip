@@ -1,0 +1,360 @@
+// Grouped matrix product over the receive segments with its epilogue:
+// out[r] = act(x[r] W[e]^T + b[e]) + residual[r] for the rows r of segment e.
+//
+// A workgroup computes one tile of BM rows by 256 columns (gated activations:
+// 128 gate and the matching 128 up columns, so that the activation needs no
+// second pass).  Both operands pass through LDS in K steps of 128 bytes per
+// row (64 bf16 or 128 fp8 channels), copied there without registers, in a
+// ring of NS stages with one barrier per step.
+//
+// The weights are the matrix instruction's first operand, so a lane's four
+// accumulators are four consecutive columns of one row: bias, residual and
+// output move in 8-byte pieces and the checkpoint's codes in dwords.
+//
+// LDS rows are 8 chunks of 16 bytes, chunk c of row r in slot c ^ (r/2 & 7):
+// the 16 rows x 16 bytes a quarter wave reads lie in 16 different slots of the
+// 256-byte bank line.  Weights that lie [k, n] (transposed) are staged as 64
+// rows of 256 columns, 32-byte granule g of row k in place g ^ (k & 3 | (k >>
+// 3 & 1) << 2), and read by the transposing LDS read: lane l of a 16-lane
+// group names row l/4 and column 4 (l % 4) and receives column l of four rows.
+#include "ep_expert_device.h"
+
+namespace ep {
+
+namespace {
+
+constexpr int kBN = 256;
+
+struct LinearK {
+    SegmentRows seg;
+    const uint8_t *x;
+    const uint8_t *x_scales;
+    const uint8_t *w;
+    const uint8_t *w_scales;
+    const uint16_t *bias;
+    const uint16_t *residual;
+    uint16_t *out;
+    uint8_t *ckpt;
+    uint8_t *ckpt_scales;
+    int n, k, m;          // weight rows, contraction, output columns
+    int kind;             // activation function
+    int col_tiles;
+};
+
+// Four consecutive scale bytes of a row from step s on, as far as the row has them.
+__device__ __forceinline__ int scales4(const uint8_t *row, int s, int groups) {
+    int v = 0;
+    if (s + 4 <= groups) {
+        __builtin_memcpy(&v, row + s, 4);
+    } else {
+        for (int i = 0; s + i < groups; ++i) v |= (int)row[s + i] << (8 * i);
+    }
+    return v;
+}
+
+template <int SB>
+__device__ __forceinline__ ep_f32x4 mfma_fp8(ep_i32x8 a, ep_i32x8 b, ep_f32x4 c, int sa, int sb) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, SB, sa, SB, sb);
+}
+
+// One 32-channel group of pre-activations (two tiles of four accumulators, the
+// other 24 in the lanes 16, 32 and 48 away) to e4m3 codes under a power of two:
+// the format of ep_cast_fp8 with UE8M0 scales, taken from the fp32 sums.
+__device__ __forceinline__ void checkpoint_group(const float *z0, const float *z1, bool valid,
+                                                 int q, uint8_t *codes, uint8_t *scale) {
+    float m = 0.0f;
+    for (int i = 0; i < 4; ++i) m = fmaxf(m, fmaxf(fabsf(z0[i]), fabsf(z1[i])));
+    m = fmaxf(m, __shfl_xor(m, 16));
+    m = fmaxf(m, __shfl_xor(m, 32));
+    m = fminf(m, 3.0e38f);
+    const uint32_t e = ue8m0_of(pow2_ceil(scale_of(m)));
+    const float inv = __uint_as_float((254u - e) << 23);
+    const uint32_t c0 = pack4_e4m3(z0[0] * inv, z0[1] * inv, z0[2] * inv, z0[3] * inv);
+    const uint32_t c1 = pack4_e4m3(z1[0] * inv, z1[1] * inv, z1[2] * inv, z1[3] * inv);
+    if (valid) {
+        *(uint32_t *)(codes + 4 * q) = c0;
+        *(uint32_t *)(codes + 16 + 4 * q) = c1;
+        if (q == 0) *scale = (uint8_t)e;
+    }
+}
+
+template <int BM, int WM, int NS, bool FP8, bool WT, bool GATED>
+__global__ __launch_bounds__(256 * WM, 2) void expert_linear_kernel(LinearK a) {
+    constexpr int kWaves = 4 * WM;
+    constexpr int MT = BM / WM / 16;               // 16-row tiles of a wave
+    constexpr int kWStage = kBN * 128, kXStage = BM * 128;
+    constexpr int kStage = kWStage + kXStage;
+    constexpr int WL = kWStage / 1024 / kWaves;    // copies of a wave per step
+    constexpr int XL = kXStage / 1024 / kWaves;
+    constexpr int ES = FP8 ? 1 : 2;
+    constexpr int BK = 128 / ES;
+    __shared__ __align__(1024) uint8_t lds[NS * kStage];
+    __shared__ int red[16];
+
+    TileAt at;
+    if (!find_tile<64 * kWaves>(a.seg, BM, a.col_tiles, blockIdx.x, red, &at)) return;
+
+    const int lane = threadIdx.x & 63, wave = wave_uniform(threadIdx.x >> 6);
+    const int l16 = lane & 15, q = lane >> 4;
+    const int wn = wave & 3, wm = wave >> 2;
+    const int K = a.k, N = a.n;
+    const int half = N >> 1;
+    const int row0 = at.mt * BM;                       // in the segment
+    const int rows = min(BM, at.rows - row0);
+
+    // copies: source offsets of this lane
+    const uint32_t ld_bytes = (uint32_t)K * ES;
+    const ep_i32x4 xb = buffer_of(a.x + ((int64_t)at.row0 + row0) * ld_bytes,
+                                  (uint32_t)rows * ld_bytes);
+    const uint32_t w_bytes = (uint32_t)N * ld_bytes;
+    const ep_i32x4 wb = buffer_of(a.w + (int64_t)at.e * w_bytes, w_bytes);
+    const int chunk = (lane & 7) ^ ((wave * 4 + (lane >> 4)) & 7);
+    uint32_t xoff[XL], woff[WL];
+    int wk[WT ? WL : 1];                               // transposed: the k row of each copy
+    for (int j = 0; j < XL; ++j) xoff[j] = (uint32_t)((j * kWaves + wave) * 8 + (lane >> 3)) * ld_bytes + chunk * 16;
+    // column of the weights at place r (0..255) of the tile: gated tiles hold,
+    // per wave, 32 gate columns and the 32 up columns that go with them
+    auto column = [&](int r) {
+        if (!GATED) return at.nt * kBN + r;
+        const int c = at.nt * (kBN / 2) + (r >> 6) * 32 + (r & 31);
+        return (r & 32) ? half + c : c;
+    };
+    for (int j = 0; j < WL; ++j) {
+        if (!WT) {
+            const int r = (j * kWaves + wave) * 8 + (lane >> 3);
+            const int c = column(r);
+            woff[j] = (uint32_t)c * ld_bytes + chunk * 16;
+            // a gated tile's columns past the halves lie in the other half or
+            // behind the matrix: their products are not stored
+            if (c >= N) woff[j] = kOutOfRange;
+        } else {
+            const int kr = (j * kWaves + wave) * 2 + (lane >> 5);
+            const int c16 = lane & 31;
+            const int f = (kr & 3) | ((kr >> 3 & 1) << 2);
+            const int c = column(((c16 >> 1) ^ f) * 16 + (c16 & 1) * 8);
+            wk[j] = kr;
+            woff[j] = (uint32_t)kr * (uint32_t)N * 2 + (uint32_t)c * 2;
+            if (c >= N) woff[j] = kOutOfRange;
+        }
+    }
+    const uint32_t lds0 = lds_offset(lds);
+    const int steps = (K + BK - 1) / BK;
+    auto copy = [&](int s, int stage) {
+        const uint32_t base = lds0 + stage * kStage + wave * 1024;
+        const bool tail = !FP8 && (s + 1) * BK > K;
+        if (tail) {
+            // channels at or past K become zeros in both operands
+            const uint32_t out = s * BK + chunk * 8 >= K ? kOutOfRange : 0;
+            for (int j = 0; j < WL; ++j) {
+                const uint32_t wo = WT ? (s * BK + wk[WT ? j : 0] >= K ? kOutOfRange : 0) : out;
+                dma16(wb, base + j * kWaves * 1024, woff[j] | wo,
+                      WT ? (uint32_t)s * BK * (uint32_t)N * 2 : s * 128);
+            }
+            for (int j = 0; j < XL; ++j)
+                dma16(xb, base + kWStage + j * kWaves * 1024, xoff[j] | out, s * 128);
+        } else {
+            for (int j = 0; j < WL; ++j)
+                dma16(wb, base + j * kWaves * 1024, woff[j],
+                      WT ? (uint32_t)s * BK * (uint32_t)N * 2 : s * 128);
+            for (int j = 0; j < XL; ++j)
+                dma16(xb, base + kWStage + j * kWaves * 1024, xoff[j], s * 128);
+        }
+    };
+
+    ep_f32x4 acc[4][MT];
+    for (int t = 0; t < 4; ++t)
+        for (int i = 0; i < MT; ++i) acc[t][i] = ep_f32x4{0, 0, 0, 0};
+
+    // fp8: this lane's scale bytes, four steps in a dword
+    const uint8_t *xs_row[FP8 ? MT : 1];
+    const uint8_t *ws_row[FP8 ? 4 : 1];
+    int xs[FP8 ? MT : 1], ws[FP8 ? 4 : 1];
+    if (FP8) {
+        const int groups = K / kFp8Group;
+        for (int i = 0; i < MT; ++i) {
+            const int r = min(wm * MT * 16 + i * 16 + l16, rows - 1);
+            xs_row[i] = a.x_scales + ((int64_t)at.row0 + row0 + r) * groups;
+        }
+        for (int t = 0; t < 4; ++t) {
+            const int c = min(column(wn * 64 + t * 16 + l16), N - 1);
+            ws_row[t] = a.w_scales + ((int64_t)at.e * N + c) * groups;
+        }
+    }
+
+    const int lrow = l16 * 128;
+    const int slot = (q ^ (l16 >> 1)) * 16;
+    auto compute = [&](int stage, auto sb) {
+        const uint8_t *wl = lds + stage * kStage;
+        const uint8_t *xl = wl + kWStage + wm * MT * 16 * 128 + lrow;
+        ep_u32x4 xf[2][MT], wf[2][4];
+        for (int kk = 0; kk < 2; ++kk) {
+            for (int t = 0; t < 4; ++t) {
+                if (!WT) {
+                    wf[kk][t] = *(const ep_u32x4 *)(wl + wn * 64 * 128 + lrow + t * 2048 + (slot ^ (kk * 64)));
+                } else {
+                    const int kr = kk * 32 + q * 8 + (l16 >> 2);
+                    const int f = (kr & 3) | ((kr >> 3 & 1) << 2);
+                    const uint8_t *p = wl + kr * 512 + (((wn * 4 + t) ^ f) * 32) + (l16 & 3) * 8;
+                    const ep_i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                        (__attribute__((address_space(3))) ep_i16x4 *)p);
+                    const ep_i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                        (__attribute__((address_space(3))) ep_i16x4 *)(p + 4 * 512));
+                    wf[kk][t].xy = __builtin_bit_cast(ep_u32x2, lo);
+                    wf[kk][t].zw = __builtin_bit_cast(ep_u32x2, hi);
+                }
+            }
+            for (int i = 0; i < MT; ++i) xf[kk][i] = *(const ep_u32x4 *)(xl + i * 2048 + (slot ^ (kk * 64)));
+            if (!FP8) {
+                for (int i = 0; i < MT; ++i)
+                    for (int t = 0; t < 4; ++t)
+                        acc[t][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                            __builtin_bit_cast(ep_bf16x8, wf[kk][t]),
+                            __builtin_bit_cast(ep_bf16x8, xf[kk][i]), acc[t][i], 0, 0, 0);
+            }
+        }
+        if (FP8) {
+            // a lane's 32 channels are chunks q and q + 4 of the row, the same
+            // in both operands; one scale covers all 128
+            for (int i = 0; i < MT; ++i)
+                for (int t = 0; t < 4; ++t) {
+                    ep_i32x8 wv, xv;
+                    wv.lo = __builtin_bit_cast(ep_i32x4, wf[0][t]);
+                    wv.hi = __builtin_bit_cast(ep_i32x4, wf[1][t]);
+                    xv.lo = __builtin_bit_cast(ep_i32x4, xf[0][i]);
+                    xv.hi = __builtin_bit_cast(ep_i32x4, xf[1][i]);
+                    acc[t][i] = mfma_fp8<decltype(sb)::value>(wv, xv, acc[t][i], ws[FP8 ? t : 0], xs[FP8 ? i : 0]);
+                }
+        }
+    };
+
+    for (int s = 0; s < NS - 1; ++s)
+        if (s < steps) copy(s, s);
+    int stage = 0;
+    auto step = [&](int s, auto sb) {
+        // stage s has landed once at most the copies of the steps after it
+        // are in flight; near the end there are none, and all are waited for
+        if (s + NS - 2 < steps) dma_wait<(NS - 2) * (WL + XL)>();
+        else dma_wait<0>();
+        barrier_only();
+        const int next = stage == 0 ? NS - 1 : stage - 1;
+        if (s + NS - 1 < steps) copy(s + NS - 1, next);
+        compute(stage, sb);
+        stage = stage + 1 == NS ? 0 : stage + 1;
+    };
+    if (FP8) {
+        const int groups = K / kFp8Group;
+        for (int s = 0; s < steps; s += 4) {
+            for (int i = 0; i < MT; ++i) xs[FP8 ? i : 0] = scales4(xs_row[FP8 ? i : 0], s, groups);
+            for (int t = 0; t < 4; ++t) ws[FP8 ? t : 0] = scales4(ws_row[FP8 ? t : 0], s, groups);
+            step(s, std::integral_constant<int, 0>{});
+            if (s + 1 < steps) step(s + 1, std::integral_constant<int, 1>{});
+            if (s + 2 < steps) step(s + 2, std::integral_constant<int, 2>{});
+            if (s + 3 < steps) step(s + 3, std::integral_constant<int, 3>{});
+        }
+    } else {
+        for (int s = 0; s < steps; ++s) step(s, std::integral_constant<int, 0>{});
+    }
+
+    // epilogue
+    const int kind = a.kind;
+    float b[4][4];
+    bool in[4];
+    int col[4];
+    for (int t = 0; t < 4; ++t) {
+        col[t] = column(wn * 64 + t * 16) + 4 * q;
+        in[t] = GATED ? col[t & 1] < half : col[t] < N;
+        for (int i = 0; i < 4; ++i) b[t][i] = 0.0f;
+        if (a.bias && in[t]) {
+            const ep_u32x2 v = *(const ep_u32x2 *)(a.bias + (int64_t)at.e * N + col[t]);
+            b[t][0] = bf16_lo(v.x); b[t][1] = bf16_hi(v.x);
+            b[t][2] = bf16_lo(v.y); b[t][3] = bf16_hi(v.y);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+        const int r = wm * MT * 16 + i * 16 + l16;
+        const bool live = r < rows;
+        const int64_t row = (int64_t)at.row0 + row0 + r;
+        float z[4][4];
+        for (int t = 0; t < 4; ++t)
+            for (int j = 0; j < 4; ++j) z[t][j] = acc[t][i][j] + b[t][j];
+        if (a.ckpt) {
+            for (int g = 0; g < 2; ++g) {
+                const int c = col[2 * g] - 4 * q;      // the group's first channel
+                checkpoint_group(z[2 * g], z[2 * g + 1], live && in[2 * g], q,
+                                 a.ckpt + row * N + c, a.ckpt_scales + row * (N >> 5) + (c >> 5));
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < (GATED ? 2 : 4); ++t) {
+            float y[4];
+            for (int j = 0; j < 4; ++j) {
+                y[j] = act_value(z[t][j], kind);
+                if (GATED) y[j] *= z[(t + 2) & 3][j];
+            }
+            if (!live || !in[t]) continue;
+            const int64_t o = row * a.m + col[t];
+            if (a.residual) {
+                const ep_u32x2 v = *(const ep_u32x2 *)(a.residual + o);
+                y[0] += bf16_lo(v.x); y[1] += bf16_hi(v.x);
+                y[2] += bf16_lo(v.y); y[3] += bf16_hi(v.y);
+            }
+            ep_u32x2 v;
+            v.x = pack_bf16(y[0], y[1]);
+            v.y = pack_bf16(y[2], y[3]);
+            *(ep_u32x2 *)(a.out + o) = v;
+        }
+    }
+}
+
+template <int BM, int WM, int NS>
+hipError_t launch_bm(const LinearArgs &a, const LinearK &k, bool gated, hipStream_t stream) {
+    // row tiles: each segment's last one may be partial
+    const int64_t most = a.seg.pairs < a.seg.num_rows ? a.seg.pairs : a.seg.num_rows;
+    const int64_t some = most < a.seg.E ? most : a.seg.E;
+    const int64_t tiles = (most / BM + some) * k.col_tiles;
+    const int64_t grid = (tiles + 7) / 8 * 8;
+    if (grid == 0) return hipSuccess;
+    if (grid > 0x7fffffff) return hipErrorInvalidConfiguration;
+    const dim3 g((unsigned)grid), t(256 * WM);
+    if (a.fp8) {
+        if (gated) expert_linear_kernel<BM, WM, NS, true, false, true><<<g, t, 0, stream>>>(k);
+        else expert_linear_kernel<BM, WM, NS, true, false, false><<<g, t, 0, stream>>>(k);
+    } else if (a.transposed) {
+        if (gated) expert_linear_kernel<BM, WM, NS, false, true, true><<<g, t, 0, stream>>>(k);
+        else expert_linear_kernel<BM, WM, NS, false, true, false><<<g, t, 0, stream>>>(k);
+    } else {
+        if (gated) expert_linear_kernel<BM, WM, NS, false, false, true><<<g, t, 0, stream>>>(k);
+        else expert_linear_kernel<BM, WM, NS, false, false, false><<<g, t, 0, stream>>>(k);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_expert_linear(const LinearArgs &a, hipStream_t stream) {
+    LinearK k = {};
+    k.seg = a.seg;
+    k.x = (const uint8_t *)a.x;
+    k.x_scales = a.x_scales;
+    k.w = (const uint8_t *)a.w;
+    k.w_scales = a.w_scales;
+    k.bias = (const uint16_t *)a.bias;
+    k.residual = (const uint16_t *)a.residual;
+    k.out = (uint16_t *)a.out;
+    k.ckpt = a.ckpt;
+    k.ckpt_scales = a.ckpt_scales;
+    k.n = a.n;
+    k.k = a.k;
+    const bool gated = act_gated(a.act);
+    k.m = gated ? a.n / 2 : a.n;
+    k.kind = act_kind(a.act);
+    const int per_tile = gated ? kBN / 2 : kBN;
+    k.col_tiles = (k.m + per_tile - 1) / per_tile;
+    const int64_t avg = a.seg.pairs / a.seg.E;
+    if (avg > 160) return launch_bm<256, 2, 2>(a, k, gated, stream);
+    if (avg > 40) return launch_bm<128, 2, 3>(a, k, gated, stream);
+    return launch_bm<32, 1, 2>(a, k, gated, stream);
+}
+
+}  // namespace ep

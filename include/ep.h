@@ -72,9 +72,15 @@ enum {
 enum { EP_DTYPE_BF16 = 0, EP_DTYPE_FP8_E4M3 = 1, EP_DTYPE_FP8_E4M3_POW2 = 2,
        EP_DTYPE_FP8_E4M3_UE8M0 = 3 };
 
+/* Activations of the expert operators: f(z), or for the gated ones f(g) * u
+ * where z = [g | u] are the halves of a row of pre-activations.  silu(z) =
+ * z / (1 + exp(-z)); gelu is its tanh form, z/2 (1 + tanh(sqrt(2/pi) (z +
+ * 0.044715 z^3))). */
+enum { EP_ACT_NONE = 0, EP_ACT_SILU = 1, EP_ACT_GELU = 2, EP_ACT_SWIGLU = 3, EP_ACT_GEGLU = 4 };
+
 /* Limits of the library. */
 enum { EP_MAX_EXPERTS = 4096, EP_MAX_PARTITIONS = 1024, EP_MAX_TOPK = 256,
-       EP_MAX_SLOT_PARTITIONS = 64, EP_MAX_HIDDEN = 1 << 20 };
+       EP_MAX_SLOT_PARTITIONS = 64, EP_MAX_HIDDEN = 1 << 20, EP_MAX_DECODE_PAIRS = 1024 };
 
 /* Shape of one layout ([API] 2.1 parameter table: num_experts,
  * expert_alignment, num_max_tokens_per_rank; 3.1 num_tokens_per_rank). */
@@ -415,6 +421,139 @@ int ep_combine_logfmt(const void *payload, int32_t hidden, int64_t num_y_rows,
                       const ep_layout_params *params, const ep_layout *layout,
                       const float *recv_topk_weights, float *combined_topk_weights, void *out,
                       void *stream);
+
+/* Expert operators: what the experts compute on the receive rows between a
+ * dispatch and its combine, and its gradients.  They work on an expert-major
+ * layout (partition_major = 0), over the rows that hold a pair: rows r of
+ * expert e, expert_offset[e] <= r < expert_offset[e] + count, count the
+ * smaller of num_tokens_per_expert[e] and the rows the segment has (fixed
+ * capacity).  Padding rows are neither read nor written, whatever they hold.
+ * Rows at or past num_rows, the rows the buffers have, are skipped and
+ * EP_DEV_RECV_OVERFLOW is set.  Of the layout only num_tokens_per_expert,
+ * expert_offset and status are used (ep_expert_activation_backward:
+ * src_of_slot, expert_offset and status).  Products are exact and summed in fp32;
+ * results do not depend on the other experts' rows, and two calls on the same
+ * inputs give the same bits. */
+
+/* ep_expert_linear - the experts' matrix product with its epilogue:
+ * z[r] = W[e] x[r] + bias[e];  out[r] = act(z[r]) + residual[r], rounded once
+ * to bf16.  With transposed = 1 and EP_ACT_NONE it is the product's data
+ * gradient: x = dz, w as the forward call had it.
+ *
+ *   x          device [num_rows, k]: bf16 (k % 8 == 0), or e4m3 codes
+ *              (x_dtype EP_DTYPE_FP8_E4M3_UE8M0, k % 128 == 0); 16-byte aligned.
+ *   x_scales   device uint8 [num_rows, k/128] for fp8 (UE8M0, one per 128
+ *              channels, as ep_dispatch and ep_cast_fp8 write them), else NULL.
+ *   w          device, x's type, 16-byte aligned: [E, n, k], or with
+ *              transposed = 1 (bf16 only) [E, k, n].
+ *   w_scales   device uint8 [E, n, k/128] for fp8 (ep_cast_fp8 of the weight
+ *              rows), else NULL.
+ *   n          columns of z: a multiple of 8; of 16 for a gated activation, of
+ *              32 (64 gated) with a checkpoint.
+ *   bias       device bf16 [E, n] or NULL, 8-byte aligned.
+ *   act        EP_ACT_*.
+ *   residual   device bf16 [num_rows, m] or NULL, 8-byte aligned; m = n, or
+ *              n/2 for a gated activation.
+ *   out        device bf16 [num_rows, m], 8-byte aligned.
+ *   ckpt, ckpt_scales  device uint8 [num_rows, n] (4-byte aligned) and
+ *              [num_rows, n/32], or both NULL: z kept in 8 bits for
+ *              ep_expert_activation_backward: e4m3 codes and UE8M0 scales per
+ *              32 channels, the format of ep_cast_fp8, taken from the fp32 z.
+ * Errors: EP_ERR_INVALID_ARG; EP_ERR_UNSUPPORTED (fp8 with transposed, k or n
+ * above EP_MAX_HIDDEN, an expert's weights of 2^31 bytes or more). */
+int ep_expert_linear(const void *x, int x_dtype, const uint8_t *x_scales, const void *w,
+                     const uint8_t *w_scales, int32_t n, int32_t k, int transposed,
+                     const void *bias, int act, const void *residual,
+                     const ep_layout_params *params, const ep_layout *layout, int64_t num_rows,
+                     void *out, uint8_t *ckpt, uint8_t *ckpt_scales, void *stream);
+
+/* ep_expert_wgrad - the product's weight and bias gradients:
+ * dw[e] = sum over the rows r of expert e of dy[r]^T x[r] (+ dw_in[e]),
+ * db[e] = sum of dy[r] (+ db_in[e]), summed in fp32 and rounded once.
+ *
+ *   dy         device bf16 [num_rows, n], n % 8 == 0; 16-byte aligned.
+ *   x, x_dtype, x_scales  the forward product's rows, [num_rows, k]: bf16
+ *              (k % 8 == 0), or e4m3 codes with UE8M0 scales per 128 channels
+ *              (k % 128 == 0), rows kept in 8 bits; 16-byte aligned.
+ *   dw_in, db_in  gradients to add to (micro-batches), or NULL; they may be
+ *              dw and db themselves.
+ *   dw         device [E, n, k], 16-byte aligned; an expert without
+ *              rows gets zeros (or dw_in).
+ *   dw_bf16    0: dw and dw_in are float; 1: bf16.
+ *   db         device float [E, n] or NULL.
+ * Errors: EP_ERR_INVALID_ARG (db_in without db among them);
+ * EP_ERR_UNSUPPORTED (k or n above EP_MAX_HIDDEN). */
+int ep_expert_wgrad(const void *dy, const void *x, int x_dtype, const uint8_t *x_scales,
+                    int32_t n, int32_t k, const ep_layout_params *params,
+                    const ep_layout *layout, int64_t num_rows, const void *dw_in,
+                    const float *db_in, void *dw, int dw_bf16, float *db, void *stream);
+
+/* ep_expert_activation_backward - the gradient through the experts'
+ * activation, from pre-activations z kept in 8 bits (or in bf16).  With h =
+ * act(z) and dh the gradient of the rows row_weights[r] * h[r] (the weights a
+ * combine multiplies by; 1 when NULL):
+ *   dpre = dL/dz;  h_out = row_weights * h (what the next product's weight
+ *   gradient multiplies);  dweights[r] = sum_i dh[r,i] h[r,i] (fp32).
+ * Where the combine's gradient rows are dispatched as they are (ep_dispatch of
+ * dL/dout) and taken through the down product's data gradient, these are the
+ * gradients of z and of the routing weights.
+ *
+ *   dh         device bf16 [num_rows, m], m = n (n/2 for a gated activation);
+ *              16-byte aligned.
+ *   pre, pre_scales  z: e4m3 codes [num_rows, n] (8-byte aligned) and UE8M0
+ *              scales [num_rows, n/32], the checkpoint of ep_expert_linear
+ *              (n % 32 == 0, 64 gated); or bf16 [num_rows, n] (16-byte aligned)
+ *              and NULL (n % 8 == 0, 16 gated).
+ *   row_weights  device float [num_rows] or NULL (ep_dispatch's
+ *              recv_topk_weights).
+ *   dpre       device bf16 [num_rows, n], 16-byte aligned.
+ *   h_out      device bf16 [num_rows, m], 16-byte aligned, or NULL.
+ *   dweights   device float [num_rows] or NULL.
+ * dpre and h_out are rounded once from fp32.  Errors: EP_ERR_INVALID_ARG;
+ * EP_ERR_UNSUPPORTED (n above EP_MAX_HIDDEN). */
+int ep_expert_activation_backward(const void *dh, const void *pre, const uint8_t *pre_scales,
+                                  int32_t n, int act, const float *row_weights,
+                                  const ep_layout_params *params, const ep_layout *layout,
+                                  int64_t num_rows, void *dpre, void *h_out, float *dweights,
+                                  void *stream);
+
+/* Bytes of device workspace ep_moe_decode needs (host call), or 0 for sizes
+ * it does not take. */
+size_t ep_moe_decode_workspace_bytes(int32_t num_tokens, int32_t num_topk, int32_t inter);
+
+/* ep_moe_decode - a whole mixture-of-experts layer for a few tokens, without
+ * a layout: out[t] = res0[t] + res1[t] + sum_k w[t,k] (W2[e] h + b2[e]), h =
+ * act(W1[e] x[t] + b1[e]), e = topk_idx[t,k].  What dispatch, two
+ * ep_expert_linear calls and ep_combine compute, in two kernels; h is rounded
+ * to bf16, the expert outputs stay in fp32 and are added in ascending k (fmaf)
+ * as ep_combine adds them.  A token's result does not depend on the others.
+ *
+ *   x            device bf16 [T, H], 16-byte aligned.
+ *   topk_idx     device int64 [T, K]; -1 = no expert (as is any id outside
+ *                [0, E), which also sets EP_DEV_BAD_EXPERT in status).  T*K <=
+ *                EP_MAX_DECODE_PAIRS.
+ *   topk_weights device float [T, K], or NULL for the unweighted sum.
+ *   w_dtype      EP_DTYPE_BF16 (H and I multiples of 8), or
+ *                EP_DTYPE_FP8_E4M3_UE8M0 (multiples of 128).
+ *   w1, w1_scales  [E, n1, H] (scales uint8 [E, n1, H/128]), n1 = I (2I gated,
+ *                gate rows first); 16-byte aligned.
+ *   w2, w2_scales  [E, H, I] (scales uint8 [E, H, I/128]); 16-byte aligned.
+ *   b1, b2       device bf16 [E, n1], [E, H] or NULL (2-byte aligned).
+ *   act          EP_ACT_*.
+ *   res0, res1   device bf16 [T, H] or NULL, 16-byte aligned (a residual, a
+ *                shared expert's output).
+ *   workspace    device, >= ep_moe_decode_workspace_bytes, 16-byte aligned;
+ *                scratch of this call.
+ *   status       device int32 [1] or NULL: EP_DEV_BAD_EXPERT is OR-ed in.
+ *   out          device bf16 [T, H], 16-byte aligned.
+ * Errors: EP_ERR_INVALID_ARG, EP_ERR_WORKSPACE, EP_ERR_UNSUPPORTED (more
+ * pairs, E above EP_MAX_EXPERTS, H or I above EP_MAX_HIDDEN). */
+int ep_moe_decode(const void *x, const int64_t *topk_idx, const float *topk_weights,
+                  int32_t num_tokens, int32_t num_topk, int32_t num_experts, int32_t hidden,
+                  int32_t inter, int w_dtype, const void *w1, const uint8_t *w1_scales,
+                  const void *b1, const void *w2, const uint8_t *w2_scales, const void *b2,
+                  int act, const void *res0, const void *res1, void *workspace,
+                  size_t workspace_bytes, int32_t *status, void *out, void *stream);
 
 /* ep_probe_dispatch_stores - a measurement aid, not a step of the method:
  * the stores of ep_dispatch for bf16 rows (the same row kernel, grid and
