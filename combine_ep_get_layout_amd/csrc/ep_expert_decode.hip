@@ -158,6 +158,8 @@ __global__ __launch_bounds__(256) void moe_decode_up_kernel(DecodeK k) {
                     acc_u = __builtin_amdgcn_mfma_f32_16x16x32_bf16(Weights<FP8>::operand(vu, su, j), b, acc_u, 0, 0, 0);
             }
         }
+        pin(acc_g);
+        pin(acc_u);
         for (int i = 0; i < 4; ++i) {
             part[wave][0][4 * q + i][l16] = acc_g[i];
             if (GATED) part[wave][GATED ? 1 : 0][4 * q + i][l16] = acc_u[i];
@@ -267,6 +269,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_decode_down_kernel(Decode
                     acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
                         Weights<FP8>::operand(v, sc, j), __builtin_bit_cast(ep_bf16x8, hv[j]), acc, 0, 0, 0);
             }
+            pin(acc);
             if (a.bias2) {
                 for (int i = 0; i < 4; ++i)
                     if (h0 + 4 * q + i < H)

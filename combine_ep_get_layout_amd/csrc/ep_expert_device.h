@@ -149,6 +149,11 @@ __device__ __forceinline__ uint32_t lds_offset(const void *p) {
     return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void *)p;
 }
 
+// Holds a matrix instruction's result at this point: the compiler may
+// otherwise move the instruction into a branch that only some lanes take, and
+// it needs all lanes' operands.
+__device__ __forceinline__ void pin(ep_f32x4 &v) { asm volatile("" : "+v"(v)); }
+
 // fp32 pairs to packed bf16, nearest even (the hardware conversion).
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     ep_bf16x2 v;

@@ -192,6 +192,11 @@ __global__ __launch_bounds__(512, 2) void expert_wgrad_kernel(WgradK a) {
 
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
+        for (int t4 = 0; t4 < 4; ++t4) pin(acc[t4][i]);
+        if (BIAS) pin(sum[BIAS ? i : 0]);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
         const int n = n0 + wn * 128 + i * 16 + l16;
         if (n >= N) continue;
         const int64_t row = ((int64_t)e * N + n) * K;
