@@ -175,7 +175,7 @@ __global__ __launch_bounds__(256) void moe_decode_up_kernel(DecodeK k) {
                     if (a.bias1)
                         z[s] += __uint_as_float((uint32_t)((const uint16_t *)a.bias1)[e * n1 + s * I + col0 + c] << 16);
                 }
-                float y = act_value(z[0], a.kind);
+                float y = a.kind == 1 ? act_value<1>(z[0]) : a.kind == 2 ? act_value<2>(z[0]) : z[0];
                 if (GATED) y *= z[1];
                 // bf16: the type a dispatch would carry and the matrix
                 // instruction takes; the one rounding between x and out

@@ -48,7 +48,7 @@ __device__ __forceinline__ int segment_rows(const SegmentRows &s, int e, int *ro
 // its L2.  `red` is LDS of at least 16 ints; the whole workgroup calls this.
 // Returns false for a workgroup without a tile.
 template <int THREADS>
-__device__ bool find_tile(const SegmentRows &s, int tile_rows, int col_tiles, int block,
+__device__ __forceinline__ bool find_tile(const SegmentRows &s, int tile_rows, int col_tiles, int block,
                           int *red, TileAt *at) {
     constexpr int kWaves = THREADS / 64;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -70,18 +70,18 @@ __device__ bool find_tile(const SegmentRows &s, int tile_rows, int col_tiles, in
         base += w < wave ? v : 0;
         total += v;
     }
-    const int64_t tiles = (int64_t)total * col_tiles;
-    const int64_t run = (tiles + 7) >> 3;
-    const int64_t t = (int64_t)(block & 7) * run + (block >> 3);
-    if ((block >> 3) >= run || t >= tiles) return false;
-    const int u = (int)(t / col_tiles);
+    const uint32_t tiles = (uint32_t)total * (uint32_t)col_tiles;   // at most the grid
+    const uint32_t run = (tiles + 7) >> 3;
+    const uint32_t t = (uint32_t)(block & 7) * run + (uint32_t)(block >> 3);
+    if ((uint32_t)(block >> 3) >= run || t >= tiles) return false;
+    const int u = (int)(t / (uint32_t)col_tiles);
     int first = base + incl - local;
     if (u >= first && u < first + local) {
         for (int e = beg; e < end; ++e) {
             const int rows = segment_rows(s, e, &row0);
             const int n = (rows + tile_rows - 1) / tile_rows;
             if (u < first + n) {
-                const int lt = (int)(t - (int64_t)first * col_tiles);
+                const int lt = (int)(t - (uint32_t)first * (uint32_t)col_tiles);
                 const int g = lt / (8 * col_tiles);
                 const int gm = min(8, n - g * 8);
                 const int rem = lt - g * 8 * col_tiles;
@@ -121,16 +121,53 @@ constexpr uint32_t kOutOfRange = 0x80000000u;   // no buffer here is longer
 // out of the buffer's range write zeros.  Asynchronous: the data is in LDS
 // after a wait on the vector memory count (dma_wait).  There is no output
 // register, so nothing the compiler could reuse too early; it does not know of
-// the copy, and the waits below carry the order.
+// the copy, and the waits below carry the order.  (m0, the LDS address, is
+// reserved: the compiler keeps nothing in it.)
 __device__ __forceinline__ void dma16(const ep_i32x4 &rsrc, uint32_t lds, uint32_t voff,
                                       uint32_t soff) {
+    ep_i32x4 r;
+    for (int i = 0; i < 4; ++i) r[i] = wave_uniform(rsrc[i]);
     asm volatile(
         "s_mov_b32 m0, %0\n\t"
         "s_nop 0\n\t"
         "buffer_load_dwordx4 %1, %2, %3 offen lds"
         :
-        : "s"(lds), "v"(voff), "s"(rsrc), "s"(soff)
-        : "m0");
+        : "s"(wave_uniform((int)lds)), "v"(voff), "s"(r), "s"(wave_uniform((int)soff)));
+}
+
+// The same for four copies to consecutive kilobytes of LDS, one call each with
+// J = 0, 1, 2, 3 in this order: J = 0 sets the LDS address, and the instruction
+// offset J * 1024 moves both addresses, so the caller's voff is kDmaBias - J *
+// 1024 more than the source's and its buffer starts kDmaBias early (biased_buffer).
+constexpr uint32_t kDmaBias = 3072;
+__device__ __forceinline__ ep_i32x4 biased_buffer(const void *p, uint32_t bytes) {
+    return buffer_of((const uint8_t *)p - kDmaBias, bytes + kDmaBias);
+}
+
+// `bytes` and `soff` when the copies of step s exist (s < steps), else an empty
+// buffer: scalar code, so that they stay scalar registers.  (The offset is
+// cleared too: a buffer's range check subtracts it from the size.)
+__device__ __forceinline__ void range_of(int s, int steps, uint32_t bytes, uint32_t soff,
+                                         ep_i32x4 &buffer, uint32_t *out) {
+    uint32_t z, o;
+    asm volatile("s_cmp_lt_i32 %2, %3\n\ts_cselect_b32 %0, %4, 0\n\ts_cselect_b32 %1, %5, 0"
+                 : "=&s"(z), "=&s"(o)
+                 : "s"(wave_uniform(s)), "s"(wave_uniform(steps)), "s"(wave_uniform((int)bytes)),
+                   "s"(wave_uniform((int)soff))
+                 : "scc");
+    buffer.z = (int)z;
+    *out = o;
+}
+
+template <int J>
+__device__ __forceinline__ void dma16_of4(const ep_i32x4 &rsrc, uint32_t lds, uint32_t voff,
+                                          uint32_t soff) {
+    ep_i32x4 r;
+    for (int i = 0; i < 4; ++i) r[i] = wave_uniform(rsrc[i]);
+    if (J == 0) asm volatile("s_mov_b32 m0, %0\n\ts_nop 0" : : "s"(wave_uniform((int)lds)));
+    asm volatile("buffer_load_dwordx4 %0, %1, %2 offen offset:%3 lds"
+                 :
+                 : "v"(voff), "s"(r), "s"(wave_uniform((int)soff)), "n"(J * 1024));
 }
 
 // All but the newest N copies of this wave have landed, and its own LDS reads
@@ -153,6 +190,35 @@ __device__ __forceinline__ uint32_t lds_offset(const void *p) {
 // otherwise move the instruction into a branch that only some lanes take, and
 // it needs all lanes' operands.
 __device__ __forceinline__ void pin(ep_f32x4 &v) { asm volatile("" : "+v"(v)); }
+
+// Tiles staged with the summed index outermost ([64 rows][128 or 256 columns]
+// of bf16, ROW bytes a row): the 32-byte granule g of row r is in place
+// g ^ granule_of(r), so that the 16 rows one transposing read takes lie in
+// different banks.
+__device__ __forceinline__ int granule_of(int r) { return (r & 3) | ((r >> 3 & 1) << 2); }
+
+// The matrix operand of 16 columns (granule g) and rows [32 h, 32 h + 32) of
+// such a tile, by the transposing LDS read: lane l of a 16-lane group names row
+// l/4 and column 4 (l % 4) of a 4 x 16 block and receives its column l.
+template <int ROW>
+__device__ __forceinline__ ep_u32x4 transposed_operand(const uint8_t *tile, int g, int h) {
+    const int lane = threadIdx.x & 63, l16 = lane & 15;
+    const int r = h * 32 + (lane >> 4) * 8 + (l16 >> 2);
+    const uint8_t *p = tile + r * ROW + (g ^ granule_of(r)) * 32 + (l16 & 3) * 8;
+    const ep_i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (__attribute__((address_space(3))) ep_i16x4 *)p);
+    const ep_i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (__attribute__((address_space(3))) ep_i16x4 *)(p + 4 * ROW));
+    ep_u32x4 v;
+    v.xy = __builtin_bit_cast(ep_u32x2, lo);
+    v.zw = __builtin_bit_cast(ep_u32x2, hi);
+    return v;
+}
+
+__device__ __forceinline__ ep_f32x4 mfma_bf16(ep_u32x4 a, ep_u32x4 b, ep_f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(ep_bf16x8, a),
+                                                   __builtin_bit_cast(ep_bf16x8, b), c, 0, 0, 0);
+}
 
 // fp32 pairs to packed bf16, nearest even (the hardware conversion).
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
@@ -185,13 +251,17 @@ __device__ __forceinline__ float gelu_gate(float z) {
     return sigmoid(c * z * __builtin_fmaf(0.044715f * z, z, 1.0f));
 }
 
-// Activation functions of one value: kind 0 none, 1 silu, 2 gelu.  z times a
-// gate that underflowed to 0 is 0 for every finite z; -inf gives -inf * 0 =
-// NaN, as the formula does.
-__device__ __forceinline__ float act_value(float z, int kind) {
-    if (kind == 1) return z * sigmoid(z);
-    if (kind == 2) return z * gelu_gate(z);
-    return z;
+// Activation functions of one value that is rounded to bf16 next: kind 0 none,
+// 1 silu, 2 gelu.  The gate's exponential takes its argument rounded to fp32
+// (relative error |z| 2^-24, under bf16's 2^-8 by far) without fast_exp's
+// remainder: half the instructions.  A gate that underflowed to 0 gives 0 for
+// every finite z; -inf gives -inf * 0 = NaN, as the formula does.
+template <int KIND>
+__device__ __forceinline__ float act_value(float z) {
+    if (KIND == 0) return z;
+    const float y = KIND == 1 ? z * -1.44269504f
+                              : z * __builtin_fmaf(z * z, -0.102943240f, -2.30220819f);
+    return z * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(y));
 }
 
 // Value and derivative of an activation function.

@@ -7,16 +7,14 @@
 // row (64 bf16 or 128 fp8 channels), copied there without registers, in a
 // ring of NS stages with one barrier per step.
 //
-// The weights are the matrix instruction's first operand, so a lane's four
-// accumulators are four consecutive columns of one row: bias, residual and
+// The weights are the matrix instruction's first operand, so four accumulators
+// of a lane are four consecutive columns of one row: bias, residual and
 // output move in 8-byte pieces and the checkpoint's codes in dwords.
 //
 // LDS rows are 8 chunks of 16 bytes, chunk c of row r in slot c ^ (r/2 & 7):
 // the 16 rows x 16 bytes a quarter wave reads lie in 16 different slots of the
 // 256-byte bank line.  Weights that lie [k, n] (transposed) are staged as 64
-// rows of 256 columns, 32-byte granule g of row k in place g ^ (k & 3 | (k >>
-// 3 & 1) << 2), and read by the transposing LDS read: lane l of a 16-lane
-// group names row l/4 and column 4 (l % 4) and receives column l of four rows.
+// rows of 256 columns and read by the transposing LDS read.
 #include "ep_expert_device.h"
 
 namespace ep {
@@ -41,6 +39,16 @@ struct LinearK {
     int col_tiles;
 };
 
+// f(0), ..., f(N - 1) with constant arguments: accumulators indexed by them
+// stay in registers whatever the body's size.
+template <int N, typename F>
+__device__ __forceinline__ void each(F f) {
+    if constexpr (N > 0) {
+        each<N - 1>(f);
+        f(std::integral_constant<int, N - 1>{});
+    }
+}
+
 // Four consecutive scale bytes of a row from step s on, as far as the row has them.
 __device__ __forceinline__ int scales4(const uint8_t *row, int s, int groups) {
     int v = 0;
@@ -58,24 +66,32 @@ __device__ __forceinline__ int scales4(const uint8_t *row, int s, int groups) {
 // 1e-5 of sum |x w|, well inside the result's bf16 rounding, for twice the bf16
 // instruction's rate.
 template <int SB>
-__device__ __forceinline__ ep_f32x4 mfma_fp8(ep_i32x8 a, ep_i32x8 b, ep_f32x4 c, int sa, int sb) {
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, SB, sa, SB, sb);
+__device__ __forceinline__ ep_f32x4 mfma_fp8(const ep_u32x4 *a, const ep_u32x4 *b, ep_f32x4 c,
+                                             int sa, int sb) {
+    // a lane's 32 channels are chunks q and q + 4 of the row, alike in both
+    // operands; one scale covers all 128
+    ep_i32x8 x, y;
+    x.lo = __builtin_bit_cast(ep_i32x4, a[0]);
+    x.hi = __builtin_bit_cast(ep_i32x4, a[1]);
+    y.lo = __builtin_bit_cast(ep_i32x4, b[0]);
+    y.hi = __builtin_bit_cast(ep_i32x4, b[1]);
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, c, 0, 0, SB, sa, SB, sb);
 }
 
-// One 32-channel group of pre-activations (two tiles of four accumulators, the
-// other 24 in the lanes 16, 32 and 48 away) to e4m3 codes under a power of two:
-// the format of ep_cast_fp8 with UE8M0 scales, taken from the fp32 sums.
-__device__ __forceinline__ void checkpoint_group(const float *z0, const float *z1, bool valid,
-                                                 int q, uint8_t *codes, uint8_t *scale) {
+// One 32-channel group of pre-activations (a lane's 8 of a row, the other 24 in
+// the lanes 16, 32 and 48 away) to e4m3 codes under a power of two: the format
+// of ep_cast_fp8 with UE8M0 scales, taken from the fp32 sums.
+__device__ __forceinline__ void checkpoint_group(const float *z, bool valid, int q, uint8_t *codes,
+                                                 uint8_t *scale) {
     float m = 0.0f;
-    for (int i = 0; i < 4; ++i) m = fmaxf(m, fmaxf(fabsf(z0[i]), fabsf(z1[i])));
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(z[i]));
     m = fmaxf(m, __shfl_xor(m, 16));
     m = fmaxf(m, __shfl_xor(m, 32));
     m = fminf(m, 3.0e38f);
     const uint32_t e = ue8m0_of(pow2_ceil(scale_of(m)));
     const float inv = __uint_as_float((254u - e) << 23);
-    const uint32_t c0 = pack4_e4m3(z0[0] * inv, z0[1] * inv, z0[2] * inv, z0[3] * inv);
-    const uint32_t c1 = pack4_e4m3(z1[0] * inv, z1[1] * inv, z1[2] * inv, z1[3] * inv);
+    const uint32_t c0 = pack4_e4m3(z[0] * inv, z[1] * inv, z[2] * inv, z[3] * inv);
+    const uint32_t c1 = pack4_e4m3(z[4] * inv, z[5] * inv, z[6] * inv, z[7] * inv);
     if (valid) {
         *(uint32_t *)(codes + 4 * q) = c0;
         *(uint32_t *)(codes + 16 + 4 * q) = c1;
@@ -83,6 +99,100 @@ __device__ __forceinline__ void checkpoint_group(const float *z0, const float *z
     }
 }
 
+// Bias, checkpoint, activation, residual and output of a wave's accumulators:
+// NG groups of 32 columns of z, group g from column c[g] (gated: the first half
+// of the groups are gates, the second their ups), by MT * 16 rows from `first`
+// of the segment, `live_rows` of them there.  Accumulator j of tile 2 g + h is
+// column 16 h + 4 q + j of group g, row lane % 16 of its row tile.
+template <int KIND, int NG, int MT, bool GATED>
+__device__ __forceinline__ void epilogue_of(const LinearK &a, const TileAt &at, int first,
+                                            int live_rows, const int *c, ep_f32x4 (*acc)[MT]) {
+    constexpr int OG = GATED ? NG / 2 : NG, NK = GATED ? 2 : 1;
+    const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
+    const int N = a.n;
+    const int64_t row0 = (int64_t)at.row0 + first + l16;
+    // one group's (gated: two groups') pre-activations at a time
+    each<OG>([&](auto gg) __attribute__((always_inline)) {
+        constexpr int g = decltype(gg)::value;
+        float b[NK][8];
+#pragma unroll
+        for (int k = 0; k < NK; ++k)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                ep_u32x2 v = {0, 0};
+                const int col = c[g + k * OG] + 16 * h + 4 * q;
+                if (a.bias && col < N) v = *(const ep_u32x2 *)(a.bias + (int64_t)at.e * N + col);
+                b[k][4 * h] = bf16_lo(v.x);
+                b[k][4 * h + 1] = bf16_hi(v.x);
+                b[k][4 * h + 2] = bf16_lo(v.y);
+                b[k][4 * h + 3] = bf16_hi(v.y);
+            }
+        // the residual of all row tiles at once: one wait
+        ep_u32x2 res[MT][2];
+        if (a.residual) {
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int col = c[g] + 16 * h + 4 * q;
+                    res[i][h] = ep_u32x2{0, 0};
+                    if (i * 16 + l16 < live_rows && col < a.m)
+                        res[i][h] = *(const ep_u32x2 *)(a.residual + (row0 + i * 16) * a.m + col);
+                }
+        }
+        each<MT>([&](auto ii) __attribute__((always_inline)) {
+            constexpr int i = decltype(ii)::value;
+            const bool live = i * 16 + l16 < live_rows;
+            const int64_t row = row0 + i * 16;
+            float z[NK][8];
+#pragma unroll
+            for (int k = 0; k < NK; ++k) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    ep_f32x4 s = acc[2 * (g + k * OG) + h][i];
+                    pin(s);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) z[k][4 * h + j] = s[j] + b[k][4 * h + j];
+                }
+                // n is a multiple of the group, so its 32 channels are there or none is
+                const int from = c[g + k * OG];
+                if (a.ckpt)
+                    checkpoint_group(z[k], live && c[g] + 32 <= a.m, q, a.ckpt + row * N + from,
+                                     a.ckpt_scales + row * (N >> 5) + (from >> 5));
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float y[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    y[j] = act_value<KIND>(z[0][4 * h + j]);
+                    if (GATED) y[j] *= z[NK - 1][4 * h + j];
+                }
+                const int col = c[g] + 16 * h + 4 * q;
+                if (a.residual) {
+                    y[0] += bf16_lo(res[i][h].x); y[1] += bf16_hi(res[i][h].x);
+                    y[2] += bf16_lo(res[i][h].y); y[3] += bf16_hi(res[i][h].y);
+                }
+                ep_u32x2 v;
+                v.x = pack_bf16(y[0], y[1]);
+                v.y = pack_bf16(y[2], y[3]);
+                if (live && col < a.m) *(ep_u32x2 *)(a.out + row * a.m + col) = v;
+            }
+        });
+        __builtin_amdgcn_sched_barrier(0);
+    });
+}
+
+template <int NG, int MT, bool GATED>
+__device__ __forceinline__ void epilogue(const LinearK &a, const TileAt &at, int first,
+                                         int live_rows, const int *c, ep_f32x4 (*acc)[MT]) {
+    if (a.kind == 1) epilogue_of<1, NG, MT, GATED>(a, at, first, live_rows, c, acc);
+    else if (a.kind == 2) epilogue_of<2, NG, MT, GATED>(a, at, first, live_rows, c, acc);
+    else if (!GATED) epilogue_of<0, NG, MT, GATED>(a, at, first, live_rows, c, acc);
+}
+
+// Tiles of up to 128 rows: bound by reading the weights unless several segments'
+// row tiles share them.  The ring of NS stages keeps NS - 1 steps in flight.
 template <int BM, int WM, int NS, bool FP8, bool WT, bool GATED>
 __global__ __launch_bounds__(256 * WM, 2) void expert_linear_kernel(LinearK a) {
     constexpr int kWaves = 4 * WM;
@@ -135,8 +245,7 @@ __global__ __launch_bounds__(256 * WM, 2) void expert_linear_kernel(LinearK a) {
         } else {
             const int kr = (j * kWaves + wave) * 2 + (lane >> 5);
             const int c16 = lane & 31;
-            const int f = (kr & 3) | ((kr >> 3 & 1) << 2);
-            const int c = column(((c16 >> 1) ^ f) * 16 + (c16 & 1) * 8);
+            const int c = column(((c16 >> 1) ^ granule_of(kr)) * 16 + (c16 & 1) * 8);
             wk[j] = kr;
             woff[j] = (uint32_t)kr * (uint32_t)N * 2 + (uint32_t)c * 2;
             if (c >= N) woff[j] = kOutOfRange;
@@ -167,69 +276,52 @@ __global__ __launch_bounds__(256 * WM, 2) void expert_linear_kernel(LinearK a) {
     };
 
     ep_f32x4 acc[4][MT];
+#pragma unroll
     for (int t = 0; t < 4; ++t)
+#pragma unroll
         for (int i = 0; i < MT; ++i) acc[t][i] = ep_f32x4{0, 0, 0, 0};
 
-    // fp8: this lane's scale bytes, four steps in a dword
-    const uint8_t *xs_row[FP8 ? MT : 1];
-    const uint8_t *ws_row[FP8 ? 4 : 1];
-    int xs[FP8 ? MT : 1], ws[FP8 ? 4 : 1];
-    if (FP8) {
+    int xs[FP8 ? MT : 1], ws[FP8 ? 4 : 1];             // fp8: scale bytes of four steps
+    auto scales = [&](int s) {
         const int groups = K / kFp8Group;
+#pragma unroll
         for (int i = 0; i < MT; ++i) {
             const int r = min(wm * MT * 16 + i * 16 + l16, rows - 1);
-            xs_row[i] = a.x_scales + ((int64_t)at.row0 + row0 + r) * groups;
+            xs[FP8 ? i : 0] = scales4(a.x_scales + ((int64_t)at.row0 + row0 + r) * groups, s, groups);
         }
+#pragma unroll
         for (int t = 0; t < 4; ++t) {
-            const int c = min(column(wn * 64 + t * 16 + l16), N - 1);
-            ws_row[t] = a.w_scales + ((int64_t)at.e * N + c) * groups;
+            const int c = min(column(wn * 64 + t * 16) + l16, N - 1);
+            ws[FP8 ? t : 0] = scales4(a.w_scales + ((int64_t)at.e * N + c) * groups, s, groups);
         }
-    }
+    };
 
-    const int lrow = l16 * 128;
-    const int slot = (q ^ (l16 >> 1)) * 16;
+    const int slot = l16 * 128 + (q ^ (l16 >> 1)) * 16;
     auto compute = [&](int stage, auto sb) {
         const uint8_t *wl = lds + stage * kStage;
-        const uint8_t *xl = wl + kWStage + wm * MT * 16 * 128 + lrow;
-        ep_u32x4 xf[2][MT], wf[2][4];
-        for (int kk = 0; kk < 2; ++kk) {
-            for (int t = 0; t < 4; ++t) {
-                if (!WT) {
-                    wf[kk][t] = *(const ep_u32x4 *)(wl + wn * 64 * 128 + lrow + t * 2048 + (slot ^ (kk * 64)));
-                } else {
-                    const int kr = kk * 32 + q * 8 + (l16 >> 2);
-                    const int f = (kr & 3) | ((kr >> 3 & 1) << 2);
-                    const uint8_t *p = wl + kr * 512 + (((wn * 4 + t) ^ f) * 32) + (l16 & 3) * 8;
-                    const ep_i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                        (__attribute__((address_space(3))) ep_i16x4 *)p);
-                    const ep_i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                        (__attribute__((address_space(3))) ep_i16x4 *)(p + 4 * 512));
-                    wf[kk][t].xy = __builtin_bit_cast(ep_u32x2, lo);
-                    wf[kk][t].zw = __builtin_bit_cast(ep_u32x2, hi);
-                }
-            }
-            for (int i = 0; i < MT; ++i) xf[kk][i] = *(const ep_u32x4 *)(xl + i * 2048 + (slot ^ (kk * 64)));
-            if (!FP8) {
-                for (int i = 0; i < MT; ++i)
-                    for (int t = 0; t < 4; ++t)
-                        acc[t][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                            __builtin_bit_cast(ep_bf16x8, wf[kk][t]),
-                            __builtin_bit_cast(ep_bf16x8, xf[kk][i]), acc[t][i], 0, 0, 0);
-            }
-        }
-        if (FP8) {
-            // a lane's 32 channels are chunks q and q + 4 of the row, the same
-            // in both operands; one scale covers all 128
+        const uint8_t *xl = wl + kWStage + wm * MT * 16 * 128;
+        ep_u32x4 wf[4][2], xf[MT][2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+                wf[t][h] = WT ? transposed_operand<512>(wl, wn * 4 + t, h)
+                              : *(const ep_u32x4 *)(wl + (wn * 4 + t) * 2048 + (slot ^ (h * 64)));
+#pragma unroll
             for (int i = 0; i < MT; ++i)
-                for (int t = 0; t < 4; ++t) {
-                    ep_i32x8 wv, xv;
-                    wv.lo = __builtin_bit_cast(ep_i32x4, wf[0][t]);
-                    wv.hi = __builtin_bit_cast(ep_i32x4, wf[1][t]);
-                    xv.lo = __builtin_bit_cast(ep_i32x4, xf[0][i]);
-                    xv.hi = __builtin_bit_cast(ep_i32x4, xf[1][i]);
-                    acc[t][i] = mfma_fp8<decltype(sb)::value>(wv, xv, acc[t][i], ws[FP8 ? t : 0], xs[FP8 ? i : 0]);
-                }
+                xf[i][h] = *(const ep_u32x4 *)(xl + i * 2048 + (slot ^ (h * 64)));
         }
+#pragma unroll
+        for (int h = 0; h < (FP8 ? 1 : 2); ++h)
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    if (FP8)
+                        acc[t][i] = mfma_fp8<decltype(sb)::value>(wf[t], xf[i], acc[t][i], ws[FP8 ? t : 0], xs[FP8 ? i : 0]);
+                    else
+                        acc[t][i] = mfma_bf16(wf[t][h], xf[i][h], acc[t][i]);
+                }
     };
 
     for (int s = 0; s < NS - 1; ++s)
@@ -247,10 +339,8 @@ __global__ __launch_bounds__(256 * WM, 2) void expert_linear_kernel(LinearK a) {
         stage = stage + 1 == NS ? 0 : stage + 1;
     };
     if (FP8) {
-        const int groups = K / kFp8Group;
         for (int s = 0; s < steps; s += 4) {
-            for (int i = 0; i < MT; ++i) xs[FP8 ? i : 0] = scales4(xs_row[FP8 ? i : 0], s, groups);
-            for (int t = 0; t < 4; ++t) ws[FP8 ? t : 0] = scales4(ws_row[FP8 ? t : 0], s, groups);
+            scales(s);
             step(s, std::integral_constant<int, 0>{});
             if (s + 1 < steps) step(s + 1, std::integral_constant<int, 1>{});
             if (s + 2 < steps) step(s + 2, std::integral_constant<int, 2>{});
@@ -259,71 +349,259 @@ __global__ __launch_bounds__(256 * WM, 2) void expert_linear_kernel(LinearK a) {
     } else {
         for (int s = 0; s < steps; ++s) step(s, std::integral_constant<int, 0>{});
     }
+    const int cols[2] = {column(wn * 64), column(wn * 64 + 32)};
+    epilogue<2, MT, GATED>(a, at, row0 + wm * MT * 16, rows - wm * MT * 16, cols, acc);
+}
 
+// Tiles of 256 rows, bound by the matrix instructions.  Four waves of 128 x 128:
+// a K step then reads 128 KB of LDS for 2048 matrix cycles of a compute unit,
+// half of what its LDS can deliver (eight waves of 64 x 128 read 192 KB and,
+// with the copies' 64 KB of writes, saturate it).
+//
+// Two stages of 64 KB fill the LDS, so what hides the copies' latency is how
+// early a piece of a stage is given back: a stage is four regions (the waves'
+// first and second 64 weight rows, first and second 64 x rows), each read to
+// registers in one phase and copied anew from the next, seven of the eight
+// phases of two steps before it is read again.  A phase is a quarter of a step:
+// the matrix instructions of one weight region and one x region, with the reads
+// of the next region and the copies placed among them (one wave runs on a SIMD:
+// nothing else would fill the gaps), then the wait and the barrier:
+//   phase   multiplies   reads (step)   copies (step)
+//     0       W0 X0        W1 (s)        W0 (s + 2)
+//     1       W1 X0        X1 (s)        W1 (s + 2)
+//     2       W0 X1        X0 (s + 1)    X1 (s + 2)
+//     3       W1 X1        W0 (s + 1)    X0 (s + 3)
+// Copies behind the last step go on from an empty buffer (they write zeros), so
+// that the number in flight, which the waits count, stays the same.  Channels
+// that do not fill a step are one more step after the loop.
+template <bool FP8, bool WT, bool GATED>
+__global__ __launch_bounds__(256, 1) void expert_linear_wide_kernel(LinearK a) {
+    constexpr int BM = 256, kWaves = 4;
+    constexpr int kRegion = 128 * 128, kStage = 4 * kRegion;     // W0, W1, X0, X1
+    constexpr int ES = FP8 ? 1 : 2;
+    constexpr int BK = 128 / ES;
+    __shared__ __align__(1024) uint8_t lds[2 * kStage];
+    __shared__ int red[16];
+
+    TileAt at;
+    if (!find_tile<64 * kWaves>(a.seg, BM, a.col_tiles, blockIdx.x, red, &at)) return;
+
+    const int lane = threadIdx.x & 63, wave = wave_uniform(threadIdx.x >> 6);
+    const int l16 = lane & 15, q = lane >> 4;
+    const int wn = wave & 1, wm = wave >> 1;
+    const int K = a.k, N = a.n;
+    const int half = N >> 1;
+    const int row0 = at.mt * BM;                       // in the segment
+    const int rows = min(BM, at.rows - row0);
+    // first column of the 64 weight rows of region t of the waves with this wn
+    auto column = [&](int n, int t) {
+        if (!GATED) return at.nt * kBN + n * 128 + t * 64;
+        return at.nt * (kBN / 2) + n * 64 + (t ? half : 0);
+    };
+
+    const uint32_t ld_bytes = (uint32_t)K * ES;
+    const uint32_t w_bytes = (uint32_t)N * ld_bytes;
+    const uint32_t x_bytes = (uint32_t)rows * ld_bytes;
+    ep_i32x4 xb = biased_buffer(a.x + ((int64_t)at.row0 + row0) * ld_bytes, x_bytes);
+    ep_i32x4 wb = biased_buffer(a.w + (int64_t)at.e * w_bytes, w_bytes);
+    // copies: a wave moves 32 rows of 128 bytes of each region, 8 at a time
+    // (transposed weights: 16 k rows of 128 columns, 4 at a time)
+    uint32_t woff[2][4], xoff[2][4];
+    const int cs = (lane & 7) ^ (lane >> 4);           // this lane's chunk of its rows, for even j
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
-        for (int t = 0; t < 4; ++t) pin(acc[t][i]);
-
-    // epilogue
-    const int kind = a.kind;
-    float b[4][4];
-    bool in[4];
-    int col[4];
-    for (int t = 0; t < 4; ++t) {
-        col[t] = column(wn * 64 + t * 16) + 4 * q;
-        in[t] = GATED ? col[t & 1] < half : col[t] < N;
-        for (int i = 0; i < 4; ++i) b[t][i] = 0.0f;
-        if (a.bias && in[t]) {
-            const ep_u32x2 v = *(const ep_u32x2 *)(a.bias + (int64_t)at.e * N + col[t]);
-            b[t][0] = bf16_lo(v.x); b[t][1] = bf16_hi(v.x);
-            b[t][2] = bf16_lo(v.y); b[t][3] = bf16_hi(v.y);
+    for (int j = 0; j < 4; ++j) {
+        const int r = wave * 32 + j * 8 + (lane >> 3);         // row of the region, 0..127
+        const int ch = cs ^ ((j & 1) * 4);                     // chunk (lane & 7) ^ (r / 2 & 7)
+        const uint32_t bias = kDmaBias - j * 1024;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            xoff[t][j] = (uint32_t)((r >> 6) * 128 + t * 64 + (r & 63)) * ld_bytes + ch * 16 + bias;
+            if (!WT) {
+                const int c = column(r >> 6, t) + (r & 63);
+                woff[t][j] = c < N ? (uint32_t)c * ld_bytes + ch * 16 + bias : kOutOfRange;
+            } else {
+                const int kr = wave * 16 + j * 4 + (lane >> 4);
+                const int g = (lane >> 1 & 7) ^ granule_of(kr);        // 16 columns each
+                const int c = column(g >> 2, t) + (g & 3) * 16 + (lane & 1) * 8;
+                woff[t][j] = c < N ? ((uint32_t)kr * (uint32_t)N + (uint32_t)c) * 2 + bias : kOutOfRange;
+            }
         }
     }
+    const uint32_t lds0 = lds_offset(lds) + wave * 4096;
+    const int steps = K / BK;                          // whole steps
+    const uint32_t w_step = WT ? (uint32_t)BK * (uint32_t)N * 2 : 128;
+    uint32_t xs_off = 0, ws_off = 0;                   // where the region being copied begins
+    auto copy_w = [&](int s, int stage, int t, auto j) {
+        constexpr int J = decltype(j)::value;
+        if (J == 0) range_of(s, steps, w_bytes + kDmaBias, s * w_step, wb, &ws_off);
+        dma16_of4<J>(wb, lds0 + stage * kStage + t * kRegion, woff[t][J], ws_off);
+    };
+    auto copy_x = [&](int s, int stage, int t, auto j) {
+        constexpr int J = decltype(j)::value;
+        if (J == 0) range_of(s, steps, x_bytes + kDmaBias, s * 128, xb, &xs_off);
+        dma16_of4<J>(xb, lds0 + stage * kStage + (2 + t) * kRegion, xoff[t][J], xs_off);
+    };
+
+    // LDS addresses of this lane's operands, by stage and half
+    const int slot = l16 * 128 + (q ^ (l16 >> 1)) * 16;
+    const uint8_t *xat[2][2], *wat[2][2];
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-        const int r = wm * MT * 16 + i * 16 + l16;
-        const bool live = r < rows;
-        const int64_t row = (int64_t)at.row0 + row0 + r;
-        float z[4][4];
-        for (int t = 0; t < 4; ++t)
-            for (int j = 0; j < 4; ++j) z[t][j] = acc[t][i][j] + b[t][j];
-        if (a.ckpt) {
-            for (int g = 0; g < 2; ++g) {
-                const int c = col[2 * g] - 4 * q;      // the group's first channel
-                checkpoint_group(z[2 * g], z[2 * g + 1], live && in[2 * g], q,
-                                 a.ckpt + row * N + c, a.ckpt_scales + row * (N >> 5) + (c >> 5));
-            }
+    for (int st = 0; st < 2; ++st)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            xat[st][h] = lds + st * kStage + 2 * kRegion + wm * 8192 + (slot ^ (h * 64));
+            wat[st][h] = lds + st * kStage + wn * 8192 + (slot ^ (h * 64));
         }
+    ep_u32x4 wf[2][4][2], xf[2][4][2];                 // [region][tile][half]
+    auto read_w = [&](int stage, int t, int i) {       // one tile
 #pragma unroll
-        for (int t = 0; t < (GATED ? 2 : 4); ++t) {
-            float y[4];
-            for (int j = 0; j < 4; ++j) {
-                y[j] = act_value(z[t][j], kind);
-                if (GATED) y[j] *= z[(t + 2) & 3][j];
-            }
-            if (!live || !in[t]) continue;
-            const int64_t o = row * a.m + col[t];
-            if (a.residual) {
-                const ep_u32x2 v = *(const ep_u32x2 *)(a.residual + o);
-                y[0] += bf16_lo(v.x); y[1] += bf16_hi(v.x);
-                y[2] += bf16_lo(v.y); y[3] += bf16_hi(v.y);
-            }
-            ep_u32x2 v;
-            v.x = pack_bf16(y[0], y[1]);
-            v.y = pack_bf16(y[2], y[3]);
-            *(ep_u32x2 *)(a.out + o) = v;
+        for (int h = 0; h < 2; ++h)
+            wf[t][i][h] = WT ? transposed_operand<256>(lds + stage * kStage + t * kRegion, wn * 4 + i, h)
+                             : *(const ep_u32x4 *)(wat[stage][h] + t * kRegion + i * 2048);
+    };
+    auto read_x = [&](int stage, int t, int i) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            xf[t][i][h] = *(const ep_u32x4 *)(xat[stage][h] + t * kRegion + i * 2048);
+    };
+
+    ep_f32x4 acc[8][8];                                // [4 region + tile] of weights, of x
+#pragma unroll
+    for (int t = 0; t < 8; ++t)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[t][i] = ep_f32x4{0, 0, 0, 0};
+    int xs[8], ws[8];                                  // fp8: scale bytes of four steps
+    auto scales = [&](int s) {
+        const int groups = K / kFp8Group;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = min(wm * 128 + i * 16 + l16, rows - 1);
+            xs[i] = scales4(a.x_scales + ((int64_t)at.row0 + row0 + r) * groups, s, groups);
+            const int c = min(column(wn, i >> 2) + (i & 3) * 16 + l16, N - 1);
+            ws[i] = scales4(a.w_scales + ((int64_t)at.e * N + c) * groups, s, groups);
+        }
+    };
+    // One phase: `read(i)` and `copy(i)`, i = 0..3, placed among the matrix
+    // instructions; then the region the next phase reads has landed, and every
+    // wave has read the one this phase read.
+    auto phase = [&](int tw, int tx, auto sb, auto read, auto copy) {
+        constexpr int n = FP8 ? 16 : 32;
+        each<n>([&](auto mm) {
+            constexpr int m = decltype(mm)::value;
+            constexpr int h = m / 16, b = m / 4 % 4, c = m % 4;
+            ep_f32x4 &d = acc[tw * 4 + b][tx * 4 + c];
+            if (FP8) d = mfma_fp8<decltype(sb)::value>(wf[tw][b], xf[tx][c], d, ws[tw * 4 + b], xs[tx * 4 + c]);
+            else d = mfma_bf16(wf[tw][b][h], xf[tx][c][h], d);
+            // reads in the first half, copies spread over all
+            if constexpr (m % (n / 8) == 0 && m < n / 2) read(m / (n / 8));
+            if constexpr (m % (n / 4) == n / 8) copy(std::integral_constant<int, m / (n / 4)>{});
+            __builtin_amdgcn_sched_barrier(0);
+        });
+        dma_wait<24>();
+        barrier_only();
+        __builtin_amdgcn_sched_barrier(0);
+    };
+
+    for (int s = 0; s < 2; ++s) {
+        each<4>([&](auto j) { copy_x(s, s, 0, j); });
+        each<4>([&](auto j) { copy_w(s, s, 0, j); });
+        each<4>([&](auto j) { copy_w(s, s, 1, j); });
+        each<4>([&](auto j) { copy_x(s, s, 1, j); });
+    }
+    dma_wait<24>();
+    barrier_only();
+    each<4>([&](auto i) { read_x(0, 0, i); });
+    each<4>([&](auto i) { read_w(0, 0, i); });
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    barrier_only();
+    each<4>([&](auto j) { copy_x(2, 0, 0, j); });
+    dma_wait<24>();
+    barrier_only();
+
+    auto step = [&](int s, auto stage, auto sb) {
+        constexpr int st = decltype(stage)::value;
+        phase(0, 0, sb, [&](int i) { read_w(st, 1, i); }, [&](auto j) { copy_w(s + 2, st, 0, j); });
+        phase(1, 0, sb, [&](int i) { read_x(st, 1, i); }, [&](auto j) { copy_w(s + 2, st, 1, j); });
+        phase(0, 1, sb, [&](int i) { read_x(st ^ 1, 0, i); }, [&](auto j) { copy_x(s + 2, st, 1, j); });
+        phase(1, 1, sb, [&](int i) { read_w(st ^ 1, 0, i); }, [&](auto j) { copy_x(s + 3, st ^ 1, 0, j); });
+    };
+    constexpr std::integral_constant<int, 0> c0{};
+    constexpr std::integral_constant<int, 1> c1{};
+    if (FP8) {
+        for (int s = 0; s < steps; s += 4) {
+            scales(s);
+            step(s, c0, c0);
+            if (s + 1 < steps) step(s + 1, c1, c1);
+            if (s + 2 < steps) step(s + 2, c0, std::integral_constant<int, 2>{});
+            if (s + 3 < steps) step(s + 3, c1, std::integral_constant<int, 3>{});
+        }
+    } else {
+        for (int s = 0; s < steps; s += 2) {
+            step(s, c0, c0);
+            if (s + 1 < steps) step(s + 1, c1, c0);
         }
     }
+    // no copy may still be on its way to this workgroup's LDS when it ends, or
+    // when the rest of the channels takes stage 0
+    dma_wait<0>();
+    if (!FP8 && K > steps * BK) {
+        barrier_only();
+        const int left = K - steps * BK;
+        each<2>([&](auto tt) {
+            constexpr int t = decltype(tt)::value;
+            each<4>([&](auto jj) {
+                constexpr int J = decltype(jj)::value;
+                const uint32_t past = (cs ^ ((J & 1) * 4)) * 8 >= left ? kOutOfRange : 0;
+                range_of(0, 1, x_bytes + kDmaBias, steps * 128, xb, &xs_off);
+                dma16_of4<J>(xb, lds0 + (2 + t) * kRegion, xoff[t][J] | past, xs_off);
+            });
+            each<4>([&](auto jj) {
+                constexpr int J = decltype(jj)::value;
+                const uint32_t past = !WT && (cs ^ ((J & 1) * 4)) * 8 >= left ? kOutOfRange : 0;
+                range_of(0, 1, w_bytes + kDmaBias, steps * w_step, wb, &ws_off);
+                dma16_of4<J>(wb, lds0 + t * kRegion, woff[t][J] | past, ws_off);
+            });
+        });
+        dma_wait<0>();
+        barrier_only();
+        each<2>([&](auto t) { each<4>([&](auto i) { read_x(0, t, i); read_w(0, t, i); }); });
+        each<2>([&](auto tw) { each<2>([&](auto tx) { each<32>([&](auto mm) {
+            constexpr int m = decltype(mm)::value, h = m / 16, b = m / 4 % 4, c = m % 4;
+            ep_f32x4 &d = acc[decltype(tw)::value * 4 + b][decltype(tx)::value * 4 + c];
+            d = mfma_bf16(wf[decltype(tw)::value][b][h], xf[decltype(tx)::value][c][h], d);
+        }); }); });
+    }
+    const int cols[4] = {column(wn, 0), column(wn, 0) + 32, column(wn, 1), column(wn, 1) + 32};
+    epilogue<4, 8, GATED>(a, at, row0 + wm * 128, rows - wm * 128, cols, acc);
+}
+
+// Workgroups for row tiles of BM rows: each segment's last one may be partial.
+int64_t grid_of(const LinearArgs &a, const LinearK &k, int BM) {
+    const int64_t most = a.seg.pairs < a.seg.num_rows ? a.seg.pairs : a.seg.num_rows;
+    const int64_t some = most < a.seg.E ? most : a.seg.E;
+    return ((most / BM + some) * k.col_tiles + 7) / 8 * 8;
+}
+
+hipError_t launch_wide(const LinearArgs &a, const LinearK &k, bool gated, hipStream_t stream) {
+    const int64_t grid = grid_of(a, k, 256);
+    if (grid > 0x7fffffff) return hipErrorInvalidConfiguration;
+    const dim3 g((unsigned)grid), t(256);
+    if (a.fp8) {
+        if (gated) expert_linear_wide_kernel<true, false, true><<<g, t, 0, stream>>>(k);
+        else expert_linear_wide_kernel<true, false, false><<<g, t, 0, stream>>>(k);
+    } else if (a.transposed) {
+        if (gated) expert_linear_wide_kernel<false, true, true><<<g, t, 0, stream>>>(k);
+        else expert_linear_wide_kernel<false, true, false><<<g, t, 0, stream>>>(k);
+    } else {
+        if (gated) expert_linear_wide_kernel<false, false, true><<<g, t, 0, stream>>>(k);
+        else expert_linear_wide_kernel<false, false, false><<<g, t, 0, stream>>>(k);
+    }
+    return hipGetLastError();
 }
 
 template <int BM, int WM, int NS>
 hipError_t launch_bm(const LinearArgs &a, const LinearK &k, bool gated, hipStream_t stream) {
-    // row tiles: each segment's last one may be partial
-    const int64_t most = a.seg.pairs < a.seg.num_rows ? a.seg.pairs : a.seg.num_rows;
-    const int64_t some = most < a.seg.E ? most : a.seg.E;
-    const int64_t tiles = (most / BM + some) * k.col_tiles;
-    const int64_t grid = (tiles + 7) / 8 * 8;
-    if (grid == 0) return hipSuccess;
+    const int64_t grid = grid_of(a, k, BM);
     if (grid > 0x7fffffff) return hipErrorInvalidConfiguration;
     const dim3 g((unsigned)grid), t(256 * WM);
     if (a.fp8) {
@@ -361,7 +639,7 @@ hipError_t launch_expert_linear(const LinearArgs &a, hipStream_t stream) {
     const int per_tile = gated ? kBN / 2 : kBN;
     k.col_tiles = (k.m + per_tile - 1) / per_tile;
     const int64_t avg = a.seg.pairs / a.seg.E;
-    if (avg > 160) return launch_bm<256, 2, 2>(a, k, gated, stream);
+    if (avg > 160) return launch_wide(a, k, gated, stream);
     if (avg > 40) return launch_bm<128, 2, 3>(a, k, gated, stream);
     return launch_bm<32, 1, 2>(a, k, gated, stream);
 }

@@ -38,8 +38,6 @@ struct WgradK {
     int bf16_out;
 };
 
-__device__ __forceinline__ int granule_of(int r) { return (r & 3) | ((r >> 3 & 1) << 2); }
-
 template <bool FP8, bool BIAS>
 __global__ __launch_bounds__(512, 2) void expert_wgrad_kernel(WgradK a) {
     __shared__ __align__(1024) uint8_t lds[2 * kStage];
