@@ -560,10 +560,10 @@ int ep_expert_linear(const void *x, int x_dtype, const uint8_t *x_scales, const 
     if ((fp8 && transposed) || n > EP_MAX_HIDDEN || k > EP_MAX_HIDDEN) return EP_ERR_UNSUPPORTED;
     if ((int64_t)n * k * (fp8 ? 1 : 2) >= ((int64_t)1 << 31)) return EP_ERR_UNSUPPORTED;
     if (a.seg.pairs == 0 || num_rows == 0) return EP_OK;
-    if (!x || !aligned16(x) || !w || !aligned16(w) || !out || !aligned8(out))
+    if (!x || !aligned16(x) || !w || !aligned16(w) || !out || !aligned16(out))
         return EP_ERR_INVALID_ARG;
     if (fp8 && (!x_scales || !w_scales)) return EP_ERR_INVALID_ARG;
-    if (!aligned8(bias) || !aligned8(residual) || !aligned4(ckpt)) return EP_ERR_INVALID_ARG;
+    if (!aligned16(bias) || !aligned16(residual) || !aligned8(ckpt)) return EP_ERR_INVALID_ARG;
     a.x = x;
     a.x_scales = x_scales;
     a.w = w;

@@ -78,117 +78,140 @@ __device__ __forceinline__ ep_f32x4 mfma_fp8(const ep_u32x4 *a, const ep_u32x4 *
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, c, 0, 0, SB, sa, SB, sb);
 }
 
-// One 32-channel group of pre-activations (a lane's 8 of a row, the other 24 in
-// the lanes 16, 32 and 48 away) to e4m3 codes under a power of two: the format
-// of ep_cast_fp8 with UE8M0 scales, taken from the fp32 sums.
-__device__ __forceinline__ void checkpoint_group(const float *z, bool valid, int q, uint8_t *codes,
-                                                 uint8_t *scale) {
-    float m = 0.0f;
-    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(z[i]));
-    m = fmaxf(m, __shfl_xor(m, 16));
-    m = fmaxf(m, __shfl_xor(m, 32));
-    m = fminf(m, 3.0e38f);
-    const uint32_t e = ue8m0_of(pow2_ceil(scale_of(m)));
-    const float inv = __uint_as_float((254u - e) << 23);
-    const uint32_t c0 = pack4_e4m3(z[0] * inv, z[1] * inv, z[2] * inv, z[3] * inv);
-    const uint32_t c1 = pack4_e4m3(z[4] * inv, z[5] * inv, z[6] * inv, z[7] * inv);
-    if (valid) {
-        *(uint32_t *)(codes + 4 * q) = c0;
-        *(uint32_t *)(codes + 16 + 4 * q) = c1;
-        if (q == 0) *scale = (uint8_t)e;
-    }
-}
+// Bias, checkpoint, activation, residual and output of a wave's accumulators: NT
+// tiles of 16 columns of z (gated: the first half gates, the second their ups)
+// by MT of 16 rows, from row `first` of the segment, `live_rows` of them there;
+// c0 is the first column of out.  Accumulator j of tile (t, i) is column 16 t + 4
+// q + j, row 16 i + lane % 16.  The sums go through the wave's part of the LDS in
+// batches of BT row tiles, fp32, 16-byte chunk c of row r in place c ^ (r & 15),
+// and come back as 8 consecutive columns of one row per lane: the arithmetic is
+// a short loop over rows (unrolled over the registers it would not fit the
+// instruction cache), and residual, output and codes move in whole lines.
+// The residual of the first batch may be on its way since before the product.
+template <int NT, int BT, bool GATED>
+struct Output {
+    static constexpr int COLS = NT * 16, OUT = GATED ? COLS / 2 : COLS;
+    static constexpr int LANES = OUT / 8;              // lanes of a row
+    static constexpr int RPI = 64 / LANES;             // rows of an iteration
+    static constexpr int IT = BT * 16 / RPI;           // iterations of a batch
+    ep_u32x4 res[IT];
 
-// Bias, checkpoint, activation, residual and output of a wave's accumulators:
-// NG groups of 32 columns of z, group g from column c[g] (gated: the first half
-// of the groups are gates, the second their ups), by MT * 16 rows from `first`
-// of the segment, `live_rows` of them there.  Accumulator j of tile 2 g + h is
-// column 16 h + 4 q + j of group g, row lane % 16 of its row tile.
-template <int KIND, int NG, int MT, bool GATED>
-__device__ __forceinline__ void epilogue_of(const LinearK &a, const TileAt &at, int first,
-                                            int live_rows, const int *c, ep_f32x4 (*acc)[MT]) {
-    constexpr int OG = GATED ? NG / 2 : NG, NK = GATED ? 2 : 1;
-    const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
-    const int N = a.n;
-    const int64_t row0 = (int64_t)at.row0 + first + l16;
-    // one group's (gated: two groups') pre-activations at a time
-    each<OG>([&](auto gg) __attribute__((always_inline)) {
-        constexpr int g = decltype(gg)::value;
-        float b[NK][8];
+    __device__ __forceinline__ void load(const LinearK &a, const TileAt &at, int first,
+                                         int live_rows, int c0, int batch) {
+        if (!a.residual) return;
+        const int lane = threadIdx.x & 63, lc = lane % LANES, lr = lane / LANES;
+        const uint16_t *p = a.residual + ((int64_t)at.row0 + first + lr) * a.m + c0 + lc * 8;
 #pragma unroll
-        for (int k = 0; k < NK; ++k)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                ep_u32x2 v = {0, 0};
-                const int col = c[g + k * OG] + 16 * h + 4 * q;
-                if (a.bias && col < N) v = *(const ep_u32x2 *)(a.bias + (int64_t)at.e * N + col);
-                b[k][4 * h] = bf16_lo(v.x);
-                b[k][4 * h + 1] = bf16_hi(v.x);
-                b[k][4 * h + 2] = bf16_lo(v.y);
-                b[k][4 * h + 3] = bf16_hi(v.y);
-            }
-        // the residual of all row tiles at once: one wait
-        ep_u32x2 res[MT][2];
-        if (a.residual) {
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int col = c[g] + 16 * h + 4 * q;
-                    res[i][h] = ep_u32x2{0, 0};
-                    if (i * 16 + l16 < live_rows && col < a.m)
-                        res[i][h] = *(const ep_u32x2 *)(a.residual + (row0 + i * 16) * a.m + col);
-                }
+        for (int i = 0; i < IT; ++i) {
+            const int r = batch * BT * 16 + i * RPI;
+            res[i] = ep_u32x4{0, 0, 0, 0};
+            if (c0 + lc * 8 < a.m && r + lr < live_rows) res[i] = *(const ep_u32x4 *)(p + (int64_t)r * a.m);
         }
-        each<MT>([&](auto ii) __attribute__((always_inline)) {
-            constexpr int i = decltype(ii)::value;
-            const bool live = i * 16 + l16 < live_rows;
-            const int64_t row = row0 + i * 16;
+    }
+};
+
+template <int KIND, int NT, int MT, int BT, bool GATED>
+__device__ __forceinline__ void epilogue_of(const LinearK &a, const TileAt &at, uint8_t *lds,
+                                            int first, int live_rows, int c0,
+                                            ep_f32x4 (*acc)[MT], Output<NT, BT, GATED> &now) {
+    typedef Output<NT, BT, GATED> O;
+    constexpr int COLS = O::COLS, OUT = O::OUT, LANES = O::LANES, RPI = O::RPI, IT = O::IT;
+    constexpr int NK = GATED ? 2 : 1;
+    const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
+    const int lc = lane % LANES, lr = lane / LANES;
+    const int N = a.n, m = a.m;
+    const int col = c0 + lc * 8;
+    const bool there = col < m;                        // n is a multiple of 8 (m too)
+    const int64_t row0 = (int64_t)at.row0 + first + lr;
+    float b[NK][8];
+#pragma unroll
+    for (int k = 0; k < NK; ++k) {
+        ep_u32x4 v = {0, 0, 0, 0};
+        if (a.bias && there) v = *(const ep_u32x4 *)(a.bias + (int64_t)at.e * N + k * m + col);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            b[k][2 * j] = bf16_lo(v[j]);
+            b[k][2 * j + 1] = bf16_hi(v[j]);
+        }
+    }
+    each<MT / BT>([&](auto bb) __attribute__((always_inline)) {
+        constexpr int batch = decltype(bb)::value;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < BT; ++i) {
+                ep_f32x4 s = acc[t][batch * BT + i];
+                pin(s);
+                *(ep_f32x4 *)(lds + (i * 16 + l16) * COLS * 4 + ((t * 4 + q) ^ l16) * 16) = s;
+            }
+        O next;
+        if (batch + 1 < MT / BT) next.load(a, at, first, live_rows, c0, batch + 1);
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            const int at_row = batch * BT * 16 + i * RPI;
+            const int r = i * RPI + lr;
+            const bool live = there && at_row + lr < live_rows;
+            const int64_t row = row0 + at_row;
             float z[NK][8];
 #pragma unroll
             for (int k = 0; k < NK; ++k) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    ep_f32x4 s = acc[2 * (g + k * OG) + h][i];
-                    pin(s);
+                    const int c = k * (OUT / 4) + lc * 2 + h;
+                    const ep_f32x4 v = *(const ep_f32x4 *)(lds + r * COLS * 4 + (c ^ (r & 15)) * 16);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) z[k][4 * h + j] = s[j] + b[k][4 * h + j];
+                    for (int j = 0; j < 4; ++j) z[k][4 * h + j] = v[j] + b[k][4 * h + j];
                 }
-                // n is a multiple of the group, so its 32 channels are there or none is
-                const int from = c[g + k * OG];
-                if (a.ckpt)
-                    checkpoint_group(z[k], live && c[g] + 32 <= a.m, q, a.ckpt + row * N + from,
-                                     a.ckpt_scales + row * (N >> 5) + (from >> 5));
+                if (a.ckpt) {
+                    // 32 channels, four lanes, to e4m3 codes under a power of
+                    // two: the format of ep_cast_fp8 with UE8M0 scales, taken
+                    // from the fp32 sums.  (n is a multiple of the group: its
+                    // channels are all there or none is.)
+                    float big = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) big = fmaxf(big, fabsf(z[k][j]));
+                    big = fminf(group_max(big, 4), 3.0e38f);
+                    const uint32_t e = ue8m0_of(pow2_ceil(scale_of(big)));
+                    const float inv = __uint_as_float((254u - e) << 23);
+                    ep_u32x2 codes;
+                    codes.x = pack4_e4m3(z[k][0] * inv, z[k][1] * inv, z[k][2] * inv, z[k][3] * inv);
+                    codes.y = pack4_e4m3(z[k][4] * inv, z[k][5] * inv, z[k][6] * inv, z[k][7] * inv);
+                    if (live) {
+                        const int64_t o = row * N + k * m + col;
+                        *(ep_u32x2 *)(a.ckpt + o) = codes;
+                        if ((lane & 3) == 0) a.ckpt_scales[o >> 5] = (uint8_t)e;
+                    }
+                }
             }
+            float y[8];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float y[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    y[j] = act_value<KIND>(z[0][4 * h + j]);
-                    if (GATED) y[j] *= z[NK - 1][4 * h + j];
-                }
-                const int col = c[g] + 16 * h + 4 * q;
-                if (a.residual) {
-                    y[0] += bf16_lo(res[i][h].x); y[1] += bf16_hi(res[i][h].x);
-                    y[2] += bf16_lo(res[i][h].y); y[3] += bf16_hi(res[i][h].y);
-                }
-                ep_u32x2 v;
-                v.x = pack_bf16(y[0], y[1]);
-                v.y = pack_bf16(y[2], y[3]);
-                if (live && col < a.m) *(ep_u32x2 *)(a.out + row * a.m + col) = v;
+            for (int j = 0; j < 8; ++j) {
+                y[j] = act_value<KIND>(z[0][j]);
+                if (GATED) y[j] *= z[NK - 1][j];
             }
-        });
-        __builtin_amdgcn_sched_barrier(0);
+            if (a.residual) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const uint32_t v = now.res[i][j >> 1];
+                    y[j] += (j & 1) ? bf16_hi(v) : bf16_lo(v);
+                }
+            }
+            if (live)
+                *(ep_u32x4 *)(a.out + row * m + col) =
+                    ep_u32x4{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]),
+                             pack_bf16(y[6], y[7])};
+        }
+        if (batch + 1 < MT / BT) now = next;
     });
 }
 
-template <int NG, int MT, bool GATED>
-__device__ __forceinline__ void epilogue(const LinearK &a, const TileAt &at, int first,
-                                         int live_rows, const int *c, ep_f32x4 (*acc)[MT]) {
-    if (a.kind == 1) epilogue_of<1, NG, MT, GATED>(a, at, first, live_rows, c, acc);
-    else if (a.kind == 2) epilogue_of<2, NG, MT, GATED>(a, at, first, live_rows, c, acc);
-    else if (!GATED) epilogue_of<0, NG, MT, GATED>(a, at, first, live_rows, c, acc);
+template <int NT, int MT, int BT, bool GATED>
+__device__ __forceinline__ void epilogue(const LinearK &a, const TileAt &at, uint8_t *lds, int first,
+                                         int live_rows, int c0, ep_f32x4 (*acc)[MT],
+                                         Output<NT, BT, GATED> &o) {
+    if (a.kind == 1) epilogue_of<1, NT, MT, BT, GATED>(a, at, lds, first, live_rows, c0, acc, o);
+    else if (a.kind == 2) epilogue_of<2, NT, MT, BT, GATED>(a, at, lds, first, live_rows, c0, acc, o);
+    else if (!GATED) epilogue_of<0, NT, MT, BT, GATED>(a, at, lds, first, live_rows, c0, acc, o);
 }
 
 // Tiles of up to 128 rows: bound by reading the weights unless several segments'
@@ -349,8 +372,11 @@ __global__ __launch_bounds__(256 * WM, 2) void expert_linear_kernel(LinearK a) {
     } else {
         for (int s = 0; s < steps; ++s) step(s, std::integral_constant<int, 0>{});
     }
-    const int cols[2] = {column(wn * 64), column(wn * 64 + 32)};
-    epilogue<2, MT, GATED>(a, at, row0 + wm * MT * 16, rows - wm * MT * 16, cols, acc);
+    barrier_only();                                    // the stages are the epilogue's now
+    Output<4, MT, GATED> o;
+    o.load(a, at, row0 + wm * MT * 16, rows - wm * MT * 16, column(wn * 64), 0);
+    epilogue<4, MT, MT, GATED>(a, at, lds + wave * MT * 4096, row0 + wm * MT * 16,
+                               rows - wm * MT * 16, column(wn * 64), acc, o);
 }
 
 // Tiles of 256 rows, bound by the matrix instructions.  Four waves of 128 x 128:
@@ -502,6 +528,8 @@ __global__ __launch_bounds__(256, 1) void expert_linear_wide_kernel(LinearK a) {
         __builtin_amdgcn_sched_barrier(0);
     };
 
+    Output<8, 4, GATED> o;
+    o.load(a, at, row0 + wm * 128, rows - wm * 128, column(wn, 0), 0);
     for (int s = 0; s < 2; ++s) {
         each<4>([&](auto j) { copy_x(s, s, 0, j); });
         each<4>([&](auto j) { copy_w(s, s, 0, j); });
@@ -571,8 +599,9 @@ __global__ __launch_bounds__(256, 1) void expert_linear_wide_kernel(LinearK a) {
             d = mfma_bf16(wf[decltype(tw)::value][b][h], xf[decltype(tx)::value][c][h], d);
         }); }); });
     }
-    const int cols[4] = {column(wn, 0), column(wn, 0) + 32, column(wn, 1), column(wn, 1) + 32};
-    epilogue<4, 8, GATED>(a, at, row0 + wm * 128, rows - wm * 128, cols, acc);
+    barrier_only();                                    // the stages are the epilogue's now
+    epilogue<8, 8, 4, GATED>(a, at, lds + wave * 32768, row0 + wm * 128, rows - wm * 128,
+                             column(wn, 0), acc, o);
 }
 
 // Workgroups for row tiles of BM rows: each segment's last one may be partial.

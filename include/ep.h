@@ -451,12 +451,12 @@ int ep_combine_logfmt(const void *payload, int32_t hidden, int64_t num_y_rows,
  *              rows), else NULL.
  *   n          columns of z: a multiple of 8; of 16 for a gated activation, of
  *              32 (64 gated) with a checkpoint.
- *   bias       device bf16 [E, n] or NULL, 8-byte aligned.
+ *   bias       device bf16 [E, n] or NULL, 16-byte aligned.
  *   act        EP_ACT_*.
- *   residual   device bf16 [num_rows, m] or NULL, 8-byte aligned; m = n, or
+ *   residual   device bf16 [num_rows, m] or NULL, 16-byte aligned; m = n, or
  *              n/2 for a gated activation.
- *   out        device bf16 [num_rows, m], 8-byte aligned.
- *   ckpt, ckpt_scales  device uint8 [num_rows, n] (4-byte aligned) and
+ *   out        device bf16 [num_rows, m], 16-byte aligned.
+ *   ckpt, ckpt_scales  device uint8 [num_rows, n] (8-byte aligned) and
  *              [num_rows, n/32], or both NULL: z kept in 8 bits for
  *              ep_expert_activation_backward: e4m3 codes and UE8M0 scales per
  *              32 channels, the format of ep_cast_fp8, taken from the fp32 z.
