@@ -387,16 +387,14 @@ __global__ __launch_bounds__(256 * WM, 2) void expert_linear_kernel(LinearK a) {
 // Two stages of 64 KB fill the LDS, so what hides the copies' latency is how
 // early a piece of a stage is given back: a stage is four regions (the waves'
 // first and second 64 weight rows, first and second 64 x rows), each read to
-// registers in one phase and copied anew from the next, seven of the eight
-// phases of two steps before it is read again.  A phase is a quarter of a step:
-// the matrix instructions of one weight region and one x region, with the reads
-// of the next region and the copies placed among them (one wave runs on a SIMD:
-// nothing else would fill the gaps), then the wait and the barrier:
-//   phase   multiplies   reads (step)   copies (step)
-//     0       W0 X0        W1 (s)        W0 (s + 2)
-//     1       W1 X0        X1 (s)        W1 (s + 2)
-//     2       W0 X1        X0 (s + 1)    X1 (s + 2)
-//     3       W1 X1        W0 (s + 1)    X0 (s + 3)
+// registers a little before it is multiplied and copied anew in the phase after
+// that.  A phase is half a step; the reads and copies are placed among its
+// matrix instructions (one wave runs on a SIMD: nothing else would fill the
+// gaps), and the wait and the barrier between phases are what is left over:
+//   phase   multiplies       reads (step)              copies (step)
+//     A     W0 X0, W1 X0     W1 (s), X1 (s)            X0, W0 (s + 2)
+//     B     W0 X1, W1 X1     X0 (s + 1), W0 (s + 1)    W1, X1 (s + 2)
+// (Four phases with a barrier each measured 100 cycles more per barrier.)
 // Copies behind the last step go on from an empty buffer (they write zeros), so
 // that the number in flight, which the waits count, stays the same.  Channels
 // that do not fill a step are one more step after the loop.
@@ -507,23 +505,24 @@ __global__ __launch_bounds__(256, 1) void expert_linear_wide_kernel(LinearK a) {
             ws[i] = scales4(a.w_scales + ((int64_t)at.e * N + c) * groups, s, groups);
         }
     };
-    // One phase: `read(i)` and `copy(i)`, i = 0..3, placed among the matrix
-    // instructions; then the region the next phase reads has landed, and every
-    // wave has read the one this phase read.
-    auto phase = [&](int tw, int tx, auto sb, auto read, auto copy) {
+    // Half a phase: `read(i)` and `copy(i)`, i = 0..3, among the matrix instructions.
+    auto part = [&](int tw, int tx, auto sb, auto read, auto copy) {
         constexpr int n = FP8 ? 16 : 32;
-        each<n>([&](auto mm) {
+        each<n>([&](auto mm) __attribute__((always_inline)) {
             constexpr int m = decltype(mm)::value;
             constexpr int h = m / 16, b = m / 4 % 4, c = m % 4;
             ep_f32x4 &d = acc[tw * 4 + b][tx * 4 + c];
             if (FP8) d = mfma_fp8<decltype(sb)::value>(wf[tw][b], xf[tx][c], d, ws[tw * 4 + b], xs[tx * 4 + c]);
             else d = mfma_bf16(wf[tw][b][h], xf[tx][c][h], d);
-            // reads in the first half, copies spread over all
-            if constexpr (m % (n / 8) == 0 && m < n / 2) read(m / (n / 8));
+            if constexpr (m % (n / 4) == 0) read(m / (n / 4));
             if constexpr (m % (n / 4) == n / 8) copy(std::integral_constant<int, m / (n / 4)>{});
             __builtin_amdgcn_sched_barrier(0);
         });
-        dma_wait<24>();
+    };
+    // end of a phase: the regions the next one reads have landed, and every
+    // wave has read those this phase read
+    auto turn = [&]() {
+        dma_wait<16>();
         barrier_only();
         __builtin_amdgcn_sched_barrier(0);
     };
@@ -540,18 +539,16 @@ __global__ __launch_bounds__(256, 1) void expert_linear_wide_kernel(LinearK a) {
     barrier_only();
     each<4>([&](auto i) { read_x(0, 0, i); });
     each<4>([&](auto i) { read_w(0, 0, i); });
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    barrier_only();
-    each<4>([&](auto j) { copy_x(2, 0, 0, j); });
-    dma_wait<24>();
-    barrier_only();
+    turn();
 
     auto step = [&](int s, auto stage, auto sb) {
         constexpr int st = decltype(stage)::value;
-        phase(0, 0, sb, [&](int i) { read_w(st, 1, i); }, [&](auto j) { copy_w(s + 2, st, 0, j); });
-        phase(1, 0, sb, [&](int i) { read_x(st, 1, i); }, [&](auto j) { copy_w(s + 2, st, 1, j); });
-        phase(0, 1, sb, [&](int i) { read_x(st ^ 1, 0, i); }, [&](auto j) { copy_x(s + 2, st, 1, j); });
-        phase(1, 1, sb, [&](int i) { read_w(st ^ 1, 0, i); }, [&](auto j) { copy_x(s + 3, st ^ 1, 0, j); });
+        part(0, 0, sb, [&](int i) { read_w(st, 1, i); }, [&](auto j) { copy_x(s + 2, st, 0, j); });
+        part(1, 0, sb, [&](int i) { read_x(st, 1, i); }, [&](auto j) { copy_w(s + 2, st, 0, j); });
+        turn();
+        part(0, 1, sb, [&](int i) { read_x(st ^ 1, 0, i); }, [&](auto j) { copy_w(s + 2, st, 1, j); });
+        part(1, 1, sb, [&](int i) { read_w(st ^ 1, 0, i); }, [&](auto j) { copy_x(s + 2, st, 1, j); });
+        turn();
     };
     constexpr std::integral_constant<int, 0> c0{};
     constexpr std::integral_constant<int, 1> c1{};
