@@ -522,6 +522,9 @@ int ep_combine_logfmt(const void *payload, int32_t hidden, int64_t num_y_rows,
 
 static bool aligned8(const void *p) { return ((uintptr_t)p & 7u) == 0; }
 
+// Bytes the kernels address with 32-bit offsets (one expert's weights, ...).
+constexpr int64_t kMaxBuffer = ((int64_t)1 << 31) - 4096;
+
 static bool is_act(int act) { return act >= EP_ACT_NONE && act <= EP_ACT_GEGLU; }
 
 // Host checks the segmented expert operators share; fills the segments.
@@ -558,7 +561,7 @@ int ep_expert_linear(const void *x, int x_dtype, const uint8_t *x_scales, const 
     if ((ckpt == nullptr) != (ckpt_scales == nullptr)) return EP_ERR_INVALID_ARG;
     if (ckpt && n % (ep::act_gated(act) ? 64 : 32) != 0) return EP_ERR_INVALID_ARG;
     if ((fp8 && transposed) || n > EP_MAX_HIDDEN || k > EP_MAX_HIDDEN) return EP_ERR_UNSUPPORTED;
-    if ((int64_t)n * k * (fp8 ? 1 : 2) >= ((int64_t)1 << 31)) return EP_ERR_UNSUPPORTED;
+    if ((int64_t)n * k * (fp8 ? 1 : 2) >= kMaxBuffer) return EP_ERR_UNSUPPORTED;
     if (a.seg.pairs == 0 || num_rows == 0) return EP_OK;
     if (!x || !aligned16(x) || !w || !aligned16(w) || !out || !aligned16(out))
         return EP_ERR_INVALID_ARG;
@@ -658,7 +661,7 @@ size_t ep_moe_decode_workspace_bytes(int32_t num_tokens, int32_t num_topk, int32
     if (num_tokens < 0 || num_topk < 1 || inter < 1 || inter > EP_MAX_HIDDEN) return 0;
     const int64_t pairs = (int64_t)num_tokens * num_topk;
     if (pairs > EP_MAX_DECODE_PAIRS) return 0;
-    return ((size_t)pairs * inter * 2 + 255) / 256 * 256 + 256;   // h, never empty
+    return ((size_t)pairs * inter * 4 + 255) / 256 * 256 + 256;   // h in two parts, never empty
 }
 
 int ep_moe_decode(const void *x, const int64_t *topk_idx, const float *topk_weights,
@@ -677,6 +680,11 @@ int ep_moe_decode(const void *x, const int64_t *topk_idx, const float *topk_weig
     const int64_t pairs = (int64_t)num_tokens * num_topk;
     if (pairs > EP_MAX_DECODE_PAIRS || num_experts > EP_MAX_EXPERTS || hidden > EP_MAX_HIDDEN ||
         inter > EP_MAX_HIDDEN)
+        return EP_ERR_UNSUPPORTED;
+    // one expert's weights, and the rows, within 32-bit offsets
+    const int64_t rows1 = (int64_t)inter * (ep::act_gated(act) ? 2 : 1);
+    if (rows1 * hidden * (fp8 ? 1 : 2) >= kMaxBuffer || (int64_t)num_tokens * hidden * 2 >= kMaxBuffer ||
+        pairs * inter * 4 >= kMaxBuffer)
         return EP_ERR_UNSUPPORTED;
     if (num_tokens == 0) return EP_OK;
     if (!x || !aligned16(x) || !topk_idx || !w1 || !aligned16(w1) || !w2 || !aligned16(w2) ||

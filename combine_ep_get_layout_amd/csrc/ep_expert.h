@@ -93,7 +93,7 @@ struct MoeDecodeArgs {
     const uint8_t *w1_scales, *w2_scales;
     const void *bias1, *bias2;   // bf16 [E, n1], [E, H] or NULL
     const void *res0, *res1;     // bf16 [T, H] or NULL
-    void *h;                     // workspace: bf16 [T*K, I]
+    void *h;                     // workspace: bf16 [T*K, 2, I], high and low parts
     void *out;                   // bf16 [T, H]
     int32_t *status;             // or NULL
     int T, K, E, H, I, kind;

@@ -1,5 +1,5 @@
 // A whole mixture-of-experts layer for a few tokens, in two kernels:
-//   h[t,k] = act(W1[e] x[t] + b1[e])                       (rounded to bf16)
+//   h[t,k] = act(W1[e] x[t] + b1[e])                       (16 significant bits)
 //   out[t] = res0 + res1 + sum_k w[t,k] (W2[e] h[t,k] + b2[e]),  e = topk_idx[t,k]
 // There is no layout and no permutation: the pairs of an expert are found in
 // topk_idx by every workgroup that needs them.
@@ -13,8 +13,10 @@
 // First kernel: a workgroup takes one expert and 16 columns of h (16 gate and
 // 16 up rows of W1); its four waves split the sum over the hidden channels and
 // add up in LDS in wave order.
-// Second kernel: a workgroup takes 16 channels of the output and all pairs:
-// its waves take the chosen experts in turn, every pair's 16 sums go to LDS in
+// Second kernel: a workgroup takes 32 channels of the output and all pairs (h is
+// read once per workgroup; 16 channels read it twice as often and were slower
+// for many pairs):
+// its waves take the chosen experts in turn, every pair's 32 sums go to LDS in
 // fp32, and the tokens' weighted sums are formed from there in ascending k, as
 // ep_combine forms them: no atomics, no rounding between the two, and a
 // token's result does not depend on the other tokens of the batch.
@@ -32,57 +34,110 @@ struct DecodeK {
     int by_pair;      // first kernel: a workgroup's expert is that of pair blockIdx.y
 };
 
-// One matrix-instruction operand of 32 channels: 8 consecutive bf16 per lane.
-// Row pointers are per lane; channels at or past n are zeros.
-template <bool FP8>
-struct Weights;
+typedef __amdgpu_buffer_rsrc_t Buffer;
 
-template <>
-struct Weights<false> {
-    const uint16_t *row;
-    __device__ __forceinline__ Weights(const void *w, const uint8_t *, int64_t r, int n)
-        : row((const uint16_t *)w + r * n) {}
-    // channels c + 32 j + 8 q .. + 7 for j = 0..3, c a multiple of 128
-    __device__ __forceinline__ void load(int c, int q, int n, ep_u32x4 *v, float *) const {
+// Reads past `bytes` return zeros; no buffer here has kOutOfRange bytes.
+__device__ __forceinline__ Buffer buffer(const void *p, int64_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc((void *)p, 0, (int)bytes, 0x00020000);
+}
+
+// 256 bytes of the rows of CT weight tiles (16 rows each), and the same channels
+// of up to 16 token rows, as they come from memory: a lane has 4 pieces of 16
+// bytes of a weight row, 8 consecutive bf16 or 16 fp8 channels (with two scale
+// bytes); the token rows' pieces follow the weights' order.  The weights pass
+// the caches in the ordinary way: the 16 rows x 64 bytes of one load are half
+// lines, and with the non-temporal hint the halves were fetched apart (5.1
+// against 5.9 TB/s).
+template <bool FP8, int CT>
+struct Chunk {
+    static constexpr int kChannels = FP8 ? 256 : 128;
+    static constexpr int kX = FP8 ? 8 : 4;
+    ep_u32x4 w[CT][4];
+    uint32_t scale[CT][FP8 ? 2 : 1];
+
+    // wv, sv, xv: this lane's byte offsets of its rows (kOutOfRange: zeros)
+    __device__ __forceinline__ void load_w(Buffer wb, const uint32_t *wv, Buffer sb, const uint32_t *sv,
+                                           int chunk, int channels) {
+        const int q = (threadIdx.x & 63) >> 4;
+        const int c = chunk * kChannels;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int at = c + j * 32 + q * 8;
-            v[j] = at < n ? load_nt((const ep_u32x4 *)(row + at)) : ep_u32x4{0, 0, 0, 0};
+        for (int t = 0; t < CT; ++t)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t o = wv[t] + q * 16 + j * 64;
+                if (FP8 ? c + j * 64 >= channels : c + j * 32 + q * 8 >= channels) o = kOutOfRange;
+                w[t][j] = __builtin_bit_cast(ep_u32x4, __builtin_amdgcn_raw_buffer_load_b128(wb, o, chunk * 256, 0));
+            }
+        if (FP8) {
+#pragma unroll
+            for (int t = 0; t < CT; ++t)
+#pragma unroll
+                for (int g = 0; g < 2; ++g)
+                    scale[t][FP8 ? g : 0] = __builtin_amdgcn_raw_buffer_load_b8(
+                        sb, c + g * 128 < channels ? sv[t] + g : kOutOfRange, chunk * 2, 0);
         }
     }
-    static __device__ __forceinline__ ep_bf16x8 operand(const ep_u32x4 *v, float, int j) {
-        return __builtin_bit_cast(ep_bf16x8, v[j]);
+    static __device__ __forceinline__ void load_x(Buffer xb, uint32_t xv, uint32_t part, int chunk,
+                                                  int channels, ep_u32x4 *x) {
+        const int q = (threadIdx.x & 63) >> 4;
+#pragma unroll
+        for (int j = 0; j < kX; ++j) {
+            // first of the 8 channels
+            const int c = chunk * kChannels + (FP8 ? (j >> 1) * 64 + q * 16 + (j & 1) * 8 : j * 32 + q * 8);
+            const uint32_t o = xv == kOutOfRange || c >= channels ? kOutOfRange : xv + c * 2;
+            x[j] = __builtin_bit_cast(ep_u32x4, __builtin_amdgcn_raw_buffer_load_b128(xb, o, part, 0));
+        }
     }
-    // first channel of operand j's 8
-    static __device__ __forceinline__ int channel(int c, int j, int q) { return c + j * 32 + q * 8; }
-    static constexpr int kLoads = 4;
+    template <int PARTS>
+    __device__ __forceinline__ void multiply(const ep_u32x4 (*x)[kX], ep_f32x4 *acc) const {
+#pragma unroll
+        for (int j = 0; j < kX; ++j)
+#pragma unroll
+            for (int t = 0; t < CT; ++t) {
+                ep_u32x4 v;
+                if (FP8) {
+                    const float s = ue8m0_value(scale[t][FP8 ? j >> 2 : 0]);
+                    const uint32_t lo = w[t][j >> 1][(j & 1) * 2], hi = w[t][j >> 1][(j & 1) * 2 + 1];
+                    v.x = fp8_pair_bf16<false>(lo, s);
+                    v.y = fp8_pair_bf16<true>(lo, s);
+                    v.z = fp8_pair_bf16<false>(hi, s);
+                    v.w = fp8_pair_bf16<true>(hi, s);
+                } else {
+                    v = w[t][FP8 ? 0 : j];
+                }
+#pragma unroll
+                for (int p = 0; p < PARTS; ++p) acc[t] = mfma_bf16(v, x[p][j], acc[t]);
+            }
+    }
 };
 
-template <>
-struct Weights<true> {
-    const uint8_t *row, *scale;
-    __device__ __forceinline__ Weights(const void *w, const uint8_t *s, int64_t r, int n)
-        : row((const uint8_t *)w + r * n), scale(s + r * (n / kFp8Group)) {}
-    // channels c + 64 i + 16 q .. + 15 for i = 0, 1
-    __device__ __forceinline__ void load(int c, int q, int n, ep_u32x4 *v, float *s) const {
-        v[0] = load_nt((const ep_u32x4 *)(row + c + q * 16));
-        v[1] = load_nt((const ep_u32x4 *)(row + c + 64 + q * 16));
-        *s = ue8m0_value(scale[c / kFp8Group]);
+// acc[t] += weights x rows over chunks [from, to): a chunk's token rows (from
+// the caches) are asked for just before the next chunk's weights (from memory),
+// so waiting for them leaves the weights in flight.  `a` holds the weights of
+// chunk `from` already.
+// PARTS 2: the token rows are sums of two bf16 rows, the second `second` bytes
+// behind the first.
+template <int PARTS, bool FP8, int CT>
+__device__ __forceinline__ void sweep(Chunk<FP8, CT> &a, Buffer wb, const uint32_t *wv, Buffer sb,
+                                      const uint32_t *sv, Buffer xb, uint32_t xv, uint32_t second,
+                                      int from, int to, int channels, ep_f32x4 *acc) {
+    typedef Chunk<FP8, CT> C;
+    C b;
+    ep_u32x4 x[PARTS][C::kX];
+    auto load_x = [&](int c) {
+#pragma unroll
+        for (int p = 0; p < PARTS; ++p) C::load_x(xb, xv, p * second, c, channels, x[p]);
+    };
+    for (int c = from; c < to; c += 2) {
+        load_x(c);
+        if (c + 1 < to) b.load_w(wb, wv, sb, sv, c + 1, channels);
+        a.template multiply<PARTS>(x, acc);
+        if (c + 1 >= to) break;
+        load_x(c + 1);
+        if (c + 2 < to) a.load_w(wb, wv, sb, sv, c + 2, channels);
+        b.template multiply<PARTS>(x, acc);
     }
-    static __device__ __forceinline__ ep_bf16x8 operand(const ep_u32x4 *v, float s, int j) {
-        const uint32_t lo = v[j >> 1][(j & 1) * 2], hi = v[j >> 1][(j & 1) * 2 + 1];
-        ep_u32x4 r;
-        r.x = fp8_pair_bf16<false>(lo, s);
-        r.y = fp8_pair_bf16<true>(lo, s);
-        r.z = fp8_pair_bf16<false>(hi, s);
-        r.w = fp8_pair_bf16<true>(hi, s);
-        return __builtin_bit_cast(ep_bf16x8, r);
-    }
-    static __device__ __forceinline__ int channel(int c, int j, int q) {
-        return c + (j >> 1) * 64 + q * 16 + (j & 1) * 8;
-    }
-    static constexpr int kLoads = 2;
-};
+}
 
 // The pairs of expert e, ascending, to list[]; returns how many.  `red` is LDS
 // of 8 ints; the whole workgroup calls this.
@@ -108,78 +163,83 @@ __device__ int pairs_of(const int64_t *topk_idx, int pairs, int64_t e, int16_t *
     return count;
 }
 
+constexpr int kUpCols = 16;       // columns of h of a workgroup of the first kernel
+
 template <bool FP8, bool GATED>
 __global__ __launch_bounds__(256) void moe_decode_up_kernel(DecodeK k) {
     const MoeDecodeArgs &a = k.a;
+    constexpr int CT = (GATED ? 2 : 1) * kUpCols / 16;
     __shared__ int16_t list[kMaxPairs];
     __shared__ int red[8];
-    __shared__ float part[4][GATED ? 2 : 1][16][17];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    __shared__ float part[4][CT][16][17];
+    const int tid = threadIdx.x, lane = tid & 63, wave = wave_uniform(tid >> 6);
     const int l16 = lane & 15, q = lane >> 4;
-    const int64_t e = k.by_pair ? a.topk_idx[blockIdx.y] : (int64_t)blockIdx.y;
+    const int e = k.by_pair ? (int)a.topk_idx[blockIdx.y] : (int)blockIdx.y;
+    const bool known = !k.by_pair || (a.topk_idx[blockIdx.y] >= 0 && a.topk_idx[blockIdx.y] < a.E);
     if (a.status && blockIdx.x == 0 && blockIdx.y == 0) {
         bool bad = false;
         for (int p = tid; p < k.pairs; p += 256) bad |= a.topk_idx[p] < -1 || a.topk_idx[p] >= a.E;
         if (bad) atomicOr(a.status, kDevBadExpert);
     }
-    if (e < 0 || e >= a.E) return;
-    const int count = pairs_of<256>(a.topk_idx, k.pairs, e, list, red);
-    // by pair: only the expert's first pair computes
-    if (count == 0 || (k.by_pair && list[0] != (int)blockIdx.y)) return;
+    if (!known) return;
 
     const int I = a.I, H = a.H, n1 = GATED ? 2 * I : I;
-    const int col0 = blockIdx.x * 16;
-    const int wcol = min(col0 + l16, I - 1);
-    const Weights<FP8> wg(a.w1, a.w1_scales, e * n1 + wcol, H);
-    const Weights<FP8> wu(a.w1, a.w1_scales, e * n1 + (GATED ? I : 0) + wcol, H);
-    // the waves take the 128-channel steps in turn
+    const int col0 = blockIdx.x * kUpCols;
+    const int64_t w_bytes = (int64_t)n1 * H * (FP8 ? 1 : 2);
+    const Buffer wb = buffer((const uint8_t *)a.w1 + e * w_bytes, w_bytes);
+    const int groups = H / kFp8Group;
+    const Buffer sb = buffer(a.w1_scales + (FP8 ? (int64_t)e * n1 * groups : 0), FP8 ? (int64_t)n1 * groups : 0);
+    const Buffer xb = buffer(a.x, (int64_t)a.T * H * 2);
+    uint32_t wv[CT], sv[CT];
+#pragma unroll
+    for (int t = 0; t < CT; ++t) {
+        // gated: tiles of gates, then of their ups
+        const int col = col0 + (t % (kUpCols / 16)) * 16 + l16;
+        const int row = col + (t >= kUpCols / 16 ? I : 0);
+        wv[t] = col < I ? (uint32_t)row * H * (FP8 ? 1 : 2) : kOutOfRange - 1024;
+        sv[t] = col < I ? (uint32_t)row * groups : kOutOfRange - 16;
+    }
+    // the waves take equal runs of the row's chunks
+    const int chunks = (H + Chunk<FP8, CT>::kChannels - 1) / Chunk<FP8, CT>::kChannels;
+    const int from = chunks * wave / 4, to = chunks * (wave + 1) / 4;
+    // by pair, the first weights are on their way while the pairs are found
+    Chunk<FP8, CT> chunk;
+    if (k.by_pair) chunk.load_w(wb, wv, sb, sv, from, H);
+    const int count = wave_uniform(pairs_of<256>(a.topk_idx, k.pairs, e, list, red));
+    // by pair: only the expert's first pair computes
+    if (count == 0 || (k.by_pair && list[0] != (int)blockIdx.y)) return;
     for (int g0 = 0; g0 < count; g0 += 16) {
         const int live = min(16, count - g0);
-        const int pair = l16 < live ? list[g0 + l16] : 0;
-        const uint16_t *x = (const uint16_t *)a.x + (int64_t)(pair / a.K) * H;
-        ep_f32x4 acc_g = {0, 0, 0, 0}, acc_u = {0, 0, 0, 0};
-#pragma unroll 2
-        for (int c = wave * 128; c < H; c += 512) {
-            ep_u32x4 vg[4], vu[4];
-            float sg = 0.0f, su = 0.0f;
-            wg.load(c, q, H, vg, &sg);
-            if (GATED) wu.load(c, q, H, vu, &su);
-            ep_u32x4 xv[4];
+        const uint32_t xv = l16 < live ? (uint32_t)(list[g0 + l16] / a.K) * H * 2 : kOutOfRange;
+        ep_f32x4 acc[CT];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int at = Weights<FP8>::channel(c, j, q);
-                xv[j] = l16 < live && at < H ? *(const ep_u32x4 *)(x + at) : ep_u32x4{0, 0, 0, 0};
-            }
+        for (int t = 0; t < CT; ++t) acc[t] = ep_f32x4{0, 0, 0, 0};
+        if (!k.by_pair || g0 > 0) chunk.load_w(wb, wv, sb, sv, from, H);
+        sweep<1, FP8, CT>(chunk, wb, wv, sb, sv, xb, xv, 0, from, to, H, acc);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const ep_bf16x8 b = __builtin_bit_cast(ep_bf16x8, xv[j]);
-                acc_g = __builtin_amdgcn_mfma_f32_16x16x32_bf16(Weights<FP8>::operand(vg, sg, j), b, acc_g, 0, 0, 0);
-                if (GATED)
-                    acc_u = __builtin_amdgcn_mfma_f32_16x16x32_bf16(Weights<FP8>::operand(vu, su, j), b, acc_u, 0, 0, 0);
-            }
-        }
-        pin(acc_g);
-        pin(acc_u);
-        for (int i = 0; i < 4; ++i) {
-            part[wave][0][4 * q + i][l16] = acc_g[i];
-            if (GATED) part[wave][GATED ? 1 : 0][4 * q + i][l16] = acc_u[i];
+        for (int t = 0; t < CT; ++t) {
+            pin(acc[t]);
+            for (int i = 0; i < 4; ++i) part[wave][t][4 * q + i][l16] = acc[t][i];
         }
         __syncthreads();
-        {
+        for (int i = tid; i < kUpCols * 16; i += 256) {
             // one column of one pair per thread
-            const int c = tid & 15, r = tid >> 4;
-            if (r < live && col0 + c < I) {
+            const int c = i % kUpCols, r = i / kUpCols, col = col0 + c;
+            if (r < live && col < I) {
                 float z[2] = {0.0f, 0.0f};
                 for (int s = 0; s < (GATED ? 2 : 1); ++s) {
-                    for (int w = 0; w < 4; ++w) z[s] += part[w][s][c][r];
+                    for (int w = 0; w < 4; ++w) z[s] += part[w][s * (kUpCols / 16) + c / 16][c % 16][r];
                     if (a.bias1)
-                        z[s] += __uint_as_float((uint32_t)((const uint16_t *)a.bias1)[e * n1 + s * I + col0 + c] << 16);
+                        z[s] += __uint_as_float((uint32_t)((const uint16_t *)a.bias1)[(int64_t)e * n1 + s * I + col] << 16);
                 }
                 float y = a.kind == 1 ? act_value<1>(z[0]) : a.kind == 2 ? act_value<2>(z[0]) : z[0];
                 if (GATED) y *= z[1];
-                // bf16: the type a dispatch would carry and the matrix
-                // instruction takes; the one rounding between x and out
-                ((__bf16 *)a.h)[(int64_t)list[g0 + r] * I + col0 + c] = (__bf16)y;
+                // the matrix instruction takes bf16: y as the sum of two of
+                // them keeps 16 significant bits, so that out is rounded once
+                __bf16 *h = (__bf16 *)a.h + (int64_t)list[g0 + r] * 2 * I + col;
+                const __bf16 hi = (__bf16)y;
+                h[0] = hi;
+                h[I] = (__bf16)(y - (float)hi);
             }
         }
         __syncthreads();
@@ -188,21 +248,22 @@ __global__ __launch_bounds__(256) void moe_decode_up_kernel(DecodeK k) {
 
 // Waves of the second kernel.
 constexpr int kDownWaves = 8;
+constexpr int kDownCols = 32;     // channels of out of its workgroup
 
 template <bool FP8>
 __global__ __launch_bounds__(64 * kDownWaves) void moe_decode_down_kernel(DecodeK k) {
     const MoeDecodeArgs &a = k.a;
-    extern __shared__ __align__(16) float y[];             // [pairs][16]
-    int *first = (int *)(y + k.pairs * 16);                // [E] first pair of an expert
+    extern __shared__ __align__(16) float y[];             // [pairs][kDownCols]
+    int *first = (int *)(y + k.pairs * kDownCols);                // [E] first pair of an expert
     int16_t *id = (int16_t *)(first + a.E);                // [pairs] expert of a pair
     int16_t *leader = id + ((k.pairs + 7) & ~7);           // [pairs] the experts' first pairs
     int16_t *mine = leader + ((k.pairs + 7) & ~7) + (threadIdx.x >> 6) * 16;   // a wave's 16 pairs
     __shared__ int red[kDownWaves];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63, wave = wave_uniform(tid >> 6);
     const int l16 = lane & 15, q = lane >> 4;
     constexpr int kThreads = 64 * kDownWaves;
     const int H = a.H, I = a.I;
-    const int h0 = blockIdx.x * 16;
+    const int h0 = blockIdx.x * kDownCols;
 
     for (int e = tid; e < a.E; e += kThreads) first[e] = k.pairs;
     __syncthreads();
@@ -230,14 +291,28 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_decode_down_kernel(Decode
         __syncthreads();
     }
 
-    const int wrow = min(h0 + l16, H - 1);
+    const int64_t w_bytes = (int64_t)H * I * (FP8 ? 1 : 2);
+    const int groups = I / kFp8Group;
+    constexpr int CT = kDownCols / 16;
+    const Buffer hb = buffer(a.h, (int64_t)k.pairs * I * 4);
+    uint32_t wv[CT], sv[CT];
+#pragma unroll
+    for (int t = 0; t < CT; ++t) {
+        const int row = h0 + t * 16 + l16;
+        wv[t] = row < H ? (uint32_t)row * I * (FP8 ? 1 : 2) : kOutOfRange - 1024;
+        sv[t] = row < H ? (uint32_t)row * groups : kOutOfRange - 16;
+    }
+    const int chunks = (I + Chunk<FP8, CT>::kChannels - 1) / Chunk<FP8, CT>::kChannels;
     for (int s = wave; s < experts; s += kDownWaves) {
-        const int p0 = leader[s];
-        const int e = id[p0];
-        const Weights<FP8> w(a.w2, a.w2_scales, (int64_t)e * H + wrow, I);
+        const int p0 = wave_uniform((int)leader[s]);
+        const int e = wave_uniform((int)id[p0]);
+        const Buffer wb = buffer((const uint8_t *)a.w2 + e * w_bytes, w_bytes);
+        const Buffer sb = buffer(a.w2_scales + (FP8 ? (int64_t)e * H * groups : 0), FP8 ? (int64_t)H * groups : 0);
         // the expert's pairs, 16 at a time in ascending order
         int from = p0;
         while (from < k.pairs) {
+            Chunk<FP8, CT> chunk;
+            chunk.load_w(wb, wv, sb, sv, 0, I);
             int live = 0;
             int p = from;
             for (; p < k.pairs && live < 16; p += 64) {
@@ -252,39 +327,33 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_decode_down_kernel(Decode
             if (n == 0) break;
             const int pair = mine[l16 < n ? l16 : 0];
             const int last = wave_uniform((int)mine[n - 1]);
-            const uint16_t *h = (const uint16_t *)a.h + (int64_t)pair * I;
-            ep_f32x4 acc = {0, 0, 0, 0};
-#pragma unroll 4
-            for (int c = 0; c < I; c += 128) {
-                ep_u32x4 v[4], hv[4];
-                float sc = 0.0f;
-                w.load(c, q, I, v, &sc);
+            const uint32_t hv = l16 < n ? (uint32_t)pair * I * 4 : kOutOfRange;
+            ep_f32x4 acc[CT];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int at = Weights<FP8>::channel(c, j, q);
-                    hv[j] = l16 < n && at < I ? *(const ep_u32x4 *)(h + at) : ep_u32x4{0, 0, 0, 0};
+            for (int t = 0; t < CT; ++t) acc[t] = ep_f32x4{0, 0, 0, 0};
+            sweep<2, FP8, CT>(chunk, wb, wv, sb, sv, hb, hv, I * 2, 0, chunks, I, acc);
+#pragma unroll
+            for (int t = 0; t < CT; ++t) {
+                pin(acc[t]);
+                if (a.bias2) {
+                    for (int i = 0; i < 4; ++i) {
+                        const int c = h0 + t * 16 + 4 * q + i;
+                        if (c < H)
+                            acc[t][i] += __uint_as_float((uint32_t)((const uint16_t *)a.bias2)[(int64_t)e * H + c] << 16);
+                    }
                 }
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                        Weights<FP8>::operand(v, sc, j), __builtin_bit_cast(ep_bf16x8, hv[j]), acc, 0, 0, 0);
+                if (l16 < n) *(ep_f32x4 *)(y + pair * kDownCols + t * 16 + 4 * q) = acc[t];
             }
-            pin(acc);
-            if (a.bias2) {
-                for (int i = 0; i < 4; ++i)
-                    if (h0 + 4 * q + i < H)
-                        acc[i] += __uint_as_float((uint32_t)((const uint16_t *)a.bias2)[(int64_t)e * H + h0 + 4 * q + i] << 16);
-            }
-            if (l16 < n) *(ep_f32x4 *)(y + pair * 16 + 4 * q) = acc;
             if (live < 16) break;        // all pairs were seen
             from = last + 1;
         }
     }
     __syncthreads();
 
-    // out[t, h0 .. h0 + 15] in pieces of 8 channels
-    for (int i = tid; i < a.T * 2; i += kThreads) {
-        const int t = i >> 1, c = (i & 1) * 8;
+    // out[t, h0 .. h0 + 31] in pieces of 8 channels
+    constexpr int kParts = kDownCols / 8;
+    for (int i = tid; i < a.T * kParts; i += kThreads) {
+        const int t = i / kParts, c = i % kParts * 8;
         if (h0 + c >= H) continue;
         const int64_t o = (int64_t)t * H + h0 + c;
         float s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
@@ -298,7 +367,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_decode_down_kernel(Decode
             const int p = t * a.K + kk;
             if (id[p] < 0) continue;
             const float w = a.topk_weights ? a.topk_weights[p] : 1.0f;
-            for (int j = 0; j < 8; ++j) s[j] = __builtin_fmaf(w, y[p * 16 + c + j], s[j]);
+            for (int j = 0; j < 8; ++j) s[j] = __builtin_fmaf(w, y[p * kDownCols + c + j], s[j]);
         }
         ep_u32x4 v;
         for (int j = 0; j < 4; ++j) v[j] = pack_bf16(s[2 * j], s[2 * j + 1]);
@@ -307,7 +376,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_decode_down_kernel(Decode
 }
 
 size_t down_lds(int pairs, int E) {
-    return (size_t)pairs * 64 + (size_t)E * 4 + (size_t)((pairs + 7) & ~7) * 4 + kDownWaves * 32;
+    return (size_t)pairs * kDownCols * 4 + (size_t)E * 4 + (size_t)((pairs + 7) & ~7) * 4 + kDownWaves * 32;
 }
 
 }  // namespace
@@ -317,8 +386,8 @@ hipError_t launch_moe_decode(const MoeDecodeArgs &a, hipStream_t stream) {
     k.a = a;
     k.pairs = a.T * a.K;
     k.by_pair = k.pairs <= a.E ? 1 : 0;
-    const dim3 up((unsigned)((a.I + 15) / 16), (unsigned)(k.by_pair ? k.pairs : a.E));
-    const dim3 down((unsigned)((a.H + 15) / 16));
+    const dim3 up((unsigned)((a.I + kUpCols - 1) / kUpCols), (unsigned)(k.by_pair ? k.pairs : a.E));
+    const dim3 down((unsigned)((a.H + kDownCols - 1) / kDownCols));
     const size_t lds = down_lds(k.pairs, a.E);
     if (a.fp8) {
         if (a.gated) moe_decode_up_kernel<true, true><<<up, dim3(256), 0, stream>>>(k);

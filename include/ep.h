@@ -461,7 +461,7 @@ int ep_combine_logfmt(const void *payload, int32_t hidden, int64_t num_y_rows,
  *              ep_expert_activation_backward: e4m3 codes and UE8M0 scales per
  *              32 channels, the format of ep_cast_fp8, taken from the fp32 z.
  * Errors: EP_ERR_INVALID_ARG; EP_ERR_UNSUPPORTED (fp8 with transposed, k or n
- * above EP_MAX_HIDDEN, an expert's weights of 2^31 bytes or more). */
+ * above EP_MAX_HIDDEN, an expert's weights of 2^31 - 4096 bytes or more). */
 int ep_expert_linear(const void *x, int x_dtype, const uint8_t *x_scales, const void *w,
                      const uint8_t *w_scales, int32_t n, int32_t k, int transposed,
                      const void *bias, int act, const void *residual,
@@ -525,9 +525,9 @@ size_t ep_moe_decode_workspace_bytes(int32_t num_tokens, int32_t num_topk, int32
 /* ep_moe_decode - a whole mixture-of-experts layer for a few tokens, without
  * a layout: out[t] = res0[t] + res1[t] + sum_k w[t,k] (W2[e] h + b2[e]), h =
  * act(W1[e] x[t] + b1[e]), e = topk_idx[t,k].  What dispatch, two
- * ep_expert_linear calls and ep_combine compute, in two kernels; h is rounded
- * to bf16, the expert outputs stay in fp32 and are added in ascending k (fmaf)
- * as ep_combine adds them.  A token's result does not depend on the others.
+ * ep_expert_linear calls and ep_combine compute, in two kernels; h keeps 16
+ * significant bits, the expert outputs stay in fp32 and are added in ascending
+ * k (fmaf) as ep_combine adds them, so out is rounded once.  A token's result does not depend on the others.
  *
  *   x            device bf16 [T, H], 16-byte aligned.
  *   topk_idx     device int64 [T, K]; -1 = no expert (as is any id outside
@@ -548,7 +548,8 @@ size_t ep_moe_decode_workspace_bytes(int32_t num_tokens, int32_t num_topk, int32
  *   status       device int32 [1] or NULL: EP_DEV_BAD_EXPERT is OR-ed in.
  *   out          device bf16 [T, H], 16-byte aligned.
  * Errors: EP_ERR_INVALID_ARG, EP_ERR_WORKSPACE, EP_ERR_UNSUPPORTED (more
- * pairs, E above EP_MAX_EXPERTS, H or I above EP_MAX_HIDDEN). */
+ * pairs, E above EP_MAX_EXPERTS, H or I above EP_MAX_HIDDEN, an expert's w1,
+ * x or 4 T*K*I of 2^31 - 4096 bytes or more). */
 int ep_moe_decode(const void *x, const int64_t *topk_idx, const float *topk_weights,
                   int32_t num_tokens, int32_t num_topk, int32_t num_experts, int32_t hidden,
                   int32_t inter, int w_dtype, const void *w1, const uint8_t *w1_scales,
