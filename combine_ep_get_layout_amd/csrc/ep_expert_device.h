@@ -170,6 +170,18 @@ __device__ __forceinline__ void dma16_of4(const ep_i32x4 &rsrc, uint32_t lds, ui
                  : "v"(voff), "s"(r), "s"(wave_uniform((int)soff)), "n"(J * 1024));
 }
 
+// 64 lanes x 1 byte, one dword of LDS each (the byte, zero extended).
+__device__ __forceinline__ void dma1(const ep_i32x4 &rsrc, uint32_t lds, uint32_t voff, uint32_t soff) {
+    ep_i32x4 r;
+    for (int i = 0; i < 4; ++i) r[i] = wave_uniform(rsrc[i]);
+    asm volatile(
+        "s_mov_b32 m0, %0\n\t"
+        "s_nop 0\n\t"
+        "buffer_load_ubyte %1, %2, %3 offen lds"
+        :
+        : "s"(wave_uniform((int)lds)), "v"(voff), "s"(r), "s"(wave_uniform((int)soff)));
+}
+
 // All but the newest N copies of this wave have landed, and its own LDS reads
 // have returned (so that a barrier after it releases the buffers they read).
 template <int N>
@@ -237,6 +249,16 @@ __device__ __forceinline__ float fast_exp(float x) {
     const float p = x * kLog2e;
     const float r = __builtin_fmaf(x, kLog2e, -p) + x * kLog2eLo;
     return __builtin_amdgcn_exp2f(p) * __builtin_fmaf(r, 0.693147181f, 1.0f);
+}
+
+// f(0), ..., f(N - 1) with constant arguments: accumulators indexed by them
+// stay in registers whatever the body's size.
+template <int N, typename F>
+__device__ __forceinline__ void each(F f) {
+    if constexpr (N > 0) {
+        each<N - 1>(f);
+        f(std::integral_constant<int, N - 1>{});
+    }
 }
 
 // 1 / (1 + exp(-z)); exp(-z) = inf gives 0.

@@ -39,16 +39,6 @@ struct LinearK {
     int col_tiles;
 };
 
-// f(0), ..., f(N - 1) with constant arguments: accumulators indexed by them
-// stay in registers whatever the body's size.
-template <int N, typename F>
-__device__ __forceinline__ void each(F f) {
-    if constexpr (N > 0) {
-        each<N - 1>(f);
-        f(std::integral_constant<int, N - 1>{});
-    }
-}
-
 // Four consecutive scale bytes of a row from step s on, as far as the row has them.
 __device__ __forceinline__ int scales4(const uint8_t *row, int s, int groups) {
     int v = 0;
