@@ -70,7 +70,8 @@ __device__ __forceinline__ ep_f32x4 mfma_fp8(const ep_u32x4 *a, const ep_u32x4 *
 
 // Bias, checkpoint, activation, residual and output of a wave's accumulators: NT
 // tiles of 16 columns of z (gated: the first half gates, the second their ups)
-// by MT of 16 rows, from row `first` of the segment, `live_rows` of them there;
+// by MT of 16 rows, STRIDE apart from row `first` of the segment on, `live_rows`
+// of the segment's rows left there;
 // c0 is the first column of out.  Accumulator j of tile (t, i) is column 16 t + 4
 // q + j, row 16 i + lane % 16.  The sums go through the wave's part of the LDS in
 // batches of BT row tiles, fp32, 16-byte chunk c of row r in place c ^ (r & 15),
@@ -78,7 +79,7 @@ __device__ __forceinline__ ep_f32x4 mfma_fp8(const ep_u32x4 *a, const ep_u32x4 *
 // a short loop over rows (unrolled over the registers it would not fit the
 // instruction cache), and residual, output and codes move in whole lines.
 // The residual of the first batch may be on its way since before the product.
-template <int NT, int BT, bool GATED>
+template <int NT, int BT, int STRIDE, bool GATED>
 struct Output {
     static constexpr int COLS = NT * 16, OUT = GATED ? COLS / 2 : COLS;
     static constexpr int LANES = OUT / 8;              // lanes of a row
@@ -86,6 +87,10 @@ struct Output {
     static constexpr int IT = BT * 16 / RPI;           // iterations of a batch
     ep_u32x4 res[IT];
 
+    // first row of iteration i of a batch
+    static __device__ __forceinline__ constexpr int row_of(int batch, int i) {
+        return (batch * BT + i * RPI / 16) * STRIDE + i * RPI % 16;
+    }
     __device__ __forceinline__ void load(const LinearK &a, const TileAt &at, int first,
                                          int live_rows, int c0, int batch) {
         if (!a.residual) return;
@@ -93,18 +98,19 @@ struct Output {
         const uint16_t *p = a.residual + ((int64_t)at.row0 + first + lr) * a.m + c0 + lc * 8;
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
-            const int r = batch * BT * 16 + i * RPI;
+            const int r = row_of(batch, i);
             res[i] = ep_u32x4{0, 0, 0, 0};
             if (c0 + lc * 8 < a.m && r + lr < live_rows) res[i] = *(const ep_u32x4 *)(p + (int64_t)r * a.m);
         }
     }
 };
 
-template <int KIND, int NT, int MT, int BT, bool GATED>
+template <int KIND, int NT, int MT, int BT, int STRIDE, bool GATED>
 __device__ __forceinline__ void epilogue_of(const LinearK &a, const TileAt &at, uint8_t *lds,
                                             int first, int live_rows, int c0,
-                                            ep_f32x4 (*acc)[MT], Output<NT, BT, GATED> &now) {
-    typedef Output<NT, BT, GATED> O;
+                                            ep_f32x4 (*acc)[MT],
+                                            Output<NT, BT, STRIDE, GATED> &now) {
+    typedef Output<NT, BT, STRIDE, GATED> O;
     constexpr int COLS = O::COLS, OUT = O::OUT, LANES = O::LANES, RPI = O::RPI, IT = O::IT;
     constexpr int NK = GATED ? 2 : 1;
     const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
@@ -138,7 +144,7 @@ __device__ __forceinline__ void epilogue_of(const LinearK &a, const TileAt &at, 
         if (batch + 1 < MT / BT) next.load(a, at, first, live_rows, c0, batch + 1);
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
-            const int at_row = batch * BT * 16 + i * RPI;
+            const int at_row = O::row_of(batch, i);
             const int r = i * RPI + lr;
             const bool live = there && at_row + lr < live_rows;
             const int64_t row = row0 + at_row;
@@ -195,17 +201,18 @@ __device__ __forceinline__ void epilogue_of(const LinearK &a, const TileAt &at, 
     });
 }
 
-template <int NT, int MT, int BT, bool GATED>
+template <int NT, int MT, int BT, int STRIDE, bool GATED>
 __device__ __forceinline__ void epilogue(const LinearK &a, const TileAt &at, uint8_t *lds, int first,
                                          int live_rows, int c0, ep_f32x4 (*acc)[MT],
-                                         Output<NT, BT, GATED> &o) {
-    if (a.kind == 1) epilogue_of<1, NT, MT, BT, GATED>(a, at, lds, first, live_rows, c0, acc, o);
-    else if (a.kind == 2) epilogue_of<2, NT, MT, BT, GATED>(a, at, lds, first, live_rows, c0, acc, o);
-    else if (!GATED) epilogue_of<0, NT, MT, BT, GATED>(a, at, lds, first, live_rows, c0, acc, o);
+                                         Output<NT, BT, STRIDE, GATED> &o) {
+    if (a.kind == 1) epilogue_of<1, NT, MT, BT, STRIDE, GATED>(a, at, lds, first, live_rows, c0, acc, o);
+    else if (a.kind == 2) epilogue_of<2, NT, MT, BT, STRIDE, GATED>(a, at, lds, first, live_rows, c0, acc, o);
+    else if (!GATED) epilogue_of<0, NT, MT, BT, STRIDE, GATED>(a, at, lds, first, live_rows, c0, acc, o);
 }
 
-// Tiles of up to 128 rows: bound by reading the weights unless several segments'
-// row tiles share them.  The ring of NS stages keeps NS - 1 steps in flight.
+// Tiles of 128 or 192 rows, for experts of few rows: bound by reading the weights.
+// The ring of NS stages keeps NS - 1 steps in flight; row tiles that hold no row
+// are not multiplied.
 template <int BM, int WM, int NS, bool FP8, bool WT, bool GATED>
 __global__ __launch_bounds__(256 * WM, 2) void expert_linear_kernel(LinearK a) {
     constexpr int kWaves = 4 * WM;
@@ -299,7 +306,7 @@ __global__ __launch_bounds__(256 * WM, 2) void expert_linear_kernel(LinearK a) {
         const int groups = K / kFp8Group;
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
-            const int r = min(wm * MT * 16 + i * 16 + l16, rows - 1);
+            const int r = min((i * WM + wm) * 16 + l16, rows - 1);
             xs[FP8 ? i : 0] = scales4(a.x_scales + ((int64_t)at.row0 + row0 + r) * groups, s, groups);
         }
 #pragma unroll
@@ -309,25 +316,27 @@ __global__ __launch_bounds__(256 * WM, 2) void expert_linear_kernel(LinearK a) {
         }
     };
 
+    // row tiles of this wave that hold a row: the waves take them in turn
+    const int live = ((rows + 15) / 16 - wm + WM - 1) / WM;
     const int slot = l16 * 128 + (q ^ (l16 >> 1)) * 16;
     auto compute = [&](int stage, auto sb) {
         const uint8_t *wl = lds + stage * kStage;
-        const uint8_t *xl = wl + kWStage + wm * MT * 16 * 128;
+        const uint8_t *xl = wl + kWStage + wm * 2048;
         ep_u32x4 wf[4][2], xf[MT][2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int t = 0; t < 4; ++t)
                 wf[t][h] = WT ? transposed_operand<512>(wl, wn * 4 + t, h)
                               : *(const ep_u32x4 *)(wl + (wn * 4 + t) * 2048 + (slot ^ (h * 64)));
 #pragma unroll
-            for (int i = 0; i < MT; ++i)
-                xf[i][h] = *(const ep_u32x4 *)(xl + i * 2048 + (slot ^ (h * 64)));
-        }
+        for (int i = 0; i < MT; ++i) {
+            if (i >= live) break;
 #pragma unroll
-        for (int h = 0; h < (FP8 ? 1 : 2); ++h)
+            for (int h = 0; h < 2; ++h)
+                xf[i][h] = *(const ep_u32x4 *)(xl + i * WM * 2048 + (slot ^ (h * 64)));
 #pragma unroll
-            for (int i = 0; i < MT; ++i)
+            for (int h = 0; h < (FP8 ? 1 : 2); ++h)
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
                     if (FP8)
@@ -335,6 +344,7 @@ __global__ __launch_bounds__(256 * WM, 2) void expert_linear_kernel(LinearK a) {
                     else
                         acc[t][i] = mfma_bf16(wf[t][h], xf[i][h], acc[t][i]);
                 }
+        }
     };
 
     for (int s = 0; s < NS - 1; ++s)
@@ -363,10 +373,12 @@ __global__ __launch_bounds__(256 * WM, 2) void expert_linear_kernel(LinearK a) {
         for (int s = 0; s < steps; ++s) step(s, std::integral_constant<int, 0>{});
     }
     barrier_only();                                    // the stages are the epilogue's now
-    Output<4, MT, GATED> o;
-    o.load(a, at, row0 + wm * MT * 16, rows - wm * MT * 16, column(wn * 64), 0);
-    epilogue<4, MT, MT, GATED>(a, at, lds + wave * MT * 4096, row0 + wm * MT * 16,
-                               rows - wm * MT * 16, column(wn * 64), acc, o);
+    constexpr int BT = MT > 4 ? MT / 2 : MT;           // row tiles of an epilogue batch
+    static_assert(kWaves * BT * 4096 <= NS * kStage && MT % BT == 0, "a batch must fit the stages");
+    Output<4, BT, WM * 16, GATED> o;
+    o.load(a, at, row0 + wm * 16, rows - wm * 16, column(wn * 64), 0);
+    epilogue<4, MT, BT, WM * 16, GATED>(a, at, lds + wave * BT * 4096, row0 + wm * 16,
+                                        rows - wm * 16, column(wn * 64), acc, o);
 }
 
 // Tiles of 256 rows, bound by the matrix instructions.  Four waves of 128 x 128:
@@ -517,7 +529,7 @@ __global__ __launch_bounds__(256, 1) void expert_linear_wide_kernel(LinearK a) {
         __builtin_amdgcn_sched_barrier(0);
     };
 
-    Output<8, 4, GATED> o;
+    Output<8, 4, 16, GATED> o;
     o.load(a, at, row0 + wm * 128, rows - wm * 128, column(wn, 0), 0);
     for (int s = 0; s < 2; ++s) {
         each<4>([&](auto j) { copy_x(s, s, 0, j); });
@@ -587,7 +599,8 @@ __global__ __launch_bounds__(256, 1) void expert_linear_wide_kernel(LinearK a) {
         }); }); });
     }
     barrier_only();                                    // the stages are the epilogue's now
-    epilogue<8, 8, 4, GATED>(a, at, lds + wave * 32768, row0 + wm * 128, rows - wm * 128,
+    static_assert(kWaves * 32768 <= 2 * kStage, "a batch must fit the stages");
+    epilogue<8, 8, 4, 16, GATED>(a, at, lds + wave * 32768, row0 + wm * 128, rows - wm * 128,
                              column(wn, 0), acc, o);
 }
 
@@ -654,10 +667,16 @@ hipError_t launch_expert_linear(const LinearArgs &a, hipStream_t stream) {
     k.kind = act_kind(a.act);
     const int per_tile = gated ? kBN / 2 : kBN;
     k.col_tiles = (k.m + per_tile - 1) / per_tile;
+    // Row tiles by the rows an expert can expect (up to 256 experts of 7168 x 4096,
+    // uniform routing).  Up to about 112 the weights' reads decide, and the deep
+    // ring of the 128-row tile reads them at 6.3 TB/s (2.4 to 2.7 ms); around 128
+    // half of the experts need a second 128-row tile, where one of 192 rows and two
+    // stages does (3.14 against 3.26 ms; 2.95 against 2.50 ms at 64 rows); from 160
+    // rows on the matrix instructions decide and the 256-row tile is the faster.
     const int64_t avg = a.seg.pairs / a.seg.E;
     if (avg > 160) return launch_wide(a, k, gated, stream);
-    if (avg > 40) return launch_bm<128, 2, 3>(a, k, gated, stream);
-    return launch_bm<32, 1, 2>(a, k, gated, stream);
+    if (avg > 112) return launch_bm<192, 2, 2>(a, k, gated, stream);
+    return launch_bm<128, 2, 3>(a, k, gated, stream);
 }
 
 }  // namespace ep

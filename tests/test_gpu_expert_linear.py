@@ -98,6 +98,25 @@ def test_fp8(gpu, T, E, K, A, k, n):
         check(gpu, lay, rows, x, w, act, b, checkpoint=True)
 
 
+@pytest.mark.parametrize("T", [100, 260, 300, 400])
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "transposed"])
+def test_rows_per_expert(gpu, T, kind):
+    """50, 130, 150 and 200 expected rows an expert (each has its row tile), with
+    experts on both sides of it."""
+    announce("linear rows per expert", T, kind)
+    g = torch.Generator(device=DEV).manual_seed(T)
+    # uneven: expert 0 gets twice its share, expert 3 none
+    idx = torch.randint(0, 5, (T, 2), generator=g, device=DEV)
+    idx = torch.where(idx >= 3, torch.where(idx == 3, 0, -1), idx)
+    tr = kind == "transposed"
+    for act in ("none", "geglu") if not tr else ("none",):
+        lay, rows, x, w, g = make(gpu, T, 4, 2, 640, 704, fp8=kind == "fp8", transposed=tr, idx=idx)
+        b = torch.randn((4, 704), generator=g, device=DEV).bfloat16()
+        m = 352 if act == "geglu" else 704
+        res = torch.randn((rows, m), generator=g, device=DEV).bfloat16()
+        check(gpu, lay, rows, x, w, act, b, res, transposed=tr, checkpoint=True)
+
+
 @pytest.mark.parametrize("E", [1, 300, 700, 4096])
 def test_many_experts_most_of_them_empty(gpu, E):
     announce("linear experts", E)
