@@ -56,14 +56,14 @@ def algorithmic_bytes(T, H, K, N, R, elem=2):
 
 
 def kernel_source_hash():
-    """Hash of the device sources (every csrc file but the host-only C-ABI
-    layer) with comments and whitespace removed: profiles/traffic.json is used
+    """Hash of the device sources of the timed path (every csrc file but the
+    host-only C-ABI layer and the expert operators) with comments and whitespace removed: profiles/traffic.json is used
     only while it matches, so any change to the code voids it and a change to
     the comments does not."""
     h = hashlib.sha256()
     d = os.path.join(ROOT, "combine_ep_get_layout_amd", "csrc")
     for f in sorted(os.listdir(d)):
-        if f == "ep_api.hip":
+        if f == "ep_api.hip" or f.startswith("ep_expert"):
             continue
         with open(os.path.join(d, f)) as fh:
             src = fh.read()
