@@ -372,6 +372,7 @@ __global__ __launch_bounds__(256 * WM, 2) void expert_linear_kernel(LinearK a) {
     } else {
         for (int s = 0; s < steps; ++s) step(s, std::integral_constant<int, 0>{});
     }
+    dma_wait<0>();
     barrier_only();                                    // the stages are the epilogue's now
     constexpr int BT = MT > 4 ? MT / 2 : MT;           // row tiles of an epilogue batch
     static_assert(kWaves * BT * 4096 <= NS * kStage && MT % BT == 0, "a batch must fit the stages");
@@ -496,7 +497,10 @@ __global__ __launch_bounds__(256, 1) void expert_linear_wide_kernel(LinearK a) {
     for (int t = 0; t < 8; ++t)
 #pragma unroll
         for (int i = 0; i < 8; ++i) acc[t][i] = ep_f32x4{0, 0, 0, 0};
-    int xs[8], ws[8];                                  // fp8: scale bytes of four steps
+    // fp8: scale bytes of four steps.  (Copied to LDS byte by byte with the
+    // operands, without a wait of their own, they took 912 us where these take
+    // 825: 64 lines a copy keep the address unit busy.)
+    int xs[8], ws[8];
     auto scales = [&](int s) {
         const int groups = K / kFp8Group;
 #pragma unroll
@@ -521,8 +525,9 @@ __global__ __launch_bounds__(256, 1) void expert_linear_wide_kernel(LinearK a) {
             __builtin_amdgcn_sched_barrier(0);
         });
     };
-    // end of a phase: the regions the next one reads have landed, and every
-    // wave has read those this phase read
+    // end of a phase: the regions the next one reads have landed (the copies of
+    // the phase before and of this one, 8 each, may be in flight), and every wave
+    // has read those this phase read
     auto turn = [&]() {
         dma_wait<16>();
         barrier_only();
@@ -597,6 +602,7 @@ __global__ __launch_bounds__(256, 1) void expert_linear_wide_kernel(LinearK a) {
             ep_f32x4 &d = acc[decltype(tw)::value * 4 + b][decltype(tx)::value * 4 + c];
             d = mfma_bf16(wf[decltype(tw)::value][b][h], xf[decltype(tx)::value][c][h], d);
         }); }); });
+        dma_wait<0>();
     }
     barrier_only();                                    // the stages are the epilogue's now
     static_assert(kWaves * 32768 <= 2 * kStage, "a batch must fit the stages");

@@ -98,6 +98,23 @@ def test_fp8(gpu, T, E, K, A, k, n):
         check(gpu, lay, rows, x, w, act, b, checkpoint=True)
 
 
+@pytest.mark.parametrize("act,n", [("swiglu", 16), ("geglu", 80), ("silu", 8)])
+def test_narrow_outputs(gpu, act, n):
+    announce("linear narrow", act, n)
+    for T, E in ((20, 3), (700, 2)):
+        lay, rows, x, w, _ = make(gpu, T, E, 1, 72, n)
+        check(gpu, lay, rows, x, w, act)
+
+
+@pytest.mark.parametrize("T", [60, 700])
+def test_transposed_weights_with_every_part_of_the_epilogue(gpu, T):
+    announce("linear transposed epilogue", T)
+    lay, rows, x, w, g = make(gpu, T, 2, 1, 136, 448, transposed=True)
+    b = torch.randn((2, 448), generator=g, device=DEV).bfloat16()
+    res = torch.randn((rows, 224), generator=g, device=DEV).bfloat16()
+    check(gpu, lay, rows, x, w, "swiglu", b, res, transposed=True, checkpoint=True)
+
+
 @pytest.mark.parametrize("T", [100, 260, 300, 400])
 @pytest.mark.parametrize("kind", ["bf16", "fp8", "transposed"])
 def test_rows_per_expert(gpu, T, kind):
