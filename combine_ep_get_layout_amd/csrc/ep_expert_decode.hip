@@ -14,12 +14,18 @@
 // 16 up rows of W1); its four waves split the sum over the hidden channels and
 // add up in LDS in wave order.
 // Second kernel: a workgroup takes 32 channels of the output and all pairs (h is
-// read once per workgroup; 16 channels read it twice as often and were slower
-// for many pairs):
-// its waves take the chosen experts in turn, every pair's 32 sums go to LDS in
-// fp32, and the tokens' weighted sums are formed from there in ascending k, as
-// ep_combine forms them: no atomics, no rounding between the two, and a
-// token's result does not depend on the other tokens of the batch.
+// read once per workgroup; 16 channels read it twice as often: 128 tokens of fp8
+// weights took 1026 us against 773): its waves take the chosen experts in turn,
+// every pair's 32 sums go to LDS in fp32, and the tokens' weighted sums are
+// formed from there in ascending k, as ep_combine forms them: no atomics, no
+// rounding between the two, and a token's result does not depend on the other
+// tokens of the batch.
+//
+// hidden 7168, intermediate 2048, 256 experts, 8 per token, gated, both kernels:
+//   bf16  1 token  126 us (5.6 TB/s of weights)   128 tokens 3714 us (6.0 TB/s)
+//   fp8   1 token   73 us (4.8 TB/s)              128 tokens 2065 us (5.4 TB/s)
+// where a kernel that only reads reaches 6.1 TB/s.  One token: 0.35 GB of fp8
+// weights are 58 us, two launches and their first loads the rest.
 #include "ep_expert_device.h"
 
 namespace ep {
@@ -41,6 +47,16 @@ __device__ __forceinline__ Buffer buffer(const void *p, int64_t bytes) {
     return __builtin_amdgcn_make_buffer_rsrc((void *)p, 0, (int)bytes, 0x00020000);
 }
 
+// An expert's weights and their scales.
+struct Weights {
+    const uint8_t *w, *scales;
+    int bytes, scale_bytes;
+    __device__ __forceinline__ Weights(const void *base, const void *scale_base, int e, int64_t rows,
+                                       int64_t row_bytes, int64_t groups)
+        : w((const uint8_t *)base + e * rows * row_bytes), scales((const uint8_t *)scale_base + e * rows * groups),
+          bytes((int)(rows * row_bytes)), scale_bytes((int)(rows * groups)) {}
+};
+
 // 256 bytes of the rows of CT weight tiles (16 rows each), and the same channels
 // of up to 16 token rows, as they come from memory: a lane has 4 pieces of 16
 // bytes of a weight row, 8 consecutive bf16 or 16 fp8 channels (with two scale
@@ -53,13 +69,16 @@ struct Chunk {
     static constexpr int kChannels = FP8 ? 256 : 128;
     static constexpr int kX = FP8 ? 8 : 4;
     ep_u32x4 w[CT][4];
-    uint32_t scale[CT][FP8 ? 2 : 1];
+    uint32_t scale;               // of tile q % CT, 128 channels q / CT
 
-    // wv, sv, xv: this lane's byte offsets of its rows (kOutOfRange: zeros)
-    __device__ __forceinline__ void load_w(Buffer wb, const uint32_t *wv, Buffer sb, const uint32_t *sv,
-                                           int chunk, int channels) {
+    // wv, xv: this lane's byte offsets of its rows, sv of its scales (kOutOfRange:
+    // zeros).  Without `some` nothing is read.
+    __device__ __forceinline__ void load_w(const Weights &src, const uint32_t *wv, uint32_t sv,
+                                           int chunk, int channels, bool some = true) {
+        const Buffer wb = buffer(src.w, src.bytes), sb = buffer(src.scales, src.scale_bytes);
         const int q = (threadIdx.x & 63) >> 4;
-        const int c = chunk * kChannels;
+        const int c = some ? chunk * kChannels : channels;
+        chunk = some ? chunk : 0;
 #pragma unroll
         for (int t = 0; t < CT; ++t)
 #pragma unroll
@@ -68,75 +87,107 @@ struct Chunk {
                 if (FP8 ? c + j * 64 >= channels : c + j * 32 + q * 8 >= channels) o = kOutOfRange;
                 w[t][j] = __builtin_bit_cast(ep_u32x4, __builtin_amdgcn_raw_buffer_load_b128(wb, o, chunk * 256, 0));
             }
-        if (FP8) {
-#pragma unroll
-            for (int t = 0; t < CT; ++t)
-#pragma unroll
-                for (int g = 0; g < 2; ++g)
-                    scale[t][FP8 ? g : 0] = __builtin_amdgcn_raw_buffer_load_b8(
-                        sb, c + g * 128 < channels ? sv[t] + g : kOutOfRange, chunk * 2, 0);
-        }
+        // one byte a lane for the four (or two) scales of a row pair
+        if (FP8) scale = __builtin_amdgcn_raw_buffer_load_b8(sb, c + q / CT * 128 < channels ? sv : kOutOfRange,
+                                                             chunk * 2, 0);
     }
-    static __device__ __forceinline__ void load_x(Buffer xb, uint32_t xv, uint32_t part, int chunk,
-                                                  int channels, ep_u32x4 *x) {
+    static __device__ __forceinline__ uint32_t scale_offset(const int *row, int rows, int groups) {
+        const int q = (threadIdx.x & 63) >> 4;
+        const int r = row[q % CT];
+        return q < 2 * CT && r < rows ? (uint32_t)(r * groups + q / CT) : kOutOfRange;
+    }
+    static __device__ __forceinline__ void load_x(Buffer xb, uint32_t xv, int chunk, int channels, ep_u32x4 *x) {
         const int q = (threadIdx.x & 63) >> 4;
 #pragma unroll
         for (int j = 0; j < kX; ++j) {
             // first of the 8 channels
             const int c = chunk * kChannels + (FP8 ? (j >> 1) * 64 + q * 16 + (j & 1) * 8 : j * 32 + q * 8);
             const uint32_t o = xv == kOutOfRange || c >= channels ? kOutOfRange : xv + c * 2;
-            x[j] = __builtin_bit_cast(ep_u32x4, __builtin_amdgcn_raw_buffer_load_b128(xb, o, part, 0));
+            x[j] = __builtin_bit_cast(ep_u32x4, __builtin_amdgcn_raw_buffer_load_b128(xb, o, 0, 0));
         }
     }
-    template <int PARTS>
-    __device__ __forceinline__ void multiply(const ep_u32x4 (*x)[kX], ep_f32x4 *acc) const {
+    // acc[g][t] += weight tile t x token rows g
+    template <int GROUPS>
+    __device__ __forceinline__ void multiply(const ep_u32x4 (*x)[kX], ep_f32x4 (*acc)[CT]) const {
+        float s[CT][2];
+        if (FP8) {
+#pragma unroll
+            for (int i = 0; i < 2 * CT; ++i)
+                s[i % CT][i / CT] = ue8m0_value(__shfl((int)scale, i * 16 + (threadIdx.x & 15)));
+        }
 #pragma unroll
         for (int j = 0; j < kX; ++j)
 #pragma unroll
             for (int t = 0; t < CT; ++t) {
                 ep_u32x4 v;
                 if (FP8) {
-                    const float s = ue8m0_value(scale[t][FP8 ? j >> 2 : 0]);
+                    const float f = s[t][FP8 ? j >> 2 : 0];
                     const uint32_t lo = w[t][j >> 1][(j & 1) * 2], hi = w[t][j >> 1][(j & 1) * 2 + 1];
-                    v.x = fp8_pair_bf16<false>(lo, s);
-                    v.y = fp8_pair_bf16<true>(lo, s);
-                    v.z = fp8_pair_bf16<false>(hi, s);
-                    v.w = fp8_pair_bf16<true>(hi, s);
+                    v.x = fp8_pair_bf16<false>(lo, f);
+                    v.y = fp8_pair_bf16<true>(lo, f);
+                    v.z = fp8_pair_bf16<false>(hi, f);
+                    v.w = fp8_pair_bf16<true>(hi, f);
                 } else {
                     v = w[t][FP8 ? 0 : j];
                 }
 #pragma unroll
-                for (int p = 0; p < PARTS; ++p) acc[t] = mfma_bf16(v, x[p][j], acc[t]);
+                for (int g = 0; g < GROUPS; ++g) acc[g][t] = mfma_bf16(v, x[g][j], acc[g][t]);
             }
     }
 };
 
-// acc[t] += weights x rows over chunks [from, to): a chunk's token rows (from
-// the caches) are asked for just before the next chunk's weights (from memory),
-// so waiting for them leaves the weights in flight.  `a` holds the weights of
-// chunk `from` already.
-// PARTS 2: the token rows are sums of two bf16 rows, the second `second` bytes
-// behind the first.
-template <int PARTS, bool FP8, int CT>
-__device__ __forceinline__ void sweep(Chunk<FP8, CT> &a, Buffer wb, const uint32_t *wv, Buffer sb,
-                                      const uint32_t *sv, Buffer xb, uint32_t xv, uint32_t second,
-                                      int from, int to, int channels, ep_f32x4 *acc) {
+// acc[g][t] += weights x rows g over chunks [from, to): a chunk's token rows
+// (from the caches) are asked for just before the next chunk's weights (from
+// memory), so that waiting for them leaves the weights in flight.  That needs a
+// loop without conditional loads: where one may be left out, the wait counts
+// every load behind it as possibly the one waited for.  `a` holds the weights
+// of chunk `from`; it is left with those of chunk next_from of `next`, if there
+// are `more`.
+template <int GROUPS, bool FP8, int CT>
+__device__ __forceinline__ void sweep(Chunk<FP8, CT> &a, const Weights &src, const uint32_t *wv, uint32_t sv,
+                                      Buffer xb, const uint32_t *xv, int from, int to, int channels,
+                                      ep_f32x4 (*acc)[CT], const Weights &next, int next_from, bool more) {
     typedef Chunk<FP8, CT> C;
     C b;
-    ep_u32x4 x[PARTS][C::kX];
+    ep_u32x4 x[GROUPS][C::kX];
+#pragma unroll
+    for (int g = 0; g < GROUPS; ++g)
+#pragma unroll
+        for (int t = 0; t < CT; ++t) acc[g][t] = ep_f32x4{0, 0, 0, 0};
     auto load_x = [&](int c) {
 #pragma unroll
-        for (int p = 0; p < PARTS; ++p) C::load_x(xb, xv, p * second, c, channels, x[p]);
+        for (int g = 0; g < GROUPS; ++g) C::load_x(xb, xv[g], c, channels, x[g]);
     };
-    for (int c = from; c < to; c += 2) {
+    // the order of loads and products is as written
+    auto fence = [] { __builtin_amdgcn_sched_barrier(0); };
+    int c = from;
+    for (; c + 1 < to; c += 2) {
         load_x(c);
-        if (c + 1 < to) b.load_w(wb, wv, sb, sv, c + 1, channels);
-        a.template multiply<PARTS>(x, acc);
-        if (c + 1 >= to) break;
+        fence();
+        b.load_w(src, wv, sv, c + 1, channels);
+        fence();
+        a.template multiply<GROUPS>(x, acc);
+        fence();
         load_x(c + 1);
-        if (c + 2 < to) a.load_w(wb, wv, sb, sv, c + 2, channels);
-        b.template multiply<PARTS>(x, acc);
+        fence();
+        const bool here = c + 2 < to;
+        Weights then = src;
+        then.w = here ? src.w : next.w;
+        then.scales = here ? src.scales : next.scales;
+        a.load_w(then, wv, sv, here ? c + 2 : next_from, channels, here || more);
+        fence();
+        b.template multiply<GROUPS>(x, acc);
+        fence();
     }
+    if (c < to) {
+        load_x(c);
+        a.template multiply<GROUPS>(x, acc);
+        a.load_w(next, wv, sv, next_from, channels, more);
+    }
+#pragma unroll
+    for (int g = 0; g < GROUPS; ++g)
+#pragma unroll
+        for (int t = 0; t < CT; ++t) pin(acc[g][t]);
 }
 
 // The pairs of expert e, ascending, to list[]; returns how many.  `red` is LDS
@@ -168,7 +219,7 @@ constexpr int kUpCols = 16;       // columns of h of a workgroup of the first ke
 template <bool FP8, bool GATED>
 __global__ __launch_bounds__(256) void moe_decode_up_kernel(DecodeK k) {
     const MoeDecodeArgs &a = k.a;
-    constexpr int CT = (GATED ? 2 : 1) * kUpCols / 16;
+    constexpr int CT = GATED ? 2 : 1;
     __shared__ int16_t list[kMaxPairs];
     __shared__ int red[8];
     __shared__ float part[4][CT][16][17];
@@ -185,42 +236,36 @@ __global__ __launch_bounds__(256) void moe_decode_up_kernel(DecodeK k) {
 
     const int I = a.I, H = a.H, n1 = GATED ? 2 * I : I;
     const int col0 = blockIdx.x * kUpCols;
-    const int64_t w_bytes = (int64_t)n1 * H * (FP8 ? 1 : 2);
-    const Buffer wb = buffer((const uint8_t *)a.w1 + e * w_bytes, w_bytes);
-    const int groups = H / kFp8Group;
-    const Buffer sb = buffer(a.w1_scales + (FP8 ? (int64_t)e * n1 * groups : 0), FP8 ? (int64_t)n1 * groups : 0);
+    const int groups = FP8 ? H / kFp8Group : 0;
+    const Weights weights(a.w1, a.w1_scales, e, n1, (int64_t)H * (FP8 ? 1 : 2), groups);
     const Buffer xb = buffer(a.x, (int64_t)a.T * H * 2);
-    uint32_t wv[CT], sv[CT];
+    uint32_t wv[CT];
+    int row[CT];
 #pragma unroll
     for (int t = 0; t < CT; ++t) {
-        // gated: tiles of gates, then of their ups
-        const int col = col0 + (t % (kUpCols / 16)) * 16 + l16;
-        const int row = col + (t >= kUpCols / 16 ? I : 0);
-        wv[t] = col < I ? (uint32_t)row * H * (FP8 ? 1 : 2) : kOutOfRange - 1024;
-        sv[t] = col < I ? (uint32_t)row * groups : kOutOfRange - 16;
+        // gated: a tile of gates, then of their ups
+        row[t] = col0 + l16 < I ? col0 + l16 + t * I : n1;
+        wv[t] = row[t] < n1 ? (uint32_t)row[t] * H * (FP8 ? 1 : 2) : kOutOfRange - 1024;
     }
+    const uint32_t sv = Chunk<FP8, CT>::scale_offset(row, n1, groups);
     // the waves take equal runs of the row's chunks
     const int chunks = (H + Chunk<FP8, CT>::kChannels - 1) / Chunk<FP8, CT>::kChannels;
     const int from = chunks * wave / 4, to = chunks * (wave + 1) / 4;
     // by pair, the first weights are on their way while the pairs are found
     Chunk<FP8, CT> chunk;
-    if (k.by_pair) chunk.load_w(wb, wv, sb, sv, from, H);
+    if (k.by_pair) chunk.load_w(weights, wv, sv, from, H);
     const int count = wave_uniform(pairs_of<256>(a.topk_idx, k.pairs, e, list, red));
     // by pair: only the expert's first pair computes
     if (count == 0 || (k.by_pair && list[0] != (int)blockIdx.y)) return;
+    if (!k.by_pair) chunk.load_w(weights, wv, sv, from, H);
     for (int g0 = 0; g0 < count; g0 += 16) {
         const int live = min(16, count - g0);
         const uint32_t xv = l16 < live ? (uint32_t)(list[g0 + l16] / a.K) * H * 2 : kOutOfRange;
-        ep_f32x4 acc[CT];
+        ep_f32x4 acc[1][CT];
+        sweep<1>(chunk, weights, wv, sv, xb, &xv, from, to, H, acc, weights, from, g0 + 16 < count);
 #pragma unroll
-        for (int t = 0; t < CT; ++t) acc[t] = ep_f32x4{0, 0, 0, 0};
-        if (!k.by_pair || g0 > 0) chunk.load_w(wb, wv, sb, sv, from, H);
-        sweep<1, FP8, CT>(chunk, wb, wv, sb, sv, xb, xv, 0, from, to, H, acc);
-#pragma unroll
-        for (int t = 0; t < CT; ++t) {
-            pin(acc[t]);
-            for (int i = 0; i < 4; ++i) part[wave][t][4 * q + i][l16] = acc[t][i];
-        }
+        for (int t = 0; t < CT; ++t)
+            for (int i = 0; i < 4; ++i) part[wave][t][4 * q + i][l16] = acc[0][t][i];
         __syncthreads();
         for (int i = tid; i < kUpCols * 16; i += 256) {
             // one column of one pair per thread
@@ -228,7 +273,7 @@ __global__ __launch_bounds__(256) void moe_decode_up_kernel(DecodeK k) {
             if (r < live && col < I) {
                 float z[2] = {0.0f, 0.0f};
                 for (int s = 0; s < (GATED ? 2 : 1); ++s) {
-                    for (int w = 0; w < 4; ++w) z[s] += part[w][s * (kUpCols / 16) + c / 16][c % 16][r];
+                    for (int w = 0; w < 4; ++w) z[s] += part[w][s][c][r];
                     if (a.bias1)
                         z[s] += __uint_as_float((uint32_t)((const uint16_t *)a.bias1)[(int64_t)e * n1 + s * I + col] << 16);
                 }
@@ -239,7 +284,7 @@ __global__ __launch_bounds__(256) void moe_decode_up_kernel(DecodeK k) {
                 __bf16 *h = (__bf16 *)a.h + (int64_t)list[g0 + r] * 2 * I + col;
                 const __bf16 hi = (__bf16)y;
                 h[0] = hi;
-                h[I] = (__bf16)(y - (float)hi);
+                h[I] = __builtin_isfinite((float)hi) ? (__bf16)(y - (float)hi) : (__bf16)0.0f;
             }
         }
         __syncthreads();
@@ -291,31 +336,33 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_decode_down_kernel(Decode
         __syncthreads();
     }
 
-    const int64_t w_bytes = (int64_t)H * I * (FP8 ? 1 : 2);
-    const int groups = I / kFp8Group;
+    const int groups = FP8 ? I / kFp8Group : 0;
     constexpr int CT = kDownCols / 16;
     const Buffer hb = buffer(a.h, (int64_t)k.pairs * I * 4);
-    uint32_t wv[CT], sv[CT];
+    uint32_t wv[CT];
+    int row[CT];
 #pragma unroll
     for (int t = 0; t < CT; ++t) {
-        const int row = h0 + t * 16 + l16;
-        wv[t] = row < H ? (uint32_t)row * I * (FP8 ? 1 : 2) : kOutOfRange - 1024;
-        sv[t] = row < H ? (uint32_t)row * groups : kOutOfRange - 16;
+        row[t] = h0 + t * 16 + l16;
+        wv[t] = row[t] < H ? (uint32_t)row[t] * I * (FP8 ? 1 : 2) : kOutOfRange - 1024;
     }
+    const uint32_t sv = Chunk<FP8, CT>::scale_offset(row, H, groups);
     const int chunks = (I + Chunk<FP8, CT>::kChannels - 1) / Chunk<FP8, CT>::kChannels;
+    auto weights = [&](int e) { return Weights(a.w2, a.w2_scales, e, H, (int64_t)I * (FP8 ? 1 : 2), groups); };
+    auto expert = [&](int s) { return wave_uniform((int)id[wave_uniform((int)leader[s])]); };
+    Chunk<FP8, CT> chunk;
+    if (wave < experts) chunk.load_w(weights(expert(wave)), wv, sv, 0, I);
     for (int s = wave; s < experts; s += kDownWaves) {
-        const int p0 = wave_uniform((int)leader[s]);
-        const int e = wave_uniform((int)id[p0]);
-        const Buffer wb = buffer((const uint8_t *)a.w2 + e * w_bytes, w_bytes);
-        const Buffer sb = buffer(a.w2_scales + (FP8 ? (int64_t)e * H * groups : 0), FP8 ? (int64_t)H * groups : 0);
+        const int e = expert(s);
+        // the expert that this wave takes after this one
+        const bool another = s + kDownWaves < experts;
+        const int e1 = expert(another ? s + kDownWaves : s);
         // the expert's pairs, 16 at a time in ascending order
-        int from = p0;
-        while (from < k.pairs) {
-            Chunk<FP8, CT> chunk;
-            chunk.load_w(wb, wv, sb, sv, 0, I);
+        int from = wave_uniform((int)leader[s]);
+        bool more = true;
+        while (more) {
             int live = 0;
-            int p = from;
-            for (; p < k.pairs && live < 16; p += 64) {
+            for (int p = from; p < k.pairs && live <= 16; p += 64) {
                 const bool hit = p + lane < k.pairs && id[p + lane] == e;
                 const uint64_t m = __ballot(hit);
                 const int at = live + __popcll(m & lanes_below());
@@ -324,28 +371,41 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_decode_down_kernel(Decode
             }
             __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
             const int n = min(live, 16);
-            if (n == 0) break;
-            const int pair = mine[l16 < n ? l16 : 0];
-            const int last = wave_uniform((int)mine[n - 1]);
-            const uint32_t hv = l16 < n ? (uint32_t)pair * I * 4 : kOutOfRange;
-            ep_f32x4 acc[CT];
+            more = live > 16;
+            from = wave_uniform((int)mine[n - 1]) + 1;
+            // columns 0..7 of the product are eight pairs' high parts of h,
+            // columns 8..15 the low parts of the same pairs
+            uint32_t hv[2];
+            int pair[2];
 #pragma unroll
-            for (int t = 0; t < CT; ++t) acc[t] = ep_f32x4{0, 0, 0, 0};
-            sweep<2, FP8, CT>(chunk, wb, wv, sb, sv, hb, hv, I * 2, 0, chunks, I, acc);
-#pragma unroll
-            for (int t = 0; t < CT; ++t) {
-                pin(acc[t]);
-                if (a.bias2) {
-                    for (int i = 0; i < 4; ++i) {
-                        const int c = h0 + t * 16 + 4 * q + i;
-                        if (c < H)
-                            acc[t][i] += __uint_as_float((uint32_t)((const uint16_t *)a.bias2)[(int64_t)e * H + c] << 16);
-                    }
-                }
-                if (l16 < n) *(ep_f32x4 *)(y + pair * kDownCols + t * 16 + 4 * q) = acc[t];
+            for (int g = 0; g < 2; ++g) {
+                const int i = g * 8 + (l16 & 7);
+                pair[g] = mine[i < n ? i : 0];
+                hv[g] = i < n ? (uint32_t)pair[g] * I * 4 + (l16 >> 3) * I * 2 : kOutOfRange;
             }
-            if (live < 16) break;        // all pairs were seen
-            from = last + 1;
+            auto products = [&](auto groups_tag) {
+                constexpr int G = decltype(groups_tag)::value;
+                ep_f32x4 acc[G][CT];
+                sweep<G>(chunk, weights(e), wv, sv, hb, hv, 0, chunks, I, acc, weights(more ? e : e1), 0,
+                         more || another);
+#pragma unroll
+                for (int g = 0; g < G; ++g)
+#pragma unroll
+                    for (int t = 0; t < CT; ++t) {
+                        ep_f32x4 v = acc[g][t];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            v[i] += __shfl_xor(v[i], 8);
+                            const int c = h0 + t * 16 + 4 * q + i;
+                            if (a.bias2 && c < H)
+                                v[i] += __uint_as_float((uint32_t)((const uint16_t *)a.bias2)[(int64_t)e * H + c] << 16);
+                        }
+                        if (l16 < 8 && g * 8 + l16 < n) *(ep_f32x4 *)(y + pair[g] * kDownCols + t * 16 + 4 * q) = v;
+                    }
+            };
+            // one or two groups of eight: a pair's sums are the same in both
+            if (n <= 8) products(std::integral_constant<int, 1>());
+            else products(std::integral_constant<int, 2>());
         }
     }
     __syncthreads();

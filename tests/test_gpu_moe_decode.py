@@ -107,6 +107,22 @@ def test_all_tokens_on_one_expert(gpu, T):
     check(gpu, T, 5, 2, 256, 128, idx=idx)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("inter", [128, 256, 384, 768])
+def test_pairs_per_expert(gpu, inter, fp8):
+    """Groups of 8 and 16 pairs, more experts than waves, odd and even numbers of
+    steps over the intermediate channels."""
+    announce("decode pairs per expert", inter, fp8)
+    counts = [0, 1, 7, 8, 9, 15, 16, 17, 1, 0, 24, 25, 32, 33, 2, 8, 9, 16, 3]
+    idx = torch.cat([torch.full((n,), e, dtype=torch.int64) for e, n in enumerate(counts)])
+    order = torch.randperm(len(idx), generator=torch.Generator().manual_seed(inter))
+    x, idx, w, w1, w2, *_, out = check(gpu, len(idx), len(counts), 1, 256, inter, fp8=fp8,
+                                       idx=idx[order].unsqueeze(1).to(DEV))
+    for t in range(0, len(idx), 29):
+        one = gpu.ep_moe_decode(x[t:t + 1], idx[t:t + 1], w[t:t + 1], w1, w2)
+        assert torch.equal(one[0].view(torch.int16), out[t].view(torch.int16))
+
+
 def test_the_most_pairs(gpu):
     check(gpu, 1024, 4, 1, 64, 64)
     check(gpu, 4, 300, 256, 64, 64)
