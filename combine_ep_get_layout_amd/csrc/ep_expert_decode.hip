@@ -26,6 +26,8 @@
 //   fp8   1 token   73 us (4.8 TB/s)              128 tokens 2065 us (5.4 TB/s)
 // where a kernel that only reads reaches 6.1 TB/s.  One token: 0.35 GB of fp8
 // weights are 58 us, two launches and their first loads the rest.
+#include <algorithm>
+
 #include "ep_expert_device.h"
 
 namespace ep {
@@ -38,6 +40,7 @@ struct DecodeK {
     MoeDecodeArgs a;
     int pairs;
     int by_pair;      // first kernel: a workgroup's expert is that of pair blockIdx.y
+    int tokens;       // second kernel: tokens of a workgroup
 };
 
 typedef __amdgpu_buffer_rsrc_t Buffer;
@@ -299,10 +302,14 @@ template <bool FP8>
 __global__ __launch_bounds__(64 * kDownWaves) void moe_decode_down_kernel(DecodeK k) {
     const MoeDecodeArgs &a = k.a;
     extern __shared__ __align__(16) float y[];             // [pairs][kDownCols]
-    int *first = (int *)(y + k.pairs * kDownCols);                // [E] first pair of an expert
+    // its tokens and their pairs, numbered from 0 here
+    const int t0 = blockIdx.y * k.tokens, tokens = min(k.tokens, a.T - t0);
+    const int pairs = tokens * a.K;
+    const int64_t *topk_idx = a.topk_idx + (int64_t)t0 * a.K;
+    int *first = (int *)(y + pairs * kDownCols);           // [E] first pair of an expert
     int16_t *id = (int16_t *)(first + a.E);                // [pairs] expert of a pair
-    int16_t *leader = id + ((k.pairs + 7) & ~7);           // [pairs] the experts' first pairs
-    int16_t *mine = leader + ((k.pairs + 7) & ~7) + (threadIdx.x >> 6) * 16;   // a wave's 16 pairs
+    int16_t *leader = id + ((pairs + 7) & ~7);             // [pairs] the experts' first pairs
+    int16_t *mine = leader + ((pairs + 7) & ~7) + (threadIdx.x >> 6) * 16;     // a wave's 16 pairs
     __shared__ int red[kDownWaves];
     const int tid = threadIdx.x, lane = tid & 63, wave = wave_uniform(tid >> 6);
     const int l16 = lane & 15, q = lane >> 4;
@@ -310,19 +317,19 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_decode_down_kernel(Decode
     const int H = a.H, I = a.I;
     const int h0 = blockIdx.x * kDownCols;
 
-    for (int e = tid; e < a.E; e += kThreads) first[e] = k.pairs;
+    for (int e = tid; e < a.E; e += kThreads) first[e] = pairs;
     __syncthreads();
-    for (int p = tid; p < k.pairs; p += kThreads) {
-        const int64_t e = a.topk_idx[p];
+    for (int p = tid; p < pairs; p += kThreads) {
+        const int64_t e = topk_idx[p];
         const bool ok = e >= 0 && e < a.E;
         id[p] = ok ? (int16_t)e : (int16_t)-1;
         if (ok) atomicMin(&first[e], p);
     }
     __syncthreads();
     int experts = 0;
-    for (int p0 = 0; p0 < k.pairs; p0 += kThreads) {
+    for (int p0 = 0; p0 < pairs; p0 += kThreads) {
         const int p = p0 + tid;
-        const bool lead = p < k.pairs && id[p] >= 0 && first[id[p]] == p;
+        const bool lead = p < pairs && id[p] >= 0 && first[id[p]] == p;
         const uint64_t m = __ballot(lead);
         if (lane == 0) red[wave] = __popcll(m);
         __syncthreads();
@@ -338,7 +345,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_decode_down_kernel(Decode
 
     const int groups = FP8 ? I / kFp8Group : 0;
     constexpr int CT = kDownCols / 16;
-    const Buffer hb = buffer(a.h, (int64_t)k.pairs * I * 4);
+    const Buffer hb = buffer((const uint16_t *)a.h + (int64_t)t0 * a.K * 2 * I, (int64_t)pairs * I * 4);
     uint32_t wv[CT];
     int row[CT];
 #pragma unroll
@@ -362,8 +369,8 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_decode_down_kernel(Decode
         bool more = true;
         while (more) {
             int live = 0;
-            for (int p = from; p < k.pairs && live <= 16; p += 64) {
-                const bool hit = p + lane < k.pairs && id[p + lane] == e;
+            for (int p = from; p < pairs && live <= 16; p += 64) {
+                const bool hit = p + lane < pairs && id[p + lane] == e;
                 const uint64_t m = __ballot(hit);
                 const int at = live + __popcll(m & lanes_below());
                 if (hit && at < 16) mine[at] = (int16_t)(p + lane);
@@ -412,10 +419,10 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_decode_down_kernel(Decode
 
     // out[t, h0 .. h0 + 31] in pieces of 8 channels
     constexpr int kParts = kDownCols / 8;
-    for (int i = tid; i < a.T * kParts; i += kThreads) {
+    for (int i = tid; i < tokens * kParts; i += kThreads) {
         const int t = i / kParts, c = i % kParts * 8;
         if (h0 + c >= H) continue;
-        const int64_t o = (int64_t)t * H + h0 + c;
+        const int64_t o = (int64_t)(t0 + t) * H + h0 + c;
         float s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
         for (int b = 0; b < 2; ++b) {
             const void *r = b ? a.res1 : a.res0;
@@ -426,7 +433,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_decode_down_kernel(Decode
         for (int kk = 0; kk < a.K; ++kk) {
             const int p = t * a.K + kk;
             if (id[p] < 0) continue;
-            const float w = a.topk_weights ? a.topk_weights[p] : 1.0f;
+            const float w = a.topk_weights ? a.topk_weights[(int64_t)t0 * a.K + p] : 1.0f;
             for (int j = 0; j < 8; ++j) s[j] = __builtin_fmaf(w, y[p * kDownCols + c + j], s[j]);
         }
         ep_u32x4 v;
@@ -447,8 +454,17 @@ hipError_t launch_moe_decode(const MoeDecodeArgs &a, hipStream_t stream) {
     k.pairs = a.T * a.K;
     k.by_pair = k.pairs <= a.E ? 1 : 0;
     const dim3 up((unsigned)((a.I + kUpCols - 1) / kUpCols), (unsigned)(k.by_pair ? k.pairs : a.E));
-    const dim3 down((unsigned)((a.H + kDownCols - 1) / kDownCols));
-    const size_t lds = down_lds(k.pairs, a.E);
+    // A compute unit holds one workgroup of the second kernel, so with few output
+    // channels the tokens are divided among more of them, as far as they all run
+    // at once (experts that two of them share are read twice).  Both kernels, with
+    // one group against several: hidden 2048, intermediate 1408, 60 experts, 4 per
+    // token, 8 tokens bf16 129 and 92 us, 128 tokens fp8 255 and 195 us; hidden
+    // 256, intermediate 1280, 32 tokens 300 and 65 us.
+    const int cols = (a.H + kDownCols - 1) / kDownCols;
+    const int groups = std::max(1, std::min(a.T, 256 / cols));
+    k.tokens = (a.T + groups - 1) / groups;
+    const dim3 down((unsigned)cols, (unsigned)((a.T + k.tokens - 1) / k.tokens));
+    const size_t lds = down_lds(k.tokens * a.K, a.E);
     if (a.fp8) {
         if (a.gated) moe_decode_up_kernel<true, true><<<up, dim3(256), 0, stream>>>(k);
         else moe_decode_up_kernel<true, false><<<up, dim3(256), 0, stream>>>(k);
