@@ -1,20 +1,21 @@
 // Grouped matrix product over the receive segments with its epilogue:
 // out[r] = act(x[r] W[e]^T + b[e]) + residual[r] for the rows r of segment e.
 //
-// A workgroup computes one tile of BM rows by 256 columns (gated activations:
-// 128 gate and the matching 128 up columns, so that the activation needs no
+// A workgroup computes one tile of BM rows by BN columns (gated activations:
+// BN / 2 gate and the matching up columns, so that the activation needs no
 // second pass).  Both operands pass through LDS in K steps of 128 bytes per
-// row (64 bf16 or 128 fp8 channels), copied there without registers, in a
-// ring of NS stages with one barrier per step.
+// row (64 bf16 or 128 fp8 channels), copied there without registers.
 //
 // The weights are the matrix instruction's first operand, so four accumulators
-// of a lane are four consecutive columns of one row: bias, residual and
-// output move in 8-byte pieces and the checkpoint's codes in dwords.
+// of a lane are four consecutive columns of one row.  The sums change lanes in
+// LDS once, so that bias, residual, codes and output move in whole lines.
 //
 // LDS rows are 8 chunks of 16 bytes, chunk c of row r in slot c ^ (r/2 & 7):
 // the 16 rows x 16 bytes a quarter wave reads lie in 16 different slots of the
 // 256-byte bank line.  Weights that lie [k, n] (transposed) are staged as 64
 // rows of 256 columns and read by the transposing LDS read.
+#include <algorithm>
+
 #include "ep_expert_device.h"
 
 namespace ep {
@@ -210,14 +211,18 @@ __device__ __forceinline__ void epilogue(const LinearK &a, const TileAt &at, uin
     else if (!GATED) epilogue_of<0, NT, MT, BT, STRIDE, GATED>(a, at, lds, first, live_rows, c0, acc, o);
 }
 
-// Tiles of 128 or 192 rows, for experts of few rows: bound by reading the weights.
+// Tiles of 128 or 192 rows by 256 columns, for experts of few rows: bound by
+// reading the weights; tiles of 64 by 64 for small products, bound by the latency
+// of a step.
 // The ring of NS stages keeps NS - 1 steps in flight; row tiles that hold no row
 // are not multiplied.
-template <int BM, int WM, int NS, bool FP8, bool WT, bool GATED>
-__global__ __launch_bounds__(256 * WM, 2) void expert_linear_kernel(LinearK a) {
-    constexpr int kWaves = 4 * WM;
+template <int BM, int WM, int WN, int NS, bool FP8, bool WT, bool GATED>
+__global__ __launch_bounds__(64 * WN * WM, 2) void expert_linear_kernel(LinearK a) {
+    constexpr int kWaves = WN * WM;
+    constexpr int BN = 64 * WN;
+    static_assert(!WT || BN == 256, "transposed weights lie in rows of 256 columns");
     constexpr int MT = BM / WM / 16;               // 16-row tiles of a wave
-    constexpr int kWStage = kBN * 128, kXStage = BM * 128;
+    constexpr int kWStage = BN * 128, kXStage = BM * 128;
     constexpr int kStage = kWStage + kXStage;
     constexpr int WL = kWStage / 1024 / kWaves;    // copies of a wave per step
     constexpr int XL = kXStage / 1024 / kWaves;
@@ -231,7 +236,7 @@ __global__ __launch_bounds__(256 * WM, 2) void expert_linear_kernel(LinearK a) {
 
     const int lane = threadIdx.x & 63, wave = wave_uniform(threadIdx.x >> 6);
     const int l16 = lane & 15, q = lane >> 4;
-    const int wn = wave & 3, wm = wave >> 2;
+    const int wn = wave % WN, wm = wave / WN;
     const int K = a.k, N = a.n;
     const int half = N >> 1;
     const int row0 = at.mt * BM;                       // in the segment
@@ -247,11 +252,11 @@ __global__ __launch_bounds__(256 * WM, 2) void expert_linear_kernel(LinearK a) {
     uint32_t xoff[XL], woff[WL];
     int wk[WT ? WL : 1];                               // transposed: the k row of each copy
     for (int j = 0; j < XL; ++j) xoff[j] = (uint32_t)((j * kWaves + wave) * 8 + (lane >> 3)) * ld_bytes + chunk * 16;
-    // column of the weights at place r (0..255) of the tile: gated tiles hold,
+    // column of the weights at place r of the tile: gated tiles hold,
     // per wave, 32 gate columns and the 32 up columns that go with them
     auto column = [&](int r) {
-        if (!GATED) return at.nt * kBN + r;
-        const int c = at.nt * (kBN / 2) + (r >> 6) * 32 + (r & 31);
+        if (!GATED) return at.nt * BN + r;
+        const int c = at.nt * (BN / 2) + (r >> 6) * 32 + (r & 31);
         return (r & 32) ? half + c : c;
     };
     for (int j = 0; j < WL; ++j) {
@@ -273,6 +278,9 @@ __global__ __launch_bounds__(256 * WM, 2) void expert_linear_kernel(LinearK a) {
     }
     const uint32_t lds0 = lds_offset(lds);
     const int steps = (K + BK - 1) / BK;
+    // copies of x that hold a row, of this wave's: the others are left out, and
+    // the rows behind the segment are what the LDS holds (they go nowhere)
+    const int xl = max(0, min(XL, ((rows + 7) / 8 - wave + kWaves - 1) / kWaves));
     auto copy = [&](int s, int stage) {
         const uint32_t base = lds0 + stage * kStage + wave * 1024;
         const bool tail = !FP8 && (s + 1) * BK > K;
@@ -285,13 +293,13 @@ __global__ __launch_bounds__(256 * WM, 2) void expert_linear_kernel(LinearK a) {
                       WT ? (uint32_t)s * BK * (uint32_t)N * 2 : s * 128);
             }
             for (int j = 0; j < XL; ++j)
-                dma16(xb, base + kWStage + j * kWaves * 1024, xoff[j] | out, s * 128);
+                if (j < xl) dma16(xb, base + kWStage + j * kWaves * 1024, xoff[j] | out, s * 128);
         } else {
             for (int j = 0; j < WL; ++j)
                 dma16(wb, base + j * kWaves * 1024, woff[j],
                       WT ? (uint32_t)s * BK * (uint32_t)N * 2 : s * 128);
             for (int j = 0; j < XL; ++j)
-                dma16(xb, base + kWStage + j * kWaves * 1024, xoff[j], s * 128);
+                if (j < xl) dma16(xb, base + kWStage + j * kWaves * 1024, xoff[j], s * 128);
         }
     };
 
@@ -320,6 +328,7 @@ __global__ __launch_bounds__(256 * WM, 2) void expert_linear_kernel(LinearK a) {
     const int live = ((rows + 15) / 16 - wm + WM - 1) / WM;
     const int slot = l16 * 128 + (q ^ (l16 >> 1)) * 16;
     auto compute = [&](int stage, auto sb) {
+        if (live <= 0) return;
         const uint8_t *wl = lds + stage * kStage;
         const uint8_t *xl = wl + kWStage + wm * 2048;
         ep_u32x4 wf[4][2], xf[MT][2];
@@ -329,12 +338,19 @@ __global__ __launch_bounds__(256 * WM, 2) void expert_linear_kernel(LinearK a) {
             for (int t = 0; t < 4; ++t)
                 wf[t][h] = WT ? transposed_operand<512>(wl, wn * 4 + t, h)
                               : *(const ep_u32x4 *)(wl + (wn * 4 + t) * 2048 + (slot ^ (h * 64)));
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            if (i >= live) break;
+        auto read_x = [&](int i) __attribute__((always_inline)) {
 #pragma unroll
             for (int h = 0; h < 2; ++h)
                 xf[i][h] = *(const ep_u32x4 *)(xl + i * WM * 2048 + (slot ^ (h * 64)));
+        };
+        read_x(0);
+        // all reads before the first product: with few registers in use the
+        // compiler would wait for each by itself
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            if (i >= live) break;
+            if (i > 0) read_x(i);
 #pragma unroll
             for (int h = 0; h < (FP8 ? 1 : 2); ++h)
 #pragma unroll
@@ -353,7 +369,10 @@ __global__ __launch_bounds__(256 * WM, 2) void expert_linear_kernel(LinearK a) {
     auto step = [&](int s, auto sb) {
         // stage s has landed once at most the copies of the steps after it
         // are in flight; near the end there are none, and all are waited for
-        if (s + NS - 2 < steps) dma_wait<(NS - 2) * (WL + XL)>();
+        if (s + NS - 2 < steps)
+            each<XL + 1>([&](auto n) __attribute__((always_inline)) {
+                if (xl == decltype(n)::value) dma_wait<(NS - 2) * (WL + decltype(n)::value)>();
+            });
         else dma_wait<0>();
         barrier_only();
         const int next = stage == 0 ? NS - 1 : stage - 1;
@@ -634,20 +653,22 @@ hipError_t launch_wide(const LinearArgs &a, const LinearK &k, bool gated, hipStr
     return hipGetLastError();
 }
 
-template <int BM, int WM, int NS>
+template <int BM, int WM, int WN, int NS>
 hipError_t launch_bm(const LinearArgs &a, const LinearK &k, bool gated, hipStream_t stream) {
     const int64_t grid = grid_of(a, k, BM);
     if (grid > 0x7fffffff) return hipErrorInvalidConfiguration;
-    const dim3 g((unsigned)grid), t(256 * WM);
+    const dim3 g((unsigned)grid), t(64 * WN * WM);
     if (a.fp8) {
-        if (gated) expert_linear_kernel<BM, WM, NS, true, false, true><<<g, t, 0, stream>>>(k);
-        else expert_linear_kernel<BM, WM, NS, true, false, false><<<g, t, 0, stream>>>(k);
+        if (gated) expert_linear_kernel<BM, WM, WN, NS, true, false, true><<<g, t, 0, stream>>>(k);
+        else expert_linear_kernel<BM, WM, WN, NS, true, false, false><<<g, t, 0, stream>>>(k);
     } else if (a.transposed) {
-        if (gated) expert_linear_kernel<BM, WM, NS, false, true, true><<<g, t, 0, stream>>>(k);
-        else expert_linear_kernel<BM, WM, NS, false, true, false><<<g, t, 0, stream>>>(k);
+        if constexpr (WN == 4) {
+            if (gated) expert_linear_kernel<BM, WM, WN, NS, false, true, true><<<g, t, 0, stream>>>(k);
+            else expert_linear_kernel<BM, WM, WN, NS, false, true, false><<<g, t, 0, stream>>>(k);
+        }
     } else {
-        if (gated) expert_linear_kernel<BM, WM, NS, false, false, true><<<g, t, 0, stream>>>(k);
-        else expert_linear_kernel<BM, WM, NS, false, false, false><<<g, t, 0, stream>>>(k);
+        if (gated) expert_linear_kernel<BM, WM, WN, NS, false, false, true><<<g, t, 0, stream>>>(k);
+        else expert_linear_kernel<BM, WM, WN, NS, false, false, false><<<g, t, 0, stream>>>(k);
     }
     return hipGetLastError();
 }
@@ -680,9 +701,24 @@ hipError_t launch_expert_linear(const LinearArgs &a, hipStream_t stream) {
     // stages does (3.14 against 3.26 ms; 2.95 against 2.50 ms at 64 rows); from 160
     // rows on the matrix instructions decide and the 256-row tile is the faster.
     const int64_t avg = a.seg.pairs / a.seg.E;
+    // A step of a small tile takes a workgroup hardly less time than one of a large
+    // tile (0.3 against 0.4 to 1 us: LDS reads and a barrier's round trip), so while
+    // the 64 x 64 tiles all run at once, two on a compute unit, they are the faster:
+    // 16 experts of 7168 x 256, bf16, 1024 rows 80 and 41 us, 4096 rows 118 and 46
+    // us; with twice as many tiles they lose (4 experts of 7168 x 4096, 1024 rows,
+    // 127 and 151 us).
+    if (!a.transposed) {
+        const int per_small = gated ? 32 : 64;
+        const int64_t cols = (k.m + per_small - 1) / per_small;
+        const int64_t live = std::max<int64_t>(1, std::min<int64_t>(a.seg.pairs, a.seg.E));
+        if (live * ((a.seg.pairs / live + 63) / 64) * cols <= 512) {
+            k.col_tiles = (int)cols;
+            return launch_bm<64, 4, 1, 4>(a, k, gated, stream);
+        }
+    }
     if (avg > 160) return launch_wide(a, k, gated, stream);
-    if (avg > 112) return launch_bm<192, 2, 2>(a, k, gated, stream);
-    return launch_bm<128, 2, 3>(a, k, gated, stream);
+    if (avg > 112) return launch_bm<192, 2, 4, 2>(a, k, gated, stream);
+    return launch_bm<128, 2, 4, 3>(a, k, gated, stream);
 }
 
 }  // namespace ep

@@ -134,6 +134,22 @@ def test_rows_per_expert(gpu, T, kind):
         check(gpu, lay, rows, x, w, act, b, res, transposed=tr, checkpoint=True)
 
 
+@pytest.mark.parametrize("T", [100, 260, 300, 400])
+@pytest.mark.parametrize("kind,k", [("bf16", 8), ("bf16", 72), ("bf16", 640), ("fp8", 128), ("fp8", 640)])
+def test_rows_per_expert_of_many_columns(gpu, T, kind, k):
+    """As above with more 64 x 64 tiles than run at once: the larger tiles."""
+    announce("linear rows per expert, many columns", T, kind, k)
+    g = torch.Generator(device=DEV).manual_seed(T)
+    idx = torch.randint(0, 5, (T, 2), generator=g, device=DEV)
+    idx = torch.where(idx >= 3, torch.where(idx == 3, 0, -1), idx)
+    for act, n in (("none", 8264), ("swiglu", 16448)):
+        lay, rows, x, w, g = make(gpu, T, 4, 2, k, n, fp8=kind == "fp8", idx=idx)
+        m = n // 2 if act == "swiglu" else n
+        b = torch.randn((4, n), generator=g, device=DEV).bfloat16()
+        res = torch.randn((rows, m), generator=g, device=DEV).bfloat16()
+        check(gpu, lay, rows, x, w, act, b, res, checkpoint=n % 32 == 0)
+
+
 @pytest.mark.parametrize("E", [1, 300, 700, 4096])
 def test_many_experts_most_of_them_empty(gpu, E):
     announce("linear experts", E)
