@@ -37,6 +37,23 @@ def test_wgrad_fp8_rows(gpu, T, E, K, n, k):
     check_wgrad(gpu, lay, rows, dy, gpu.ep_cast_fp8(x, 128, scale_fmt="ue8m0"), g)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("n,k", [(2056, 1000), (1024, 2176)])
+def test_wgrad_of_large_outputs(gpu, n, k, fp8):
+    """At least 256 tiles of 256 x 256, of experts with no, one, and many rows."""
+    if fp8:
+        k = (k + 127) // 128 * 128
+    announce("wgrad large", n, k, fp8)
+    counts = [0, 1, 63, 64, 65, 400, 1000, 1700]
+    idx = torch.cat([torch.full((c,), e, dtype=torch.int64) for e, c in enumerate(counts)])
+    idx = idx[torch.randperm(len(idx), generator=torch.Generator().manual_seed(n))].unsqueeze(1).to(DEV)
+    lay, rows, x, _, g = make(gpu, len(idx), len(counts), 1, k, 8, idx=idx)
+    if fp8:
+        x = gpu.ep_cast_fp8(x, 128, scale_fmt="ue8m0")
+    dy = torch.randn((rows, n), generator=g, device=DEV).bfloat16()
+    check_wgrad(gpu, lay, rows, dy, x, g)
+
+
 def check_wgrad(gpu, lay, rows, dy, x, g):
     E, n = lay.num_experts, dy.shape[1]
     k = (x[0] if isinstance(x, tuple) else x).shape[1]
