@@ -139,7 +139,7 @@ __device__ __forceinline__ void dma16(const ep_i32x4 &rsrc, uint32_t lds, uint32
 // J = 0, 1, 2, 3 in this order: J = 0 sets the LDS address, and the instruction
 // offset J * 1024 moves both addresses, so the caller's voff is kDmaBias - J *
 // 1024 more than the source's and its buffer starts kDmaBias early (biased_buffer).
-constexpr uint32_t kDmaBias = 3072;
+constexpr uint32_t kDmaBias = 3 * 1024;
 __device__ __forceinline__ ep_i32x4 biased_buffer(const void *p, uint32_t bytes) {
     return buffer_of((const uint8_t *)p - kDmaBias, bytes + kDmaBias);
 }
