@@ -13,8 +13,9 @@
 // First kernel: a workgroup takes one expert and 16 columns of h (16 gate and
 // 16 up rows of W1); its four waves split the sum over the hidden channels and
 // add up in LDS in wave order.
-// Second kernel: a workgroup takes 32 channels of the output and all pairs (h is
-// read once per workgroup; 16 channels read it twice as often: 128 tokens of fp8
+// Second kernel: a workgroup takes 32 channels of the output and all pairs, or,
+// where the output has few channels, those of a run of tokens (h is read once per
+// workgroup; 16 channels read it twice as often: 128 tokens of fp8
 // weights took 1026 us against 773): its waves take the chosen experts in turn,
 // every pair's 32 sums go to LDS in fp32, and the tokens' weighted sums are
 // formed from there in ascending k, as ep_combine forms them: no atomics, no
@@ -22,8 +23,8 @@
 // tokens of the batch.
 //
 // hidden 7168, intermediate 2048, 256 experts, 8 per token, gated, both kernels:
-//   bf16  1 token  126 us (5.6 TB/s of weights)   128 tokens 3714 us (6.0 TB/s)
-//   fp8   1 token   73 us (4.8 TB/s)              128 tokens 2065 us (5.4 TB/s)
+//   bf16  1 token  126 us (5.6 TB/s of weights)   128 tokens 3700 us (6.0 TB/s)
+//   fp8   1 token   73 us (4.8 TB/s)              128 tokens 2090 us (5.3 TB/s)
 // where a kernel that only reads reaches 6.1 TB/s.  One token: 0.35 GB of fp8
 // weights are 58 us, two launches and their first loads the rest.
 #include <algorithm>
