@@ -612,13 +612,13 @@ __global__ __launch_bounds__(256, 1) void expert_linear_wide_kernel(LinearK a) {
             each<4>([&](auto jj) {
                 constexpr int J = decltype(jj)::value;
                 const uint32_t past = (cs ^ ((J & 1) * 4)) * 8 >= left ? kOutOfRange : 0;
-                range_of(0, 1, x_bytes + kDmaBias, steps * 128, xb, &xs_off);
+                if (J == 0) range_of(0, 1, x_bytes + kDmaBias, steps * 128, xb, &xs_off);
                 dma16_of4<J>(xb, lds0 + (2 + t) * kRegion, xoff[t][J] | past, xs_off);
             });
             each<4>([&](auto jj) {
                 constexpr int J = decltype(jj)::value;
                 const uint32_t past = !WT && (cs ^ ((J & 1) * 4)) * 8 >= left ? kOutOfRange : 0;
-                range_of(0, 1, w_bytes + kDmaBias, steps * w_step, wb, &ws_off);
+                if (J == 0) range_of(0, 1, w_bytes + kDmaBias, steps * w_step, wb, &ws_off);
                 dma16_of4<J>(wb, lds0 + t * kRegion, woff[t][J] | past, ws_off);
             });
         });

@@ -319,6 +319,7 @@ __global__ __launch_bounds__(256, 1) void expert_wgrad_wide_kernel(WgradK a) {
     // the buffer of a step's rows: offsets stay in 32 bits, and rows behind the
     // last (all of them behind the last step) read as zeros
     uint32_t region1 = 0;             // byte offset of region 1, 0 in an empty buffer
+    uint32_t from = 0;                // of the region being copied
     auto rows_of = [&](const uint8_t *p, int s, uint32_t row_bytes, uint32_t early) {
         const int left = max(0, min(kRows, rows - s * kRows));
         ep_i32x4 b = buffer_of(p + ((int64_t)row0 + s * kRows) * row_bytes - early, left * row_bytes + early);
@@ -331,14 +332,20 @@ __global__ __launch_bounds__(256, 1) void expert_wgrad_wide_kernel(WgradK a) {
     ep_i32x4 yb, xb;
     auto copy_y = [&](int s, int stage, int t, auto j) {
         constexpr int J = decltype(j)::value;
-        if (J == 0) yb = rows_of(a.dy, s, (uint32_t)N * 2, kDmaBias);
-        dma16_of4<J>(yb, lds0 + (stage * 2 + t) * kRegion, yoff[J], t ? region1 : 0);
+        if (J == 0) {
+            yb = rows_of(a.dy, s, (uint32_t)N * 2, kDmaBias);
+            from = t ? region1 : 0;
+        }
+        dma16_of4<J>(yb, lds0 + (stage * 2 + t) * kRegion, yoff[J], from);
     };
     auto copy_x = [&](int s, int stage, int t, auto j) {
         constexpr int J = decltype(j)::value;
         if (FP8) return;
-        if (J == 0) xb = rows_of(a.x, s, (uint32_t)K * 2, kDmaBias);
-        dma16_of4<J>(xb, xlds0 + (stage * 2 + t) * kRegion, xoff[J], t ? region1 : 0);
+        if (J == 0) {
+            xb = rows_of(a.x, s, (uint32_t)K * 2, kDmaBias);
+            from = t ? region1 : 0;
+        }
+        dma16_of4<J>(xb, xlds0 + (stage * 2 + t) * kRegion, xoff[J], from);
     };
     // a raw step: 16 KB of codes, and per wave 64 scale bytes (a dword each)
     auto copy_raw = [&](int s, auto j) {
@@ -349,8 +356,9 @@ __global__ __launch_bounds__(256, 1) void expert_wgrad_wide_kernel(WgradK a) {
             const ep_i32x4 sb = rows_of(a.x_scales, s, (uint32_t)groups, 0);
             dma1(sb, at + kRaw + wave * 256, soff, 0);
             xb = rows_of(a.x, s, (uint32_t)K, kDmaBias);
+            from = 0;
         }
-        dma16_of4<J>(xb, at + wave * 4096, xoff[J], 0);
+        dma16_of4<J>(xb, at + wave * 4096, xoff[J], from);
     };
     // raw codes of step s to region t: a thread's 32 channels of one row, in
     // four pieces of 8
