@@ -121,29 +121,29 @@ constexpr uint32_t kOutOfRange = 0x80000000u;   // no buffer here is longer
 // out of the buffer's range write zeros.  Asynchronous: the data is in LDS
 // after a wait on the vector memory count (dma_wait).  There is no output
 // register, so nothing the compiler could reuse too early; it does not know of
-// the copy, and the waits below carry the order.  (m0, the LDS address, is
-// reserved: the compiler keeps nothing in it.)  The wait states are the copy's
-// own, since the compiler does not look into the statement: one after the write
-// of m0, and five where a vector instruction (a broadcast, a reload of a spilled
-// scalar) has just written the descriptor or the offset.
+// the copy, and the waits below carry the order.  m0, the LDS address, is an
+// operand: whatever is compiled between two copies, each finds its own there (the
+// compiler leaves out the writes that change nothing).  The wait states are the
+// copy's own, since the compiler does not look into the statement: one after a
+// write of m0, and five where a vector instruction (a broadcast, a reload of a
+// spilled scalar) has just written the descriptor or the offset.
 __device__ __forceinline__ void dma16(const ep_i32x4 &rsrc, uint32_t lds, uint32_t voff,
                                       uint32_t soff) {
     ep_i32x4 r;
     for (int i = 0; i < 4; ++i) r[i] = wave_uniform(rsrc[i]);
     asm volatile(
-        "s_mov_b32 m0, %0\n\t"
         "s_nop 4\n\t"
-        "buffer_load_dwordx4 %1, %2, %3 offen lds"
+        "buffer_load_dwordx4 %0, %1, %2 offen lds"
         :
-        : "s"(wave_uniform((int)lds)), "v"(voff), "s"(r), "s"(wave_uniform((int)soff)));
+        : "v"(voff), "s"(r), "s"(wave_uniform((int)soff)), "{m0}"(wave_uniform((int)lds)));
 }
 
 // The same for four copies to consecutive kilobytes of LDS, one call each with
-// J = 0, 1, 2, 3 in this order: J = 0 sets the LDS address, and the instruction
+// J = 0, 1, 2, 3 in this order and the first one's LDS address: the instruction
 // offset J * 1024 moves both addresses, so the caller's voff is kDmaBias - J *
 // 1024 more than the source's and its buffer starts kDmaBias early (biased_buffer).
-// The first waits for the scalar operands, the others take them from it: there a
-// wait of their own cost 3% of a large product.
+// The first waits for the descriptor and the offset, the others take them from it:
+// there a wait of five states cost 3% of a large product.
 constexpr uint32_t kDmaBias = 3 * 1024;
 __device__ __forceinline__ ep_i32x4 biased_buffer(const void *p, uint32_t bytes) {
     return buffer_of((const uint8_t *)p - kDmaBias, bytes + kDmaBias);
@@ -171,15 +171,15 @@ __device__ __forceinline__ void dma16_of4(ep_i32x4 &rsrc, uint32_t lds, uint32_t
         ep_i32x4 r;
         for (int i = 0; i < 4; ++i) r[i] = wave_uniform(rsrc[i]);
         uint32_t o = wave_uniform((int)soff);
-        asm volatile("s_mov_b32 m0, %2\n\ts_nop 4\n\tbuffer_load_dwordx4 %3, %0, %1 offen lds"
+        asm volatile("s_nop 4\n\tbuffer_load_dwordx4 %2, %0, %1 offen lds"
                      : "+s"(r), "+s"(o)
-                     : "s"(wave_uniform((int)lds)), "v"(voff));
+                     : "v"(voff), "{m0}"(wave_uniform((int)lds)));
         rsrc = r;
         soff = o;
     } else {
-        asm volatile("buffer_load_dwordx4 %2, %0, %1 offen offset:%3 lds"
+        asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %2, %0, %1 offen offset:%3 lds"
                      : "+s"(rsrc), "+s"(soff)
-                     : "v"(voff), "n"(J * 1024));
+                     : "v"(voff), "n"(J * 1024), "{m0}"(wave_uniform((int)lds)));
     }
 }
 
@@ -188,11 +188,10 @@ __device__ __forceinline__ void dma1(const ep_i32x4 &rsrc, uint32_t lds, uint32_
     ep_i32x4 r;
     for (int i = 0; i < 4; ++i) r[i] = wave_uniform(rsrc[i]);
     asm volatile(
-        "s_mov_b32 m0, %0\n\t"
         "s_nop 4\n\t"
-        "buffer_load_ubyte %1, %2, %3 offen lds"
+        "buffer_load_ubyte %0, %1, %2 offen lds"
         :
-        : "s"(wave_uniform((int)lds)), "v"(voff), "s"(r), "s"(wave_uniform((int)soff)));
+        : "v"(voff), "s"(r), "s"(wave_uniform((int)soff)), "{m0}"(wave_uniform((int)lds)));
 }
 
 // All but the newest N copies of this wave have landed, and its own LDS reads

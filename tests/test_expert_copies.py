@@ -31,6 +31,18 @@ extern "C" __global__ void fresh_descriptor(const uint64_t *p, const int *n, uin
     dma16_of4<2>(four, 0x3000, v, soff);
     dma16_of4<3>(four, 0x3000, v, soff);
 }
+
+// other copies between the first and the others of four
+extern "C" __global__ void other_copies_between(const void *p, int n, uint32_t v) {
+    ep_i32x4 r = buffer_of(p, n);
+    uint32_t soff = 0;
+    dma16_of4<0>(r, 0x1000, v, soff);
+    dma1(r, 0x2000, v, 0);
+    dma16_of4<1>(r, 0x1000, v, soff);
+    dma16(r, 0x3000, v, 0);
+    dma16_of4<2>(r, 0x1000, v, soff);
+    dma16_of4<3>(r, 0x1000, v, soff);
+}
 """
 
 
@@ -95,6 +107,18 @@ def test_scalars_from_vector_instructions_are_waited_for(kernels):
     code = kernels["fresh_descriptor"]
     assert any(line.startswith("v_readfirstlane") for line in code)
     assert check_waits(code) == 6
+
+
+def test_every_copy_finds_its_own_lds_address(kernels):
+    scalars, seen = {}, []
+    for line in kernels["other_copies_between"]:
+        m = re.match(r"s_mov(?:k_i32|_b32) (\w+), (\w+)$", line)
+        if m:
+            to, what = m.groups()
+            scalars[to] = int(what, 0) if what[0].isdigit() else scalars.get(what)
+        elif is_copy(line):
+            seen.append(scalars.get("m0"))
+    assert seen == [0x1000, 0x2000, 0x1000, 0x3000, 0x1000, 0x1000]
 
 
 @pytest.mark.parametrize("name", ["ep_expert_linear", "ep_expert_wgrad"])
