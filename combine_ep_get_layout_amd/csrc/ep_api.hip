@@ -643,6 +643,7 @@ int ep_expert_activation_backward(const void *dh, const void *pre, const uint8_t
     a.total_rows = layout->expert_offset + p->num_experts;
     a.status = layout->status;
     a.num_rows = rows;
+    a.entries = p->max_recv_rows;
     a.dh = dh;
     a.pre = pre;
     a.pre_scales = pre_scales;

@@ -61,10 +61,11 @@ struct WgradArgs {
 hipError_t launch_expert_wgrad(const WgradArgs &a, hipStream_t stream);
 
 struct ActBackwardArgs {
-    const int32_t *src_of_slot;  // [num_rows] >= 0 where a row holds a pair
+    const int32_t *src_of_slot;  // [entries] >= 0 where a row holds a pair
     const int32_t *total_rows;   // rows in use
     int32_t *status;
-    int64_t num_rows;
+    int64_t num_rows;            // rows of the buffers, at most `entries`
+    int64_t entries;
     const void *dh;              // bf16 [num_rows, m]
     const void *pre;             // bf16 or e4m3 [num_rows, n]
     const uint8_t *pre_scales;   // [num_rows, n/32] when pre is e4m3, else NULL

@@ -53,8 +53,15 @@ __global__ __launch_bounds__(256) void act_backward_kernel(ActK k) {
     const ActBackwardArgs &a = k.a;
     const int lane = threadIdx.x & 63;
     const int64_t used = *a.total_rows;
-    if (used > a.num_rows && blockIdx.x == 0 && threadIdx.x == 0)
-        atomicOr(a.status, kDevRecvOverflow);
+    if (used > a.num_rows) {
+        // rows that the buffers lack: only those that hold a pair are missed
+        const int64_t end = used < a.entries ? used : a.entries;
+        bool missed = used > a.entries;                // as the layout itself reports it
+        for (int64_t r = a.num_rows + (int64_t)blockIdx.x * 256 + threadIdx.x; r < end;
+             r += (int64_t)gridDim.x * 256)
+            missed |= a.src_of_slot[r] >= 0;
+        if (missed) atomicOr(a.status, kDevRecvOverflow);
+    }
     const int64_t rows = used < a.num_rows ? used : a.num_rows;
     const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
     if (row >= rows || a.src_of_slot[row] < 0) return;
