@@ -32,7 +32,7 @@ __device__ __forceinline__ int segment_rows(const SegmentRows &s, int e, int *ro
     const int c = min(s.counts[e], have);
     *row0 = o;
     const int64_t room = s.num_rows - o;
-    if (c > room) {
+    if (c > 0 && c > room) {    // an empty segment may begin behind the buffers
         atomicOr(s.status, kDevRecvOverflow);
         return room > 0 ? (int)room : 0;
     }

@@ -77,3 +77,14 @@ def test_buffers_that_end_inside_the_pairs(gpu, op, short):
     lay = layout(gpu, [20, 3, 37, 5])
     last = int(lay.expert_offset[3]) + 5
     assert run(gpu, op, lay, last - short) == gpu.EP_DEV_RECV_OVERFLOW
+
+
+@pytest.mark.parametrize("op", OPS)
+def test_experts_without_rows_behind_the_buffers(gpu, op):
+    """The last pair is expert 1's; experts 2 and 3 begin behind its padding."""
+    announce("expert status, empty experts behind the buffers", op)
+    lay = layout(gpu, [20, 3, 0, 0])
+    last = int(lay.expert_offset[1]) + 3
+    assert last < int(lay.expert_offset[2])
+    assert run(gpu, op, lay, last) == 0
+    assert run(gpu, op, lay, last - 1) == gpu.EP_DEV_RECV_OVERFLOW
