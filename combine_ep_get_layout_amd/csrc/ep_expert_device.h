@@ -308,7 +308,9 @@ __device__ __forceinline__ void act_both(float z, int kind, float *f, float *df)
         // p = sigmoid(2 y): d/dz (z p) = p + z p (1 - p) 2 y'
         const float p = gelu_gate(z);
         *f = z * p;
-        *df = __builtin_fmaf(*f * (1.0f - p), 1.59576912f * __builtin_fmaf(0.134145f * z, z, 1.0f), p);
+        // (p is 0 or 1 long before |z| = 64: the cut keeps y' finite, and its term 0)
+        const float c = fminf(fmaxf(z, -64.0f), 64.0f);
+        *df = __builtin_fmaf(*f * (1.0f - p), 1.59576912f * __builtin_fmaf(0.134145f * c, c, 1.0f), p);
     } else {
         *f = z;
         *df = 1.0f;

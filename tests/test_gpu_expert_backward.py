@@ -178,3 +178,33 @@ def test_activation_backward_against_differences(gpu, act):
         ref.assert_near(dpre[held][:, col], num, 1e-6 * (1 + cv.abs().amax(1) * 8), what=f"col {col}")
     num = (loss(zv, wv + step) - loss(zv, wv - step)) / (2 * step)
     ref.assert_near(dw[held], num, 1e-4 * torch.ones_like(num), ref.U, "dweights")
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "swiglu", "geglu"])
+def test_activation_of_huge_values(gpu, act):
+    """From about 100 on an activation is z or 0 and its derivative 1 or 0, to the
+    last bit of fp32, up to the end of the format."""
+    announce("activation of huge values", act)
+    lay, rows, _, _, g = make(gpu, 40, 2, 1, 8, 8)
+    n, m = 64, 32 if ref.gated(act) else 64
+    z = torch.randn((rows, n), generator=g, device=DEV).bfloat16()
+    huge = torch.tensor([100.0, 1e10, 2e19, 6e19, 1e20, 1e30, 3e38], device=DEV).bfloat16()
+    z[:, :7], z[:, 7:14] = huge, -huge
+    dh = (torch.randn((rows, m), generator=g, device=DEV) * 2.0 ** -10).bfloat16()
+    if ref.gated(act):
+        z[:, 32:46] = 1.0
+    dpre, h, dw = gpu.ep_expert_activation_backward(dh, z, lay, act)
+    held = held_rows(lay, rows)
+    assert torch.equal(dpre[held][:, :7], dh[held][:, :7])
+    assert (dpre[held][:, 7:14] == 0).all()
+    assert torch.equal(h[held][:, :7], z[held][:, :7]) and (h[held][:, 7:14] == 0).all()
+    if ref.gated(act):
+        assert torch.equal(dpre[held][:, 32:39], (dh[held][:, :7].double() * huge.double()).bfloat16())
+        assert (dpre[held][:, 39:46] == 0).all()
+    assert torch.isfinite(dw[held]).all() and torch.isfinite(dpre[held].float()).all()
+    # and forward, from the product's sums
+    x = torch.zeros((rows, n), device=DEV, dtype=torch.bfloat16)
+    x[:] = z
+    w = torch.eye(n, device=DEV).bfloat16().expand(2, n, n).contiguous()
+    out, _ = gpu.ep_expert_linear(x, w, lay, activation=act)
+    assert torch.equal(out[held][:, :7], huge.expand(int(held.sum()), 7)) and (out[held][:, 7:14] == 0).all()
