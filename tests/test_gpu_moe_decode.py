@@ -164,3 +164,45 @@ def test_against_the_dispatched_path(gpu):
     grow = (h[:R].double().abs().amax() * ref.value(w2).abs().sum(2).amax()
             + 2 * y[:R].double().abs().amax())
     ref.assert_near(path, want, err + ref.BF16_HALF * w.double().sum(1, keepdim=True) * grow)
+
+
+# From 4104 channels on, the second kernel has more than 128 column tiles and one
+# workgroup of it takes every token: an expert's pairs then meet in one wave.
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("inter", [128, 384])
+def test_pairs_per_expert_in_one_workgroup(gpu, inter, fp8):
+    """No, one, two and three passes of up to 16 pairs of an expert, of one and two
+    groups of 8; more experts than waves, some behind each other in one wave."""
+    announce("decode pairs per expert, one workgroup", inter, fp8)
+    counts = [0, 1, 7, 8, 9, 15, 16, 17, 1, 0, 24, 25, 32, 33, 2, 8, 9, 16, 3]
+    idx = torch.cat([torch.full((n,), e, dtype=torch.int64) for e, n in enumerate(counts)])
+    order = torch.randperm(len(idx), generator=torch.Generator().manual_seed(inter))
+    x, idx, w, w1, w2, *_, out = check(gpu, len(idx), len(counts), 1, 4224 if fp8 else 4104, inter,
+                                       fp8=fp8, idx=idx[order].unsqueeze(1).to(DEV))
+    for t in range(0, len(idx), 13):
+        one = gpu.ep_moe_decode(x[t:t + 1], idx[t:t + 1], w[t:t + 1], w1, w2)
+        assert torch.equal(one[0].view(torch.int16), out[t].view(torch.int16))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("T", [4, 8, 9, 17, 100])
+def test_all_tokens_on_one_expert_in_one_workgroup(gpu, T, fp8):
+    announce("decode one expert, one workgroup", T, fp8)
+    idx = torch.full((T, 2), 3, device=DEV, dtype=torch.int64)
+    idx[::3, 1] = 1
+    x, idx, w, w1, w2, *_, out = check(gpu, T, 5, 2, 4224 if fp8 else 4104, 128, fp8=fp8, idx=idx,
+                                       act="geglu")
+    for t in (0, T // 2, T - 1):
+        one = gpu.ep_moe_decode(x[t:t + 1], idx[t:t + 1], w[t:t + 1], w1, w2, "geglu")
+        assert torch.equal(one[0].view(torch.int16), out[t].view(torch.int16))
+
+
+@pytest.mark.parametrize("T,E,K,inter", [(1024, 4, 1, 64), (128, 4096, 8, 8)])
+def test_the_most_pairs_in_one_workgroup(gpu, T, E, K, inter):
+    """256 pairs of an expert, and the most local memory that the second kernel takes."""
+    announce("decode most pairs, one workgroup", T, E, K, inter)
+    x, idx, w, w1, w2, b1, b2, rs, out = check(gpu, T, E, K, 4104, inter, biases=True, res=1)
+    for t in (0, T // 2, T - 1):
+        one = gpu.ep_moe_decode(x[t:t + 1], idx[t:t + 1], w[t:t + 1], w1, w2, "swiglu", b1, b2,
+                                rs[0][t:t + 1])
+        assert torch.equal(one[0].view(torch.int16), out[t].view(torch.int16))
