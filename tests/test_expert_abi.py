@@ -140,3 +140,30 @@ def test_binding_refuses_host_tensors():
         ep.ep_expert_activation_backward(x, x, lay)
     with pytest.raises(ValueError):
         ep.ep_moe_decode(x, torch.zeros((8, 2), dtype=torch.int64), None, w, w)
+
+
+def test_decode_workspace_holds_both_parts_of_h():
+    """Two bf16 parts an element; sizes whose rounding up cannot hide a missing part."""
+    f = _abi.load().ep_moe_decode_workspace_bytes
+    for T, K, inter in [(1, 1, 256), (1, 1, 1000), (4, 2, 128), (7, 3, 1408), (128, 8, 2048),
+                        (1024, 1, 1 << 20)]:
+        assert f(T, K, inter) >= 4 * T * K * inter
+        assert decode(T=T, K=K, I=inter // 8 * 8, nb=4 * T * K * (inter // 8 * 8) - 1) in (WS, UNS)
+
+
+def test_binding_names_the_activation_it_does_not_know():
+    import torch
+
+    import combine_ep_get_layout_amd as ep
+    lay = ep.Layout(_params(4, 2, 4), torch.device("cpu"))
+    x = torch.zeros((8, 64), dtype=torch.bfloat16)
+    w = torch.zeros((4, 64, 64), dtype=torch.bfloat16)
+    idx = torch.zeros((8, 2), dtype=torch.int64)
+    for call in (lambda: ep.ep_expert_linear(x, w, lay, activation="tanh"),
+                 lambda: ep.ep_expert_activation_backward(x, x, lay, activation="tanh"),
+                 lambda: ep.ep_moe_decode(x, idx, None, w, w, activation="tanh")):
+        with pytest.raises(ValueError, match="activation must be one of"):
+            call()
+    # known names get past that check, to the tensors
+    with pytest.raises(ValueError, match="GPU tensor"):
+        ep.ep_expert_linear(x, w, lay, activation="gelu")
