@@ -948,7 +948,12 @@ def ep_expert_activation_backward(dh: torch.Tensor,
     recv_topk_weights; 1 if None).  Returns (dpre bf16 [rows, N], row_weights *
     h bf16 [rows, M], dweights float32 [rows] = sum of dh * h).  Padding rows
     are left as they were; `out` may name the three buffers (None entries are
-    allocated)."""
+    allocated).
+
+    With dh from the dispatched gradient dout of the layer, dweights is the
+    gradient of the routing weights of y = w2 h.  Where y also has a bias b2,
+    add (dout rows * b2[e]).sum(1); b2's own gradient is db of an
+    ep_expert_wgrad over the dout rows times row_weights."""
     lib = load_library()
     act, gated = _activation(activation)
     scales = None

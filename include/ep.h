@@ -497,7 +497,11 @@ int ep_expert_wgrad(const void *dy, const void *x, int x_dtype, const uint8_t *x
  *   gradient multiplies);  dweights[r] = sum_i dh[r,i] h[r,i] (fp32).
  * Where the combine's gradient rows are dispatched as they are (ep_dispatch of
  * dL/dout) and taken through the down product's data gradient, these are the
- * gradients of z and of the routing weights.
+ * gradients of z and, with a down product y = W2 h without a bias, of the routing
+ * weights.  With y = W2 h + b2 a row's weight also multiplies b2: its gradient
+ * is dweights[r] + sum_c dL/dout[r,c] b2[e,c], which the caller adds; and b2's is
+ * the sum of row_weights[r] * dL/dout[r] over the expert's rows, db of an
+ * ep_expert_wgrad whose dy are the rows so weighted (not of the rows as they are).
  *
  *   dh         device bf16 [num_rows, m], m = n (n/2 for a gated activation);
  *              16-byte aligned.

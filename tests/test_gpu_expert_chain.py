@@ -183,3 +183,51 @@ def test_graph_replays_match_eager(gpu):
         torch.cuda.synchronize()
         for i, (a, b) in enumerate(zip(seen, want)):
             assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), i
+
+
+@pytest.mark.parametrize("T,E,K,A", [(150, 4, 2, 16), (900, 3, 2, 128)])
+def test_gradients_behind_a_down_bias(gpu, T, E, K, A):
+    """out = sum_k w (W2 h + b2): the routing weights' gradient needs b2's term, and
+    b2's own is the column sum of the weighted gradient rows."""
+    announce("chain with a down bias", T, E, K, A)
+    H, inter = 256, 192
+    g = torch.Generator(device=DEV).manual_seed(T)
+    idx = routing(T, E, K, T)
+    w = torch.rand((T, K), generator=g, device=DEV)
+    x = torch.randn((T, H), generator=g, device=DEV).bfloat16()
+    w1 = (torch.randn((E, 2 * inter, H), generator=g, device=DEV) * H ** -0.5).bfloat16()
+    w2 = (torch.randn((E, H, inter), generator=g, device=DEV) * inter ** -0.5).bfloat16()
+    b2 = torch.randn((E, H), generator=g, device=DEV).bfloat16()
+    dout = torch.randn((T, H), generator=g, device=DEV).bfloat16()
+
+    lay = gpu.ep_get_layout(idx, E, A)
+    recv, _, rw = gpu.ep_dispatch(x, lay, w, zero_padding=True)
+    _, kept = gpu.ep_expert_linear(recv, w1, lay, activation="swiglu", checkpoint=True)
+    drow, _, _ = gpu.ep_dispatch(dout, lay, zero_padding=True)
+    dh, _ = gpu.ep_expert_linear(drow, w2, lay, transposed=True)
+    _, _, dweights = gpu.ep_expert_activation_backward(dh, kept, lay, "swiglu", rw)
+    weighted = (drow.float() * rw.unsqueeze(1)).bfloat16()
+    _, db2 = gpu.ep_expert_wgrad(weighted, recv, lay, bias_grad=True)
+
+    z8 = ref.value(kept)
+    missing = 0.0
+    for e, a, b in ref.spans(lay, lay.max_recv_rows):
+        pair = lay.src_of_slot.long()[a:b]
+        t, wt = pair // K, w.flatten()[pair].double().unsqueeze(1)
+        de, bias = dout[t].double(), b2[e].double()
+        f = ref.f_df(z8[a:b, :inter], "swiglu")[0]
+        h = f * z8[a:b, inter:]
+        # L = sum_r w_r dout_r . (W2 h_r + b2)
+        want = (de * (h @ w2[e].double().T + bias)).sum(1)
+        dhe = Bounded(de).product(w2[e].double()).rounded()
+        err = dhe.times(Bounded(h, 4 * ref.ACT_U * h.abs())).e.sum(1)
+        err += inter * ref.U * (dhe.v * h).abs().sum(1) + (H + 2) * ref.U * (de * bias).abs().sum(1)
+        term = (drow[a:b].float() * b2[e].float()).sum(1)
+        # the sum of the two: one more rounding, of the first relative to itself
+        err += ref.U * ((dhe.v * h).sum(1).abs() + (de * bias).sum(1).abs())
+        ref.assert_near(dweights[a:b] + term, want, err, ref.U, "routing weights")
+        missing = max(missing, ((dweights[a:b].double() - want).abs() - err).max().item() if b > a else 0.0)
+        ref.assert_near(db2[e], (wt * de).sum(0),
+                        (ref.BF16_HALF + (b - a + 1) * ref.U) * (wt * de).abs().sum(0) * (1 + ref.BF16_HALF),
+                        ref.U, "db2")
+    assert missing > 1.0                               # the term matters here
