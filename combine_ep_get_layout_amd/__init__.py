@@ -836,7 +836,8 @@ def ep_expert_linear(x: Union[torch.Tensor, Tuple[torch.Tensor, torch.Tensor]],
     "swiglu" / "geglu" on z = [gate | up].  residual: bf16 like out.
     checkpoint=True (or the two buffers) also keeps z in 8 bits: (e4m3 codes
     [rows, N], UE8M0 scales uint8 [rows, N/32]) for
-    ep_expert_activation_backward.  Returns (out bf16 [rows, N or N/2],
+    ep_expert_activation_backward (fp8 rows are then multiplied exactly, at the
+    bf16 products' rate).  Returns (out bf16 [rows, N or N/2],
     checkpoint or None).  Padding rows are left as they were."""
     lib = load_library()
     act, gated = _activation(activation)

@@ -433,8 +433,9 @@ int ep_combine_logfmt(const void *payload, int32_t hidden, int64_t num_y_rows,
  * expert_offset and status are used (ep_expert_activation_backward:
  * src_of_slot, expert_offset and status).  bf16 products are exact and summed
  * in fp32; the fp8 instruction adds into fp32 too, but cuts products below
- * 2^-13 of the largest of their 8 channels.  Results do not depend on the
- * other experts' rows, and two calls on the same inputs give the same bits. */
+ * 2^-13 of the largest of their 8 channels (ep_expert_linear with a checkpoint
+ * does without it: see there).  Results do not depend on the other experts'
+ * rows, and two calls on the same inputs give the same bits. */
 
 /* ep_expert_linear - the experts' matrix product with its epilogue:
  * z[r] = W[e] x[r] + bias[e];  out[r] = act(z[r]) + residual[r], rounded once
@@ -460,6 +461,9 @@ int ep_combine_logfmt(const void *payload, int32_t hidden, int64_t num_y_rows,
  *              [num_rows, n/32], or both NULL: z kept in 8 bits for
  *              ep_expert_activation_backward: e4m3 codes and UE8M0 scales per
  *              32 channels, the format of ep_cast_fp8, taken from the fp32 z.
+ *              Of fp8 rows z is then summed from exact products too, at the bf16
+ *              products' rate, and out may differ in its last bit from a call
+ *              without a checkpoint.
  * Errors: EP_ERR_INVALID_ARG; EP_ERR_UNSUPPORTED (fp8 with transposed, k or n
  * above EP_MAX_HIDDEN, an expert's weights of 2^31 - 4096 bytes or more). */
 int ep_expert_linear(const void *x, int x_dtype, const uint8_t *x_scales, const void *w,

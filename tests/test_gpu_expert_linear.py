@@ -252,3 +252,43 @@ def test_other_streams_at_once(gpu):
     for g, v, (lay, *_) in zip(got, want, jobs):
         R = lay.num_recv_rows()
         assert torch.equal(g[:R].view(torch.int16), v[:R].view(torch.int16))
+
+
+@pytest.mark.parametrize("T", [100, 260, 400])
+@pytest.mark.parametrize("act,n", [("none", 8256), ("swiglu", 16512), ("silu", 64)])
+@pytest.mark.parametrize("k", [128, 640])
+def test_checkpoint_of_fp8_products_keeps_the_small_ones(gpu, T, act, n, k):
+    """One product in 8 is some 2^14 times the others and cancels against the next 8
+    channels' one: z is the sum of the small ones.  With a checkpoint the products
+    are exact and their sum is off by no more than one of fp32 terms, in every tile."""
+    announce("linear fp8 checkpoint, small products", T, act, n, k)
+    E = 4
+    idx = torch.arange(T, device=DEV).remainder(3).unsqueeze(1)
+    lay = gpu.ep_get_layout(idx, E)
+    rows = lay.max_recv_rows
+    g = torch.Generator(device=DEV).manual_seed(T)
+
+    def codes(shape, sign):
+        v = torch.randint(8, 16, shape, generator=g, device=DEV).float() / 4      # 2 to 3.75
+        v = v * torch.where(torch.rand(shape, generator=g, device=DEV) < 0.3, -1.0, 1.0)
+        v[..., ::8] = 256.0
+        if sign:
+            v[..., 8::16] = -256.0
+        return v.to(torch.float8_e4m3fn)
+
+    def scales(shape):
+        return torch.randint(118, 123, shape, generator=g, device=DEV, dtype=torch.uint8)
+
+    x = (codes((rows, k), False), scales((rows, k // 128)))
+    w = (codes((E, n, k), True), scales((E, n, k // 128)))
+    b = torch.randn((E, n), generator=g, device=DEV).mul_(0.01).bfloat16()
+    out, ck = gpu.ep_expert_linear(x, w, lay, bias=b, activation=act, checkpoint=True)
+    xv, wv = ref.value(x), ref.value(w)
+    for e, lo, hi in ref.spans(lay, rows):
+        if lo == hi:
+            continue
+        z = xv[lo:hi] @ wv[e].T + b[e].double()
+        dz = (k + 1) * ref.U * (xv[lo:hi].abs() @ wv[e].T.abs()) + 2 * ref.U * z.abs()
+        ref.assert_checkpoint(ck[0][lo:hi], ck[1][lo:hi], z, dz)
+        y, dy = ref.activate(z, act, dz)
+        ref.assert_near(out[lo:hi], y, dy, what=f"rows {lo} to {hi}")
