@@ -428,14 +428,18 @@ int ep_combine_logfmt(const void *payload, int32_t hidden, int64_t num_y_rows,
  * expert e, expert_offset[e] <= r < expert_offset[e] + count, count the
  * smaller of num_tokens_per_expert[e] and the rows the segment has (fixed
  * capacity).  Padding rows are neither read nor written, whatever they hold.
- * Rows at or past num_rows, the rows the buffers have, are skipped and
- * EP_DEV_RECV_OVERFLOW is set.  Of the layout only num_tokens_per_expert,
- * expert_offset and status are used (ep_expert_activation_backward:
- * src_of_slot, expert_offset and status).  bf16 products are exact and summed
- * in fp32; the fp8 instruction adds into fp32 too, but cuts products below
- * 2^-13 of the largest of their 8 channels (ep_expert_linear with a checkpoint
- * does without it: see there).  Results do not depend on the other experts'
- * rows, and two calls on the same inputs give the same bits. */
+ * Rows that hold a pair and lie at or past num_rows, the rows the buffers have,
+ * are skipped and EP_DEV_RECV_OVERFLOW is set (with num_rows = 0
+ * ep_expert_linear and ep_expert_activation_backward return at once instead).
+ * Outputs must not overlap inputs, except as named: out may be residual, dw and
+ * db may be dw_in and db_in, dpre may be a bf16 pre and h_out may be dh.  Of the
+ * layout only num_tokens_per_expert, expert_offset and status are used
+ * (ep_expert_activation_backward: src_of_slot, expert_offset and status).
+ * bf16 products are exact and summed in fp32; the fp8 instruction adds into
+ * fp32 too, but cuts products below 2^-13 of the largest of their 8 channels
+ * (ep_expert_linear with a checkpoint does without it: see there).  Results do
+ * not depend on the other experts' rows, and two calls on the same inputs give
+ * the same bits. */
 
 /* ep_expert_linear - the experts' matrix product with its epilogue:
  * z[r] = W[e] x[r] + bias[e];  out[r] = act(z[r]) + residual[r], rounded once
@@ -535,7 +539,8 @@ size_t ep_moe_decode_workspace_bytes(int32_t num_tokens, int32_t num_topk, int32
  * act(W1[e] x[t] + b1[e]), e = topk_idx[t,k].  What dispatch, two
  * ep_expert_linear calls and ep_combine compute, in two kernels; h keeps 16
  * significant bits, the expert outputs stay in fp32 and are added in ascending
- * k (fmaf) as ep_combine adds them, so out is rounded once.  A token's result does not depend on the others.
+ * k (fmaf) as ep_combine adds them, so out is rounded once.  A token's result does
+ * not depend on the others.
  *
  *   x            device bf16 [T, H], 16-byte aligned.
  *   topk_idx     device int64 [T, K]; -1 = no expert (as is any id outside
@@ -554,7 +559,8 @@ size_t ep_moe_decode_workspace_bytes(int32_t num_tokens, int32_t num_topk, int32
  *   workspace    device, >= ep_moe_decode_workspace_bytes, 16-byte aligned;
  *                scratch of this call.
  *   status       device int32 [1] or NULL: EP_DEV_BAD_EXPERT is OR-ed in.
- *   out          device bf16 [T, H], 16-byte aligned.
+ *   out          device bf16 [T, H], 16-byte aligned; it may be res0 or res1,
+ *                and must not overlap the other inputs.
  * Errors: EP_ERR_INVALID_ARG, EP_ERR_WORKSPACE, EP_ERR_UNSUPPORTED (more
  * pairs, E above EP_MAX_EXPERTS, H or I above EP_MAX_HIDDEN, an expert's w1,
  * x or 4 T*K*I of 2^31 - 4096 bytes or more). */

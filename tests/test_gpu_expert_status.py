@@ -88,3 +88,39 @@ def test_experts_without_rows_behind_the_buffers(gpu, op):
     assert last < int(lay.expert_offset[2])
     assert run(gpu, op, lay, last) == 0
     assert run(gpu, op, lay, last - 1) == gpu.EP_DEV_RECV_OVERFLOW
+
+
+def test_buffers_without_rows(gpu):
+    """No rows at all: linear and the activation's backward return at once, the
+    status as it was; the weight gradient still writes its zeros, and reports."""
+    lay = layout(gpu, [20, 3, 37, 5])
+    x = torch.zeros((0, K), device=DEV, dtype=torch.bfloat16)
+    y = torch.zeros((0, N), device=DEV, dtype=torch.bfloat16)
+    w = torch.zeros((4, N, K), device=DEV, dtype=torch.bfloat16)
+    assert gpu.ep_expert_linear(x, w, lay)[0].shape == (0, N)
+    assert gpu.ep_expert_activation_backward(y, y, lay, "silu")[0].shape == (0, N)
+    assert lay.status.item() == 0
+    dw, db = gpu.ep_expert_wgrad(y, x, lay, bias_grad=True)
+    assert (dw == 0).all() and (db == 0).all() and lay.status.item() == gpu.EP_DEV_RECV_OVERFLOW
+
+
+def test_results_into_what_they_add_to(gpu):
+    """out may be the residual itself, dpre and h_out the bf16 z and dh."""
+    lay = layout(gpu, [200, 3, 0, 137])
+    rows = lay.max_recv_rows
+    g = torch.Generator(device=DEV).manual_seed(3)
+    held = torch.zeros(rows, dtype=torch.bool, device=DEV)
+    for _, a, b in ref.spans(lay, rows):
+        held[a:b] = True
+    new = lambda n: torch.randn((rows, n), generator=g, device=DEV).bfloat16()  # noqa: E731
+    for E_n, act in ((96, "none"), (1056, "swiglu"), (8320, "geglu")):
+        m = E_n // 2 if ref.gated(act) else E_n
+        x, res, w = new(K), new(m), torch.randn((4, E_n, K), generator=g, device=DEV).bfloat16()
+        want, _ = gpu.ep_expert_linear(x, w, lay, activation=act, residual=res)
+        got, _ = gpu.ep_expert_linear(x, w, lay, activation=act, residual=res, out=res)
+        assert got is res and torch.equal(got[held], want[held])
+        z, dh = new(E_n), new(m)
+        want = gpu.ep_expert_activation_backward(dh, z, lay, act)
+        got = gpu.ep_expert_activation_backward(dh, z, lay, act, out=(z, dh, None))
+        for p, q in zip(got, want):
+            assert torch.equal(p[held], q[held])

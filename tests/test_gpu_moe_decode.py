@@ -206,3 +206,12 @@ def test_the_most_pairs_in_one_workgroup(gpu, T, E, K, inter):
         one = gpu.ep_moe_decode(x[t:t + 1], idx[t:t + 1], w[t:t + 1], w1, w2, "swiglu", b1, b2,
                                 rs[0][t:t + 1])
         assert torch.equal(one[0].view(torch.int16), out[t].view(torch.int16))
+
+
+@pytest.mark.parametrize("H", [256, 4104])
+def test_result_into_a_residual(gpu, H):
+    x, idx, w, w1, w2, b1, b2, rs, want = check(gpu, 30, 6, 2, H, 64, biases=True, res=2)
+    for i in range(2):
+        r = [t.clone() for t in rs]
+        got = gpu.ep_moe_decode(x, idx, w, w1, w2, "swiglu", b1, b2, tuple(r), out=r[i])
+        assert got is r[i] and torch.equal(got, want)
