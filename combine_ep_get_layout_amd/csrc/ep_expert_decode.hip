@@ -24,9 +24,9 @@
 //
 // hidden 7168, intermediate 2048, 256 experts, 8 per token, gated, both kernels:
 //   bf16  1 token  126 us (5.6 TB/s of weights)   128 tokens 3700 us (6.0 TB/s)
-//   fp8   1 token   73 us (4.8 TB/s)              128 tokens 2090 us (5.3 TB/s)
-// where a kernel that only reads reaches 6.1 TB/s.  One token: 0.35 GB of fp8
-// weights are 58 us, two launches and their first loads the rest.
+//   fp8   1 token   74 us (4.8 TB/s)              128 tokens 2090 to 2220 us (5.3 to 5.0)
+// where a kernel that only reads reaches 6.4 TB/s.  One token: 0.35 GB of fp8
+// weights are 56 us, two launches and their first loads the rest.
 #include <algorithm>
 
 #include "ep_expert_device.h"

@@ -244,8 +244,8 @@ __device__ __forceinline__ void epilogue(const LinearK &a, const TileAt &at, uin
 }
 
 // Tiles of 128 or 192 rows by 256 columns, for experts of few rows: bound by
-// reading the weights (256 experts of 7168 x 4096, 128 rows each, swiglu: 3.07 ms,
-// 5.1 TB/s); tiles of 64 by 64 for small products, bound by the latency
+// reading the weights (256 experts of 7168 x 4096, 128 rows each, swiglu: 3.1 ms,
+// 5.0 TB/s); tiles of 64 by 64 for small products, bound by the latency
 // of a step.
 // The ring of NS stages keeps NS - 1 steps in flight; row tiles that hold no row
 // are not multiplied.
@@ -474,10 +474,9 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void expert_linear_kernel(LinearK 
 //
 // 8 experts, 32768 rows: 7168 to 4096 with swiglu and checkpoint 1.54 ms (1.25
 // PFLOP/s; the matrix instructions run 70 to 74% of the cycles, at the 1.6 to 1.8
-// GHz that the power allows), transposed 4096 to 7168 1.46 ms (1.32), 2048 to 7168
-// with bias and residual 0.87 ms (1.11: nine tenths of a tile's 72 us are the
-// product, the epilogue and the first copies the rest), fp8 7168 to 4096 0.80 to
-// 0.88 ms (2.2 to 2.4).  A library product of 32768 x 4096 x 7168 without an
+// GHz that the power allows), transposed 4096 to 7168 1.48 ms (1.30), 2048 to 7168
+// with bias and residual 0.86 ms (1.12: a tile takes 60 us, 45 of them its 32 steps,
+// the epilogue and the first copies the rest), fp8 7168 to 4096 0.82 ms (2.3).  A library product of 32768 x 4096 x 7168 without an
 // epilogue reaches 1.56 (bf16) and 3.2 (fp8) on the same card.
 template <int IN, bool WT, bool GATED>
 __global__ __launch_bounds__(256, 1) void expert_linear_wide_kernel(LinearK a) {
@@ -787,10 +786,14 @@ hipError_t launch_expert_linear(const LinearArgs &a, hipStream_t stream) {
     k.col_tiles = (k.m + per_tile - 1) / per_tile;
     // Row tiles by the rows an expert can expect (up to 256 experts of 7168 x 4096,
     // uniform routing).  Up to about 112 the weights' reads decide, and the deep
-    // ring of the 128-row tile reads them at 6.3 TB/s (2.4 to 2.7 ms); around 128
+    // ring of the 128-row tile reads them in 2.4 ms (16 rows, 6.3 TB/s) to 2.8 ms
+    // (110 rows, 5.5); around 128
     // half of the experts need a second 128-row tile, where one of 192 rows and two
     // stages does (3.14 against 3.26 ms; 2.95 against 2.50 ms at 64 rows); from 160
-    // rows on the matrix instructions decide and the 256-row tile is the faster.
+    // rows on the matrix instructions decide and the 256-row tile is the faster.  (The
+    // rule does not count tiles: with fewer of them than compute units, as of 4
+    // experts of 7168 x 4096 with 256 rows each, some stay idle: 126 us, of which
+    // reading the weights is 40.)
     const int64_t avg = a.seg.pairs / a.seg.E;
     // A step of a small tile takes a workgroup hardly less time than one of a large
     // tile (0.3 against 0.4 to 1 us: LDS reads and a barrier's round trip), so while

@@ -121,11 +121,14 @@ __device__ __forceinline__ void write_sum(const WgradK &a, int e, int n0, ep_f32
     }
 }
 
-// Tiles of 128 x 128, for few rows an expert: bound by writing dW, so what
-// counts is many workgroups in flight (two on a compute unit).  Four waves of 64
+// Tiles of 128 x 128, for few rows an expert or few tiles.  With few rows bound by
+// writing dW, so what counts is many workgroups in flight (two on a compute unit);
+// with many rows and few tiles by the steps of 64 rows, which one workgroup takes
+// one after another, 0.6 us each (0.9 on fp8 rows): 4096 rows an expert take 41 to
+// 44 us (60 to 64) from 4 experts of 128 x 128 to 4 of 1024 x 1024.  Four waves of 64
 // x 64, two stages.  fp8 rows pass through registers while the step before is
 // computed.  16 experts of 1408 x 1024, 129 rows each, added to fp32 gradients:
-// 36 us, 0.195 GB at 5.4 TB/s (51 us with cold caches).
+// 37 us, 0.195 GB at 5.3 TB/s (51 us with cold caches).
 constexpr int kT = 128;
 constexpr int kOperand = kRows * kT * 2;
 constexpr int kStage = 2 * kOperand;
@@ -274,8 +277,8 @@ __global__ __launch_bounds__(256, 2) void expert_wgrad_kernel(WgradK a) {
 // next step in phase A and X1 in phase B; these regions then need no second
 // stage, which makes room for three raw steps.
 //
-// 8 experts of 4096 x 7168, 32768 rows: bf16 1.57 ms (1.22 PFLOP/s), fp8 rows 1.70
-// to 1.77 (1.1).  A library product with both operands transposed reaches 1.17.
+// 8 experts of 4096 x 7168, 32768 rows: bf16 1.53 to 1.57 ms (1.22 PFLOP/s), fp8 rows
+// 1.73 to 1.80 (1.1).  A library product with both operands transposed reaches 1.17.
 constexpr int kWT = 256;
 constexpr int kRegion = kRows * 128 * 2;
 
