@@ -476,7 +476,8 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void expert_linear_kernel(LinearK 
 // PFLOP/s; the matrix instructions run 70 to 74% of the cycles, at the 1.6 to 1.8
 // GHz that the power allows), transposed 4096 to 7168 1.48 ms (1.30), 2048 to 7168
 // with bias and residual 0.86 ms (1.12: a tile takes 60 us, 45 of them its 32 steps,
-// the epilogue and the first copies the rest), fp8 7168 to 4096 0.82 ms (2.3).  A library product of 32768 x 4096 x 7168 without an
+// the epilogue and the first copies the rest), fp8 7168 to 4096 0.82 ms (2.3).  A
+// library product of 32768 x 4096 x 7168 without an
 // epilogue reaches 1.56 (bf16) and 3.2 (fp8) on the same card.
 template <int IN, bool WT, bool GATED>
 __global__ __launch_bounds__(256, 1) void expert_linear_wide_kernel(LinearK a) {
@@ -787,9 +788,8 @@ hipError_t launch_expert_linear(const LinearArgs &a, hipStream_t stream) {
     // Row tiles by the rows an expert can expect (up to 256 experts of 7168 x 4096,
     // uniform routing).  Up to about 112 the weights' reads decide, and the deep
     // ring of the 128-row tile reads them in 2.4 ms (16 rows, 6.3 TB/s) to 2.8 ms
-    // (110 rows, 5.5); around 128
-    // half of the experts need a second 128-row tile, where one of 192 rows and two
-    // stages does (3.14 against 3.26 ms; 2.95 against 2.50 ms at 64 rows); from 160
+    // (110 rows, 5.5); around 128 half of the experts need a second 128-row tile,
+    // where one of 192 rows and two stages does (3.14 against 3.26 ms; 2.95 against 2.50 ms at 64 rows); from 160
     // rows on the matrix instructions decide and the 256-row tile is the faster.  (The
     // rule does not count tiles: with fewer of them than compute units, as of 4
     // experts of 7168 x 4096 with 256 rows each, some stay idle: 126 us, of which

@@ -437,7 +437,9 @@ int ep_combine_logfmt(const void *payload, int32_t hidden, int64_t num_y_rows,
  * (ep_expert_activation_backward: src_of_slot, expert_offset and status).
  * bf16 products are exact and summed in fp32; the fp8 instruction adds into
  * fp32 too, but cuts products below 2^-13 of the largest of their 8 channels
- * (ep_expert_linear with a checkpoint does without it: see there).  Results do
+ * (ep_expert_linear with a checkpoint does without it: see there).  There, in
+ * ep_expert_wgrad and in ep_moe_decode fp8 values become bf16 on the way, which
+ * is exact for scale bytes from 10 to 246.  Results do
  * not depend on the other experts' rows, and two calls on the same inputs give
  * the same bits. */
 
@@ -466,8 +468,8 @@ int ep_combine_logfmt(const void *payload, int32_t hidden, int64_t num_y_rows,
  *              ep_expert_activation_backward: e4m3 codes and UE8M0 scales per
  *              32 channels, the format of ep_cast_fp8, taken from the fp32 z.
  *              Of fp8 rows z is then summed from exact products too, at the bf16
- *              products' rate, and out may differ in its last bit from a call
- *              without a checkpoint.
+ *              products' rate, and out differs from that of a call without a
+ *              checkpoint by what the fp8 instruction cuts.
  * Errors: EP_ERR_INVALID_ARG; EP_ERR_UNSUPPORTED (fp8 with transposed, k or n
  * above EP_MAX_HIDDEN, an expert's weights of 2^31 - 4096 bytes or more). */
 int ep_expert_linear(const void *x, int x_dtype, const uint8_t *x_scales, const void *w,

@@ -231,3 +231,51 @@ def test_gradients_behind_a_down_bias(gpu, T, E, K, A):
                         (ref.BF16_HALF + (b - a + 1) * ref.U) * (wt * de).abs().sum(0) * (1 + ref.BF16_HALF),
                         ref.U, "db2")
     assert missing > 1.0                               # the term matters here
+
+
+@pytest.mark.parametrize("byte", [10, 30, 220, 246])
+def test_scales_near_the_ends(gpu, byte):
+    """fp8 values that pass through bf16 on their way (checkpoint, weight gradient,
+    decode): smallest and largest codes under the smallest and largest scales that
+    keep them normal numbers."""
+    announce("expert scales near the ends", byte)
+    T, E, K, k, n = 300, 3, 2, 256, 128
+    g = torch.Generator(device=DEV).manual_seed(byte)
+    back = 2.0 ** (127 - byte)
+
+    def fp8(shape, b):
+        c = torch.randint(0, 127, shape, generator=g, device=DEV, dtype=torch.uint8)
+        c = c | torch.randint(0, 2, shape, generator=g, device=DEV, dtype=torch.uint8) << 7
+        return c, torch.full((*shape[:-1], shape[-1] // 128), b, device=DEV, dtype=torch.uint8)
+
+    idx = routing(T, E, K, byte)
+    lay = gpu.ep_get_layout(idx, E)
+    rows = lay.max_recv_rows
+    x, w = fp8((rows, k), byte), fp8((E, n, k), 254 - byte)
+    out, ck = gpu.ep_expert_linear(x, w, lay, checkpoint=True)
+    for rs, _, _, y, _ in ref.linear(x, w, None, "none", None, False, ref.spans(lay, rows)):
+        e = next(e for e, a, b in ref.spans(lay, rows) if a == rs.start and b > a)
+        err = (k + 1) * ref.U * (ref.value(x)[rs].abs() @ ref.value(w)[e].T.abs())
+        ref.assert_near(out[rs], y, err, what="linear")
+        ref.assert_checkpoint(ck[0][rs], ck[1][rs], y, err)
+
+    dy = (torch.randn((rows, n), generator=g, device=DEV) * back).bfloat16()
+    dw, _ = gpu.ep_expert_wgrad(dy, x, lay)
+    for e, a, b in ref.spans(lay, rows):
+        yv, xv = dy[a:b].double(), ref.value(x)[a:b]
+        ref.assert_near(dw[e], yv.T @ xv, (b - a) * ref.U * (yv.abs().T @ xv.abs()), ref.U, "dw")
+
+    xt = (torch.randn((20, k), generator=g, device=DEV) * back * 2.0 ** -12).bfloat16()
+    w1, w2 = fp8((E, n, k), byte), fp8((E, k, n), 112)
+    few = gpu.ep_moe_decode(xt, idx[:20], None, w1, w2, "none")
+    want, err = (torch.zeros((20, k), dtype=torch.float64, device=DEV) for _ in "ab")
+    for e in range(E):
+        t, _ = (idx[:20] == e).nonzero(as_tuple=True)
+        v1, v2, xv = ref.value(w1)[e], ref.value(w2)[e], xt[t].double()
+        h = xv @ v1.T
+        dh = (k + 1) * ref.U * (xv.abs() @ v1.T.abs())
+        dh = dh + ref.BF16_HALF ** 2 * (h.abs() + dh)
+        y = h @ v2.T
+        want.index_add_(0, t, y)
+        err.index_add_(0, t, (dh + (n + 1) * ref.U * (h.abs() + dh)) @ v2.T.abs() + (K + 2) * ref.U * y.abs())
+    ref.assert_near(few, want, err, what="decode")
