@@ -19,6 +19,10 @@ library's gfx950 kernels.  The functions carry the C entry points' names:
   ep_expert_wgrad(dy, x, layout, ...)               -> (dw, db)
   ep_expert_activation_backward(dh, pre, layout, ...) -> (dpre, h, dweights)
   ep_moe_decode(x, topk_idx, topk_weights, w1, w2, ...) -> out
+  ep_cast_fp8_blocks(w, ...)                        -> ((codes, scales), transposed pair or None)
+  ep_block_linear(x, w, layout=None, ...)           -> out
+  ep_gated_ffn(x, w1, w2, ...)                      -> (out, z or None)
+  ep_gated_ffn_backward(dout, x, z, w1, w2, ...)    -> (dx, dw1, dw2)
 
 Semantics follow the DeepEP v2 test page ("DeepEP test target API
 reference", sec. 2.1 dispatch, 2.2 combine, 3.1-3.2 the V1 layout tensors and
@@ -43,6 +47,7 @@ __all__ = ["load_library", "Layout", "ep_get_layout", "ep_get_layout_noalloc", "
            "ep_dispatch_partitioned", "ep_combine_partitioned", "ep_combine_reduced",
            "ep_expert_linear",
            "ep_expert_wgrad", "ep_expert_activation_backward", "ep_moe_decode",
+           "ep_cast_fp8_blocks", "ep_block_linear", "ep_gated_ffn", "ep_gated_ffn_backward",
            "worst_case_recv_rows", "ep_probe_dispatch_stores", "EpError", "EP_DEV_BAD_EXPERT", "EP_DEV_CAPACITY",
            "EP_DEV_RECV_OVERFLOW"]
 
@@ -1051,3 +1056,198 @@ def ep_moe_decode(x: torch.Tensor, topk_idx: torch.Tensor, topk_weights: Optiona
             _ptr(w1_bias), _ptr(w2), _ptr(s2), _ptr(w2_bias), act, _ptr(b0), _ptr(b1), _ptr(ws),
             nbytes, _ptr(status), _ptr(out), _stream(dev))
     return out
+
+
+def _codes_and_scales(v, name):
+    """(e4m3 codes, fp32 scales) of 8-bit rows or weights; the scales' shape is
+    checked by the caller."""
+    if not isinstance(v, (tuple, list)) or len(v) != 2:
+        raise ValueError(f"{name} must be (fp8 codes, float32 scales)")
+    codes, scales = v
+    _need_cuda(codes, name)
+    _need_cuda(scales, f"{name} scales")
+    if not _is_fp8(codes):
+        raise ValueError(f"{name} must be (fp8 codes, float32 scales)")
+    if codes.shape[-1] % _FP8_ROW_GROUP:
+        raise ValueError(f"{name} needs a multiple of {_FP8_ROW_GROUP} channels")
+    if scales.dtype != torch.float32:
+        raise ValueError(f"{name}'s scales must be float32 (scale_fmt 'fp32' or 'pow2')")
+    return codes, scales
+
+
+def _scale_blocks(n: int) -> int:
+    return (n + _FP8_ROW_GROUP - 1) // _FP8_ROW_GROUP
+
+
+def ep_cast_fp8_blocks(w: torch.Tensor, transposed: bool = False,
+                       out: Optional[Sequence[torch.Tensor]] = None):
+    """Weights to e4m3 with one fp32 scale per 128 x 128 block, for
+    ep_block_linear: w bf16 [N, K] or [E, N, K] (N and K multiples of 8) to codes
+    of its shape and scales [(E,) ceil(N/128), ceil(K/128)] = max(amax, 1e-4) /
+    448.  With transposed=True also the same of the transposed matrices, codes
+    [(E,) K, N] and scales [(E,) ceil(K/128), ceil(N/128)], the weights of the
+    product's data gradient, from the same read.  `out` may name the buffers
+    (codes, scales, and with transposed=True the other two).  Returns ((codes,
+    scales), (codes_t, scales_t) or None)."""
+    lib = load_library()
+    _need_cuda(w, "w")
+    if w.dtype != torch.bfloat16:
+        raise ValueError("w must be bf16")
+    if w.dim() not in (2, 3):
+        raise ValueError("w must be [N, K] or [E, N, K]")
+    lead, (N, K) = tuple(w.shape[:-2]), w.shape[-2:]
+    dev = w.device
+    shapes = [(*lead, N, K), (*lead, _scale_blocks(N), _scale_blocks(K))]
+    if transposed:
+        shapes += [(*lead, K, N), (*lead, _scale_blocks(K), _scale_blocks(N))]
+    if out is None:
+        bufs = [torch.empty(s, dtype=torch.float32 if i & 1 else torch.float8_e4m3fn, device=dev)
+                for i, s in enumerate(shapes)]
+    else:
+        bufs = list(out)
+        if len(bufs) != len(shapes):
+            raise ValueError(f"out must be {len(shapes)} buffers")
+        for i, (t, s) in enumerate(zip(bufs, shapes)):
+            _check3(t, "scales" if i & 1 else "codes", _F32 if i & 1 else _F8, s)
+    codes_t, scales_t = bufs[2:] if transposed else (None, None)
+    _launch("ep_cast_fp8_blocks", dev, lib.ep_cast_fp8_blocks, bufs,
+            _ptr(w), lead[0] if lead else 1, N, K, _ptr(bufs[0]), _ptr(bufs[1]), _ptr(codes_t),
+            _ptr(scales_t), _stream(dev))
+    return (bufs[0], bufs[1]), ((codes_t, scales_t) if transposed else None)
+
+
+def ep_block_linear(x: Tuple[torch.Tensor, torch.Tensor], w: Tuple[torch.Tensor, torch.Tensor],
+                    layout: Optional[Layout] = None, bias: Optional[torch.Tensor] = None,
+                    activation: str = "none", residual: Optional[torch.Tensor] = None,
+                    out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The matrix product of 8-bit rows and weights with one fp32 scale for each
+    block of 128, with its epilogue: out[r] = act(w x[r] + bias) + residual[r].
+
+    x: (e4m3 codes [rows, K], float32 scales [rows, K/128]), as
+    ep_dispatch(recv_fp8=True) and ep_cast_fp8(x, 128) give them.  w: (e4m3 codes
+    [E, N, K], float32 scales [E, ceil(N/128), K/128]) of ep_cast_fp8_blocks.
+    With a layout, row r takes the weights of its expert, and rows that hold no
+    pair are left as they were; without one all rows take w [N, K], scales
+    [ceil(N/128), K/128] (a shared expert; bias [N]).  bias: bf16 [E, N].
+    activation: "none", "silu", "gelu" (tanh form), or "swiglu" / "geglu" on z =
+    [gate | up] (N a multiple of 64, else of 8).  residual: bf16 like out.
+    Returns out, bf16 [rows, N or N/2].
+
+    The data gradient is the same call: the gradient rows through ep_cast_fp8 and
+    the transposed pair of ep_cast_fp8_blocks."""
+    lib = load_library()
+    act, gated = _activation(activation)
+    x, x_scales = _codes_and_scales(x, "x")
+    w, w_scales = _codes_and_scales(w, "w")
+    lead = () if layout is None else (layout.num_experts,)
+    if x.dim() != 2 or w.dim() != 2 + len(lead):
+        raise ValueError("x must be [rows, K] and w [E, N, K], or [N, K] without a layout")
+    rows, K = x.shape
+    N = w.shape[-2]
+    _check3(w, "w", _F8, (*lead, N, K))
+    _check3(x_scales, "x scales", _F32, (rows, K // _FP8_ROW_GROUP))
+    _check3(w_scales, "w scales", _F32, (*lead, _scale_blocks(N), K // _FP8_ROW_GROUP))
+    M = N // 2 if gated else N
+    dev = x.device
+    if bias is not None:
+        _check3(bias, "bias", _BF16, (*lead, N))
+    if residual is not None:
+        _check(residual, "residual", _BF16, M, min_rows=rows)
+    if out is None:
+        out = torch.empty((rows, M), dtype=torch.bfloat16, device=dev)
+    _check(out, "out", _BF16, M, min_rows=rows)
+    params = None if layout is None else ctypes.byref(layout.params)
+    ptrs = None if layout is None else ctypes.byref(layout.ptrs())
+    _launch("ep_block_linear", dev, lib.ep_block_linear,
+            [x_scales, w, w_scales, bias, residual, out, None if layout is None else layout.status],
+            _ptr(x), _ptr(x_scales), _ptr(w), _ptr(w_scales), N, K, _ptr(bias), act,
+            _ptr(residual), params, ptrs, rows, _ptr(out), _stream(dev))
+    return out
+
+
+def _ffn_sizes(x: torch.Tensor, w1: torch.Tensor, w2: torch.Tensor, activation: str):
+    act, gated = _activation(activation)
+    if not gated:
+        raise ValueError('the block\'s activation must be "swiglu" or "geglu"')
+    _need_cuda(x, "x")
+    if x.dim() != 2 or w2.dim() != 2:
+        raise ValueError("x must be [T, H], w1 [2 I, H] and w2 [H, I]")
+    T, H = x.shape
+    inter = w2.shape[1]
+    _check(x, "x", _BF16, H)
+    _check3(w1, "w1", _BF16, (2 * inter, H))
+    _check3(w2, "w2", _BF16, (H, inter))
+    return act, T, H, inter
+
+
+def ep_gated_ffn(x: torch.Tensor, w1: torch.Tensor, w2: torch.Tensor, activation: str = "swiglu",
+                 residual: Optional[torch.Tensor] = None,
+                 save: Union[bool, torch.Tensor] = False, out: Optional[torch.Tensor] = None):
+    """The gated feed-forward block that every token passes (a shared expert):
+    z = x w1^T = [gate | up], out = (f(gate) * up) w2^T + residual.
+
+    x: bf16 [T, H].  w1: bf16 [2 I, H], gate rows first; w2: bf16 [H, I] (H and I
+    multiples of 8).  activation: "swiglu" or "geglu".  residual: bf16 [T, H] (the
+    stream, or ep_combine's output; it may be `out`).  save=True (or the buffer,
+    bf16 [T, 2 I]) also keeps z for ep_gated_ffn_backward.  Returns (out bf16
+    [T, H], z or None)."""
+    lib = load_library()
+    act, T, H, inter = _ffn_sizes(x, w1, w2, activation)
+    dev = x.device
+    z = save if isinstance(save, torch.Tensor) else None
+    if z is None and save:
+        z = torch.empty((T, 2 * inter), dtype=torch.bfloat16, device=dev)
+    if out is None:
+        out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+    _check(z, "z", _BF16, 2 * inter, rows=T)
+    _check(residual, "residual", _BF16, H, rows=T)
+    _check(out, "out", _BF16, H, rows=T)
+    nbytes = int(lib.ep_gated_ffn_workspace_bytes(T, inter, 0))
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    _launch("ep_gated_ffn", dev, lib.ep_gated_ffn, [w1, w2, residual, z, out],
+            _ptr(x), T, H, inter, _ptr(w1), _ptr(w2), act, _ptr(residual), _ptr(z), _ptr(ws),
+            nbytes, _ptr(out), _stream(dev))
+    return out, z
+
+
+def ep_gated_ffn_backward(dout: torch.Tensor, x: torch.Tensor, z: torch.Tensor, w1: torch.Tensor,
+                          w2: torch.Tensor, activation: str = "swiglu",
+                          dtype: torch.dtype = torch.float32,
+                          accumulate: Optional[Sequence[Optional[torch.Tensor]]] = None,
+                          out: Optional[Sequence[Optional[torch.Tensor]]] = None):
+    """The gradients of ep_gated_ffn: (dx bf16 [T, H], dw1 [2 I, H], dw2 [H, I]),
+    the weights' in `dtype` (float32 or bfloat16).
+
+    dout: bf16 [T, H], the gradient of out (and of its residual).  z: what the
+    forward pass kept.  accumulate=(dw1, dw2): gradients the new ones are added to;
+    `out` may name the result buffers (dx, dw1, dw2; None entries are allocated),
+    the same tensors included.  dz and h = f(gate) * up are rounded to bf16 on the
+    way, sums are fp32."""
+    lib = load_library()
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("dtype must be float32 or bfloat16")
+    act, T, H, inter = _ffn_sizes(x, w1, w2, activation)
+    _check(dout, "dout", _BF16, H, rows=T)
+    _check(z, "z", _BF16, 2 * inter, rows=T)
+    dev = x.device
+    dx, dw1, dw2 = (list(out) + [None] * 3)[:3] if out is not None else (None, None, None)
+    in1, in2 = (list(accumulate) + [None, None])[:2] if accumulate is not None else (None, None)
+    if dx is None:
+        dx = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+    if dw1 is None:
+        dw1 = torch.empty((2 * inter, H), dtype=dtype, device=dev)
+    if dw2 is None:
+        dw2 = torch.empty((H, inter), dtype=dtype, device=dev)
+    _check(dx, "dx", _BF16, H, rows=T)
+    for name, t, shape in (("dw1", dw1, (2 * inter, H)), ("accumulate dw1", in1, (2 * inter, H)),
+                           ("dw2", dw2, (H, inter)), ("accumulate dw2", in2, (H, inter))):
+        if t is not None:
+            _check3(t, name, (dtype,), shape)
+    nbytes = int(lib.ep_gated_ffn_workspace_bytes(T, inter, 1))
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    _launch("ep_gated_ffn_backward", dev, lib.ep_gated_ffn_backward,
+            [dout, z, w1, w2, in1, in2, dx, dw1, dw2],
+            _ptr(dout), _ptr(x), _ptr(z), T, H, inter, _ptr(w1), _ptr(w2), act, _ptr(in1),
+            _ptr(in2), _ptr(ws), nbytes, _ptr(dx), _ptr(dw1), _ptr(dw2),
+            1 if dtype == torch.bfloat16 else 0, _stream(dev))
+    return dx, dw1, dw2

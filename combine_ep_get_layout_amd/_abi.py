@@ -42,7 +42,9 @@ EXPORTS = ("ep_get_layout_workspace_bytes", "ep_worst_case_recv_rows", "ep_get_l
            "ep_combine_reduced", "ep_cast_fp8", "ep_logfmt_row_bytes", "ep_logfmt_encode",
            "ep_logfmt_decode", "ep_combine_logfmt", "ep_probe_dispatch_stores",
            "ep_expert_linear", "ep_expert_wgrad", "ep_expert_activation_backward",
-           "ep_moe_decode_workspace_bytes", "ep_moe_decode", "ep_status_string")
+           "ep_moe_decode_workspace_bytes", "ep_moe_decode", "ep_cast_fp8_blocks",
+           "ep_block_linear", "ep_gated_ffn_workspace_bytes", "ep_gated_ffn",
+           "ep_gated_ffn_backward", "ep_status_string")
 
 
 class LayoutParams(ctypes.Structure):
@@ -141,6 +143,18 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.ep_moe_decode.argtypes = [vp, vp, vp, i32, i32, i32, i32, i32, ctypes.c_int, vp, vp, vp, vp,
                                   vp, vp, ctypes.c_int, vp, vp, vp, sz, vp, vp, vp]
     lib.ep_moe_decode.restype = ctypes.c_int
+    lib.ep_cast_fp8_blocks.argtypes = [vp, i32, i32, i32, vp, vp, vp, vp, vp]
+    lib.ep_cast_fp8_blocks.restype = ctypes.c_int
+    lib.ep_block_linear.argtypes = [vp, vp, vp, vp, i32, i32, vp, ctypes.c_int, vp,
+                                    P(LayoutParams), P(LayoutPtrs), i64, vp, vp]
+    lib.ep_block_linear.restype = ctypes.c_int
+    lib.ep_gated_ffn_workspace_bytes.argtypes = [i64, i32, ctypes.c_int]
+    lib.ep_gated_ffn_workspace_bytes.restype = sz
+    lib.ep_gated_ffn.argtypes = [vp, i64, i32, i32, vp, vp, ctypes.c_int, vp, vp, vp, sz, vp, vp]
+    lib.ep_gated_ffn.restype = ctypes.c_int
+    lib.ep_gated_ffn_backward.argtypes = [vp, vp, vp, i64, i32, i32, vp, vp, ctypes.c_int, vp, vp,
+                                          vp, sz, vp, vp, vp, ctypes.c_int, vp]
+    lib.ep_gated_ffn_backward.restype = ctypes.c_int
     lib.ep_status_string.argtypes = [ctypes.c_int]
     lib.ep_status_string.restype = ctypes.c_char_p
     _lib = lib

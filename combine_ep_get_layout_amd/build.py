@@ -17,7 +17,8 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libep.so")
 SOURCES = ["ep_api.hip", "ep_layout.hip", "ep_dispatch.hip", "ep_combine.hip", "ep_logfmt.hip",
            "ep_expert_linear.hip", "ep_expert_wgrad.hip", "ep_expert_act.hip",
-           "ep_expert_decode.hip"]
+           "ep_expert_decode.hip", "ep_block_linear.hip", "ep_cast_blocks.hip", "ep_few_rows.hip",
+           "ep_ffn.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -725,6 +725,160 @@ int ep_moe_decode(const void *x, const int64_t *topk_idx, const float *topk_weig
     return to_status(ep::launch_moe_decode(a, (hipStream_t)stream));
 }
 
+int ep_cast_fp8_blocks(const void *w, int32_t num, int32_t n, int32_t k, uint8_t *codes,
+                       float *scales, uint8_t *codes_t, float *scales_t, void *stream) {
+    if (num < 0 || n < 8 || k < 8 || n % 8 != 0 || k % 8 != 0) return EP_ERR_INVALID_ARG;
+    if ((codes == nullptr) != (scales == nullptr) || (codes_t == nullptr) != (scales_t == nullptr))
+        return EP_ERR_INVALID_ARG;
+    if (n > EP_MAX_HIDDEN || k > EP_MAX_HIDDEN) return EP_ERR_UNSUPPORTED;
+    const int64_t blocks = (int64_t)((n + 127) / 128) * ((k + 127) / 128);
+    if (blocks * num > 0x7fffffff) return EP_ERR_UNSUPPORTED;
+    if (num == 0) return EP_OK;
+    if (!w || !aligned16(w) || (!codes && !codes_t) || !aligned8(codes) || !aligned8(codes_t) ||
+        !aligned4(scales) || !aligned4(scales_t))
+        return EP_ERR_INVALID_ARG;
+    ep::CastBlocksArgs a = {};
+    a.w = w;
+    a.codes = codes;
+    a.scales = scales;
+    a.codes_t = codes_t;
+    a.scales_t = scales_t;
+    a.num = num;
+    a.n = n;
+    a.k = k;
+    return to_status(ep::launch_cast_blocks(a, (hipStream_t)stream));
+}
+
+// The one segment of dense rows.
+static void dense_rows(int64_t num_rows, ep::SegmentRows *seg) {
+    *seg = {};
+    seg->E = 1;
+    seg->num_rows = seg->pairs = seg->each = num_rows;
+}
+
+int ep_block_linear(const void *x, const float *x_scales, const void *w, const float *w_scales,
+                    int32_t n, int32_t k, const void *bias, int act, const void *residual,
+                    const ep_layout_params *p, const ep_layout *layout, int64_t num_rows,
+                    void *out, void *stream) {
+    ep::BlockLinearArgs a = {};
+    if ((p == nullptr) != (layout == nullptr)) return EP_ERR_INVALID_ARG;
+    if (p) {
+        const int rc = segment_checks(p, layout, num_rows, &a.seg);
+        if (rc != EP_OK) return rc;
+    } else {
+        if (num_rows < 0 || num_rows >= ((int64_t)1 << 31)) return EP_ERR_INVALID_ARG;
+        dense_rows(num_rows, &a.seg);
+    }
+    if (!is_act(act) || n < 8 || n % (ep::act_gated(act) ? 64 : 8) != 0) return EP_ERR_INVALID_ARG;
+    if (k < ep::kFp8Group || k % ep::kFp8Group != 0) return EP_ERR_INVALID_ARG;
+    if (n > EP_MAX_HIDDEN || k > EP_MAX_HIDDEN || (int64_t)n * k >= kMaxBuffer)
+        return EP_ERR_UNSUPPORTED;
+    if (a.seg.pairs == 0 || num_rows == 0) return EP_OK;
+    if (!x || !aligned16(x) || !w || !aligned16(w) || !out || !aligned16(out))
+        return EP_ERR_INVALID_ARG;
+    if (!x_scales || !aligned4(x_scales) || !w_scales || !aligned4(w_scales))
+        return EP_ERR_INVALID_ARG;
+    if (!aligned16(bias) || !aligned16(residual)) return EP_ERR_INVALID_ARG;
+    a.x = x;
+    a.x_scales = x_scales;
+    a.w = w;
+    a.w_scales = w_scales;
+    a.bias = bias;
+    a.residual = residual;
+    a.out = out;
+    a.n = n;
+    a.k = k;
+    a.act = act;
+    return to_status(ep::launch_block_linear(a, (hipStream_t)stream));
+}
+
+// Bytes of h (backward: and dz), each begun on a line.
+static size_t ffn_part(int64_t num_tokens, int64_t columns) {
+    return ((size_t)num_tokens * columns * 2 + 255) / 256 * 256;
+}
+
+size_t ep_gated_ffn_workspace_bytes(int64_t num_tokens, int32_t inter, int backward) {
+    if (num_tokens < 0 || num_tokens >= ((int64_t)1 << 31) || inter < 1 ||
+        inter > EP_MAX_HIDDEN / 2 || (backward != 0 && backward != 1))
+        return 0;
+    return ffn_part(num_tokens, inter) + (backward ? ffn_part(num_tokens, 2 * (int64_t)inter) : 0) + 256;
+}
+
+static int ffn_checks(int64_t num_tokens, int32_t hidden, int32_t inter, int act) {
+    if (num_tokens < 0 || num_tokens >= ((int64_t)1 << 31)) return EP_ERR_INVALID_ARG;
+    if (hidden < 8 || hidden % 8 != 0 || inter < 8 || inter % 8 != 0) return EP_ERR_INVALID_ARG;
+    if (act != EP_ACT_SWIGLU && act != EP_ACT_GEGLU) return EP_ERR_INVALID_ARG;
+    if (hidden > EP_MAX_HIDDEN || inter > EP_MAX_HIDDEN / 2 || (int64_t)hidden * inter * 4 >= kMaxBuffer)
+        return EP_ERR_UNSUPPORTED;
+    return EP_OK;
+}
+
+int ep_gated_ffn(const void *x, int64_t num_tokens, int32_t hidden, int32_t inter, const void *w1,
+                 const void *w2, int act, const void *residual, void *z, void *workspace,
+                 size_t workspace_bytes, void *out, void *stream) {
+    const int rc = ffn_checks(num_tokens, hidden, inter, act);
+    if (rc != EP_OK) return rc;
+    if (num_tokens == 0) return EP_OK;
+    if (!x || !aligned16(x) || !w1 || !aligned16(w1) || !w2 || !aligned16(w2) || !out ||
+        !aligned16(out) || !aligned16(residual) || !aligned16(z))
+        return EP_ERR_INVALID_ARG;
+    if (!workspace || !aligned16(workspace) ||
+        workspace_bytes < ep_gated_ffn_workspace_bytes(num_tokens, inter, 0))
+        return EP_ERR_WORKSPACE;
+    ep::FfnArgs a = {};
+    a.x = x;
+    a.w1 = w1;
+    a.w2 = w2;
+    a.residual = residual;
+    a.z = z;
+    a.h = workspace;
+    a.out = out;
+    a.rows = num_tokens;
+    a.hidden = hidden;
+    a.inter = inter;
+    a.act = act;
+    return to_status(ep::launch_gated_ffn(a, (hipStream_t)stream));
+}
+
+int ep_gated_ffn_backward(const void *dout, const void *x, const void *z, int64_t num_tokens,
+                          int32_t hidden, int32_t inter, const void *w1, const void *w2, int act,
+                          const void *dw1_in, const void *dw2_in, void *workspace,
+                          size_t workspace_bytes, void *dx, void *dw1, void *dw2, int dw_bf16,
+                          void *stream) {
+    const int rc = ffn_checks(num_tokens, hidden, inter, act);
+    if (rc != EP_OK) return rc;
+    if (dw_bf16 != 0 && dw_bf16 != 1) return EP_ERR_INVALID_ARG;
+    if (!dw1 || !aligned16(dw1) || !dw2 || !aligned16(dw2) || !aligned16(dw1_in) || !aligned16(dw2_in))
+        return EP_ERR_INVALID_ARG;
+    if (num_tokens > 0) {
+        if (!dout || !aligned16(dout) || !x || !aligned16(x) || !z || !aligned16(z) || !w1 ||
+            !aligned16(w1) || !w2 || !aligned16(w2) || !aligned16(dx))
+            return EP_ERR_INVALID_ARG;
+        if (!workspace || !aligned16(workspace) ||
+            workspace_bytes < ep_gated_ffn_workspace_bytes(num_tokens, inter, 1))
+            return EP_ERR_WORKSPACE;
+    }
+    ep::FfnBackwardArgs a = {};
+    a.dout = dout;
+    a.x = x;
+    a.z = z;
+    a.w1 = w1;
+    a.w2 = w2;
+    a.dw1_in = dw1_in;
+    a.dw2_in = dw2_in;
+    a.h = workspace;
+    a.dz = (uint8_t *)workspace + ffn_part(num_tokens, inter);
+    a.dx = dx;
+    a.dw1 = dw1;
+    a.dw2 = dw2;
+    a.rows = num_tokens;
+    a.hidden = hidden;
+    a.inter = inter;
+    a.act = act;
+    a.bf16_out = dw_bf16 == 1;
+    return to_status(ep::launch_gated_ffn_backward(a, (hipStream_t)stream));
+}
+
 const char *ep_status_string(int code) {
     switch (code) {
         case EP_OK: return "ok";

@@ -1,0 +1,235 @@
+// Product of e4m3 rows, one fp32 scale per 128 channels, with e4m3 weights, one per
+// 128 x 128 block, and its epilogue:
+//   z[r, c] = sum_b sx[r, b] sw[c / 128, b] sum_(k in b) x[r, k] w[c, k]
+//   out[r] = act(z[r] + bias[e]) + residual[r]        (rows r of segment e, or dense)
+//
+// The fp8 matrix instruction takes powers of two as scales, these are any fp32
+// numbers.  One instruction of 16 x 16 x 128 sums one block of the contraction, so
+// its result, begun at zero, is multiplied by the two scales and added to the fp32
+// sums by ordinary instructions: four for the four values of a lane.  (Held in
+// units of the latest scales instead, the sums would take as many.)  They run
+// beside the matrix instructions of the other wave of the SIMD, and the sums have to
+// lie in ordinary registers, so eight waves of 64 columns x 128 rows share a tile of
+// 256 x 256, not four of 128 x 128.
+//
+// The weights are the instruction's first operand: a lane's values are consecutive
+// columns of one row, with one row scale, and a wave's 64 columns lie in one block
+// of the weights (gated: 32 gate and 32 up columns in one each).
+//
+// Scales of four steps are copied to LDS with the operands of the first of them, in
+// two buffers: ordinary loads would make the compiler wait for the copies in flight.
+#include "ep_linear_device.h"
+
+namespace ep {
+
+namespace {
+
+struct BlockK {
+    LinearK l;
+    const float *xs;       // [num_rows, k/128]
+    const float *ws;       // [E, ceil(n/128), k/128]
+};
+
+template <int BM, int WM, int WN, int NS, bool GATED>
+__global__ __launch_bounds__(64 * WN * WM, 2) void block_linear_kernel(BlockK p) {
+    constexpr int kWaves = WN * WM;
+    constexpr int BN = 64 * WN;
+    constexpr int MT = BM / WM / 16;                   // 16-row tiles of a wave
+    constexpr int kWStage = BN * 128, kXStage = BM * 128;
+    constexpr int kStage = kWStage + kXStage;
+    constexpr int WL = kWStage / 1024 / kWaves;        // copies of a wave per step
+    constexpr int XL = kXStage / 1024 / kWaves;
+    constexpr int SL = (BM / 16 + kWaves - 1) / kWaves;    // and of row scales, per four steps
+    constexpr int kXScales = SL * kWaves * 256, kScales = kXScales + kWaves * 256;
+    __shared__ __align__(1024) uint8_t lds[NS * kStage + 2 * kScales];
+    __shared__ int red[16];
+    const LinearK &a = p.l;
+    uint8_t *const slds = lds + NS * kStage;
+
+    TileAt at;
+    if (!find_tile<64 * kWaves>(a.seg, BM, a.col_tiles, blockIdx.x, red, &at)) return;
+
+    const int lane = threadIdx.x & 63, wave = wave_uniform(threadIdx.x >> 6);
+    const int l16 = lane & 15, q = lane >> 4;
+    const int wn = wave % WN, wm = wave / WN;
+    const int K = a.k, N = a.n;
+    const int half = N >> 1;
+    const int row0 = at.mt * BM;                       // in the segment
+    const int rows = min(BM, at.rows - row0);
+    const int groups = K / kFp8Group;
+
+    const ep_i32x4 xb = buffer_of(a.x + ((int64_t)at.row0 + row0) * K, (uint32_t)rows * K);
+    const uint32_t w_bytes = (uint32_t)N * K;
+    const ep_i32x4 wb = buffer_of(a.w + (int64_t)at.e * w_bytes, w_bytes);
+    const int wblocks = (N + kFp8Group - 1) / kFp8Group;
+    const ep_i32x4 xsb = buffer_of(p.xs + ((int64_t)at.row0 + row0) * groups, (uint32_t)(rows * groups) * 4);
+    const ep_i32x4 wsb = buffer_of(p.ws + (int64_t)at.e * wblocks * groups, (uint32_t)(wblocks * groups) * 4);
+    // column of z at place r of the tile: gated tiles hold, per wave, 32 gate
+    // columns and the 32 up columns that go with them
+    auto column = [&](int r) {
+        if (!GATED) return at.nt * BN + r;
+        const int c = at.nt * (BN / 2) + (r >> 6) * 32 + (r & 31);
+        return (r & 32) ? half + c : c;
+    };
+    const int chunk = (lane & 7) ^ ((wave * 4 + (lane >> 4)) & 7);
+    uint32_t xoff[XL], woff[WL];
+    for (int j = 0; j < XL; ++j) xoff[j] = (uint32_t)((j * kWaves + wave) * 8 + (lane >> 3)) * K + chunk * 16;
+    for (int j = 0; j < WL; ++j) {
+        const int c = column((j * kWaves + wave) * 8 + (lane >> 3));
+        woff[j] = c < N ? (uint32_t)c * K + chunk * 16 : kOutOfRange;
+    }
+    // scales: lane l copies step l % 4 of row l / 4 (of this wave's weight blocks,
+    // the gates' or only one and the ups')
+    const int sk = lane & 3;
+    uint32_t soff[SL], wsoff = kOutOfRange;
+    for (int j = 0; j < SL; ++j) soff[j] = (uint32_t)(((j * kWaves + wave) * 16 + (lane >> 2)) * groups + sk) * 4;
+    if (lane < 8) {
+        const int c = column(wn * 64 + (lane >> 2) * 32);
+        if (c < N) wsoff = (uint32_t)(c / kFp8Group * groups + sk) * 4;
+    }
+    const uint32_t lds0 = lds_offset(lds), slds0 = lds_offset(slds);
+    const int steps = groups;
+    auto copy = [&](int s, int stage) {
+        if ((s & 3) == 0) {
+            const uint32_t base = slds0 + (s >> 2 & 1) * kScales + wave * 256;
+            const uint32_t past = s + sk >= groups ? kOutOfRange : 0;
+            for (int j = 0; j < SL; ++j) dma4(xsb, base + j * kWaves * 256, soff[j] | past, s * 4);
+            dma4(wsb, base + kXScales, wsoff | past, s * 4);
+        }
+        const uint32_t base = lds0 + stage * kStage + wave * 1024;
+        for (int j = 0; j < WL; ++j) dma16(wb, base + j * kWaves * 1024, woff[j], s * 128);
+        for (int j = 0; j < XL; ++j) dma16(xb, base + kWStage + j * kWaves * 1024, xoff[j], s * 128);
+    };
+
+    ep_f32x4 acc[4][MT];
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int i = 0; i < MT; ++i) acc[t][i] = ep_f32x4{0, 0, 0, 0};
+
+    const int slot = l16 * 128 + (q ^ (l16 >> 1)) * 16;
+    auto compute = [&](int s, int stage) {
+        const uint8_t *wl = lds + stage * kStage;
+        const uint8_t *xl = wl + kWStage + wm * 2048;
+        const uint8_t *sl = slds + (s >> 2 & 1) * kScales + (s & 3) * 4;
+        ep_u32x4 wf[4][2], xf[2][2];
+        auto read_x = [&](int i) __attribute__((always_inline)) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                xf[i & 1][h] = *(const ep_u32x4 *)(xl + i * WM * 2048 + (slot ^ (h * 64)));
+        };
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                wf[t][h] = *(const ep_u32x4 *)(wl + (wn * 4 + t) * 2048 + (slot ^ (h * 64)));
+        read_x(0);
+        float sx[MT], sw[2];
+        sw[0] = *(const float *)(sl + kXScales + wave * 256);
+        sw[1] = GATED ? *(const float *)(sl + kXScales + wave * 256 + 16) : sw[0];
+#pragma unroll
+        for (int i = 0; i < MT; ++i) sx[i] = *(const float *)(sl + ((i * WM + wm) * 16 + l16) * 16);
+        __builtin_amdgcn_sched_barrier(0);
+        // the product of tile n is added to the sums two tiles later
+        ep_f32x4 part[3];
+        auto add = [&](auto nn) __attribute__((always_inline)) {
+            constexpr int n = decltype(nn)::value, i = n >> 2, t = n & 3;
+            const float f = sx[i] * sw[t >> 1];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[t][i][j] = __builtin_fmaf(part[n % 3][j], f, acc[t][i][j]);
+        };
+        each<4 * MT>([&](auto nn) __attribute__((always_inline)) {
+            constexpr int n = decltype(nn)::value, i = n >> 2, t = n & 3;
+            if constexpr (t == 0 && i + 1 < MT) read_x(i + 1);
+            part[n % 3] = mfma_fp8_plain(wf[t], xf[i & 1], ep_f32x4{0, 0, 0, 0});
+            if constexpr (n >= 2) add(std::integral_constant<int, n - 2>{});
+            __builtin_amdgcn_sched_barrier(0);
+        });
+        add(std::integral_constant<int, 4 * MT - 2>{});
+        add(std::integral_constant<int, 4 * MT - 1>{});
+    };
+
+    for (int s = 0; s < NS - 1; ++s)
+        if (s < steps) copy(s, s);
+    // stage s has landed once at most the copies of the steps after it are in
+    // flight, with the scales of those that begin a group of four; near the end
+    // there are none, and all are waited for
+    constexpr int kAhead = NS - 2;                     // whole steps that may be in flight
+    int stage = 0;
+    for (int s = 0; s < steps; ++s) {
+        if (kAhead == 0 || s + kAhead >= steps) {
+            dma_wait<0>();
+        } else {
+            bool first = false;
+            for (int j = 1; j <= kAhead; ++j) first |= (s + j & 3) == 0;
+            if (first) dma_wait<kAhead * (WL + XL) + SL + 1>();
+            else dma_wait<kAhead * (WL + XL)>();
+        }
+        barrier_only();
+        const int next = stage == 0 ? NS - 1 : stage - 1;
+        if (s + NS - 1 < steps) copy(s + NS - 1, next);
+        compute(s, stage);
+        stage = stage + 1 == NS ? 0 : stage + 1;
+    }
+    dma_wait<0>();
+    barrier_only();                                    // the stages are the epilogue's now
+    constexpr int BT = MT > 4 ? MT / 2 : MT;           // row tiles of an epilogue batch
+    static_assert(kWaves * BT * 4096 <= NS * kStage && MT % BT == 0, "a batch must fit the stages");
+    static_assert(NS - 1 <= 4, "a group's scales are read before the copies of the group after the next");
+    Output<4, BT, WM * 16, GATED> o;
+    o.load(a, at, row0 + wm * 16, rows - wm * 16, column(wn * 64), 0);
+    epilogue<4, MT, BT, WM * 16, GATED, kPlain>(a, at, lds + wave * BT * 4096, row0 + wm * 16,
+                                                rows - wm * 16, column(wn * 64), acc, o);
+}
+
+template <int BM, int WM, int WN, int NS>
+hipError_t launch_tiles(const BlockK &k, bool gated, hipStream_t stream) {
+    const int64_t grid = grid_of(k.l.seg, k.l.col_tiles, BM);
+    if (grid > 0x7fffffff) return hipErrorInvalidConfiguration;
+    const dim3 g((unsigned)grid), t(64 * WN * WM);
+    if (gated) block_linear_kernel<BM, WM, WN, NS, true><<<g, t, 0, stream>>>(k);
+    else block_linear_kernel<BM, WM, WN, NS, false><<<g, t, 0, stream>>>(k);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_block_linear(const BlockLinearArgs &a, hipStream_t stream) {
+    if (!a.seg.offsets && a.seg.num_rows <= kFewRows) {
+        FewRowsArgs f = {};
+        f.x = a.x;
+        f.x_scales = a.x_scales;
+        f.w = a.w;
+        f.w_scales = a.w_scales;
+        f.bias = a.bias;
+        f.residual = a.residual;
+        f.out = a.out;
+        f.rows = (int)a.seg.num_rows;
+        f.n = a.n;
+        f.k = a.k;
+        f.act = a.act;
+        return launch_few_rows(f, stream);
+    }
+    BlockK k = {};
+    k.l.seg = a.seg;
+    k.l.x = (const uint8_t *)a.x;
+    k.l.w = (const uint8_t *)a.w;
+    k.l.bias = (const uint16_t *)a.bias;
+    k.l.residual = (const uint16_t *)a.residual;
+    k.l.out = (uint16_t *)a.out;
+    k.l.n = a.n;
+    k.l.k = a.k;
+    k.xs = a.x_scales;
+    k.ws = a.w_scales;
+    const bool gated = act_gated(a.act);
+    k.l.m = gated ? a.n / 2 : a.n;
+    k.l.kind = act_kind(a.act);
+    const RowTile tile = row_tile(a.seg, k.l.m, gated, false);
+    k.l.col_tiles = (k.l.m + tile.cols - 1) / tile.cols;
+    if (tile.rows == 64) return launch_tiles<64, 4, 1, 4>(k, gated, stream);
+    if (tile.rows == 256) return launch_tiles<256, 2, 4, 2>(k, gated, stream);
+    if (tile.rows == 192) return launch_tiles<192, 2, 4, 2>(k, gated, stream);
+    return launch_tiles<128, 2, 4, 3>(k, gated, stream);
+}
+
+}  // namespace ep

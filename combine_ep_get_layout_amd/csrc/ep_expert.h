@@ -17,7 +17,8 @@ constexpr int kCheckpointGroup = 32;
 
 // Rows of a receive layout by segment: segment e holds rows
 // [offsets[e], offsets[e] + min(counts[e], offsets[e+1] - offsets[e])), of
-// which only those under num_rows exist.
+// which only those under num_rows exist.  Without a layout (offsets NULL) rows
+// [e * each, min((e + 1) * each, num_rows)).
 struct SegmentRows {
     const int32_t *counts;
     const int32_t *offsets;
@@ -25,6 +26,7 @@ struct SegmentRows {
     int E;
     int64_t num_rows;
     int64_t pairs;        // upper bound of the rows that hold a pair
+    int64_t each;         // rows of a segment without a layout
 };
 
 struct LinearArgs {
@@ -85,6 +87,78 @@ inline int act_kind(int act) {
            : act == EP_ACT_GELU || act == EP_ACT_GEGLU ? 2 : 0;
 }
 inline bool act_gated(int act) { return act == EP_ACT_SWIGLU || act == EP_ACT_GEGLU; }
+
+// Dense rows, at most kFewRows of them.
+constexpr int kFewRows = 64;
+struct FewRowsArgs {
+    const void *x;               // [rows, k]
+    const float *x_scales;       // e4m3: [rows, k/128], bf16: NULL
+    const void *w;               // [n, k]
+    const float *w_scales;       // e4m3: [ceil(n/128), k/128]
+    const void *bias;            // bf16 [n] or NULL
+    const void *residual;        // bf16 [rows, m] or NULL
+    void *out;                   // bf16 [rows, m]
+    int rows, n, k;
+    int act;                     // EP_ACT_*
+};
+
+hipError_t launch_few_rows(const FewRowsArgs &a, hipStream_t stream);
+
+// The product of e4m3 rows with fp32 scales per 128 channels and e4m3 weights
+// with fp32 scales per 128 x 128 block.
+struct BlockLinearArgs {
+    SegmentRows seg;
+    const void *x;               // [num_rows, k]
+    const float *x_scales;       // [num_rows, k/128]
+    const void *w;               // [E, n, k]
+    const float *w_scales;       // [E, ceil(n/128), k/128]
+    const void *bias;            // bf16 [E, n] or NULL
+    const void *residual;        // bf16 [num_rows, m] or NULL
+    void *out;                   // bf16 [num_rows, m]
+    int n, k;
+    int act;                     // EP_ACT_*
+};
+
+hipError_t launch_block_linear(const BlockLinearArgs &a, hipStream_t stream);
+
+struct CastBlocksArgs {
+    const void *w;               // bf16 [num, n, k]
+    uint8_t *codes;              // [num, n, k] or NULL
+    float *scales;               // [num, ceil(n/128), ceil(k/128)]
+    uint8_t *codes_t;            // [num, k, n] or NULL
+    float *scales_t;             // [num, ceil(k/128), ceil(n/128)]
+    int num, n, k;
+};
+
+hipError_t launch_cast_blocks(const CastBlocksArgs &a, hipStream_t stream);
+
+// The gated feed-forward block over dense rows.
+struct FfnArgs {
+    const void *x;               // bf16 [rows, hidden]
+    const void *w1, *w2;         // bf16 [2 inter, hidden], [hidden, inter]
+    const void *residual;        // bf16 [rows, hidden] or NULL
+    void *z;                     // bf16 [rows, 2 inter] or NULL
+    void *h;                     // workspace: bf16 [rows, inter]
+    void *out;                   // bf16 [rows, hidden]
+    int64_t rows;
+    int hidden, inter, act;
+};
+
+hipError_t launch_gated_ffn(const FfnArgs &a, hipStream_t stream);
+
+struct FfnBackwardArgs {
+    const void *dout, *x, *z;    // bf16 [rows, hidden], [rows, hidden], [rows, 2 inter]
+    const void *w1, *w2;
+    const void *dw1_in, *dw2_in; // dw's type, or NULL
+    void *dz, *h;                // workspace: bf16 [rows, 2 inter], [rows, inter]
+    void *dx;                    // bf16 [rows, hidden] or NULL
+    void *dw1, *dw2;             // fp32 or bf16
+    int64_t rows;
+    int hidden, inter, act;
+    bool bf16_out;
+};
+
+hipError_t launch_gated_ffn_backward(const FfnBackwardArgs &a, hipStream_t stream);
 
 struct MoeDecodeArgs {
     const void *x;               // bf16 [T, H]

@@ -27,6 +27,11 @@ struct TileAt {
 
 // Rows of segment e that hold a pair and exist.
 __device__ __forceinline__ int segment_rows(const SegmentRows &s, int e, int *row0) {
+    if (!s.offsets) {           // dense rows, `each` of them a segment
+        const int64_t from = (int64_t)e * s.each;
+        *row0 = (int)from;
+        return (int)max((int64_t)0, min(s.each, s.num_rows - from));
+    }
     const int o = s.offsets[e];
     const int have = s.offsets[e + 1] - o;
     const int c = min(s.counts[e], have);
@@ -183,6 +188,17 @@ __device__ __forceinline__ void dma16_of4(ep_i32x4 &rsrc, uint32_t lds, uint32_t
     }
 }
 
+// 64 lanes x 4 bytes, in lane order.
+__device__ __forceinline__ void dma4(const ep_i32x4 &rsrc, uint32_t lds, uint32_t voff, uint32_t soff) {
+    ep_i32x4 r;
+    for (int i = 0; i < 4; ++i) r[i] = wave_uniform(rsrc[i]);
+    asm volatile(
+        "s_nop 4\n\t"
+        "buffer_load_dword %0, %1, %2 offen lds"
+        :
+        : "v"(voff), "s"(r), "s"(wave_uniform((int)soff)), "{m0}"(wave_uniform((int)lds)));
+}
+
 // 64 lanes x 1 byte, one dword of LDS each (the byte, zero extended).
 __device__ __forceinline__ void dma1(const ep_i32x4 &rsrc, uint32_t lds, uint32_t voff, uint32_t soff) {
     ep_i32x4 r;
@@ -242,6 +258,17 @@ __device__ __forceinline__ ep_u32x4 transposed_operand(const uint8_t *tile, int 
 __device__ __forceinline__ ep_f32x4 mfma_bf16(ep_u32x4 a, ep_u32x4 b, ep_f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(ep_bf16x8, a),
                                                    __builtin_bit_cast(ep_bf16x8, b), c, 0, 0, 0);
+}
+
+// 128 channels of fp8 codes: a lane's 32 are pieces q and q + 4 of 16 of a row's
+// 128 bytes, alike in both operands.  (Without scale operands.)
+__device__ __forceinline__ ep_f32x4 mfma_fp8_plain(const ep_u32x4 *a, const ep_u32x4 *b, ep_f32x4 c) {
+    ep_i32x8 x, y;
+    x.lo = __builtin_bit_cast(ep_i32x4, a[0]);
+    x.hi = __builtin_bit_cast(ep_i32x4, a[1]);
+    y.lo = __builtin_bit_cast(ep_i32x4, b[0]);
+    y.hi = __builtin_bit_cast(ep_i32x4, b[1]);
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, c, 0, 0, 0, 0, 0, 0);
 }
 
 // fp32 pairs to packed bf16, nearest even (the hardware conversion).

@@ -573,6 +573,110 @@ int ep_moe_decode(const void *x, const int64_t *topk_idx, const float *topk_weig
                   int act, const void *res0, const void *res1, void *workspace,
                   size_t workspace_bytes, int32_t *status, void *out, void *stream);
 
+/* Products in e4m3 with one fp32 scale for each block of 128: rows with a scale
+ * per 128 channels, as ep_dispatch and ep_cast_fp8 write them
+ * (EP_DTYPE_FP8_E4M3, or _POW2, group 128), and weights with one per 128 x 128
+ * block. */
+
+/* ep_cast_fp8_blocks - weights to e4m3 with one scale per 128 x 128 block, and
+ * the transposed matrix with them (the operand of a product's data gradient).
+ *
+ *   w         device bf16 [num, n, k], 16-byte aligned; n and k multiples of 8.
+ *   codes     device uint8 [num, n, k], 8-byte aligned, and
+ *   scales    device float [num, ceil(n/128), ceil(k/128)]; both or neither.
+ *   codes_t   device uint8 [num, k, n], 8-byte aligned, and
+ *   scales_t  device float [num, ceil(k/128), ceil(n/128)]; both or neither.
+ * Per block (the last ones of a matrix may be partial) s = max(amax, 1e-4f) /
+ * 448, code = e4m3_rne(w / s), as ep_cast_fp8 forms them; NaN is left out of amax.
+ * codes_t holds the same codes and scales transposed.  EP_ERR_INVALID_ARG (num < 0,
+ * sizes, pointers; neither pair); EP_ERR_UNSUPPORTED (n or k above EP_MAX_HIDDEN,
+ * 2^31 blocks or more). */
+int ep_cast_fp8_blocks(const void *w, int32_t num, int32_t n, int32_t k, uint8_t *codes,
+                       float *scales, uint8_t *codes_t, float *scales_t, void *stream);
+
+/* ep_block_linear - the matrix product with these scales and its epilogue: with
+ * b = k/128 blocks,
+ *   z[r, c] = sum_b x_scales[r, b] w_scales[c/128, b] sum over the block's k of x[r, k] w[c, k]
+ *   out[r] = act(z[r] + bias) + residual[r], rounded once to bf16.
+ *
+ *   x          device e4m3 codes [num_rows, k], k % 128 == 0; 16-byte aligned.
+ *   x_scales   device float [num_rows, k/128].
+ *   w          device e4m3 codes [E, n, k], 16-byte aligned.
+ *   w_scales   device float [E, ceil(n/128), k/128].
+ *   n          columns of z: a multiple of 8 (of 64 for a gated activation).
+ *   bias       device bf16 [E, n] or NULL, 16-byte aligned.
+ *   act        EP_ACT_*.
+ *   residual   device bf16 [num_rows, m] or NULL, 16-byte aligned; m = n, or
+ *              n/2 for a gated activation.  It may be out.
+ *   params, layout  the receive layout of the rows (expert-major), as for
+ *              ep_expert_linear: of x, x_scales, residual and out only rows that hold
+ *              a pair are read or written; or both NULL: num_rows dense rows, E = 1.
+ *   out        device bf16 [num_rows, m], 16-byte aligned.
+ * A block's sum is the fp8 instruction's (fp32; it cuts products below 2^-13 of
+ * the largest of their 8 channels); the blocks are scaled and added in fp32.  The
+ * data gradient is the same call on gradient rows cast to 8 bits and the codes_t of
+ * the weights.  Two calls on the same inputs give the same bits; a row's result does
+ * not depend on the others' values, but with another number of rows its sums may be
+ * formed in another order.  Errors: EP_ERR_INVALID_ARG; EP_ERR_UNSUPPORTED (k or n
+ * above EP_MAX_HIDDEN, a matrix of 2^31 - 4096 bytes or more). */
+int ep_block_linear(const void *x, const float *x_scales, const void *w, const float *w_scales,
+                    int32_t n, int32_t k, const void *bias, int act, const void *residual,
+                    const ep_layout_params *params, const ep_layout *layout, int64_t num_rows,
+                    void *out, void *stream);
+
+/* The gated feed-forward block that every token passes (a shared expert; its
+ * output, or that of the routed experts, is the other's bias or residual):
+ *   z = x W1^T = [gate | up],  h = f(gate) * up,  out = h W2^T + residual. */
+
+/* Bytes of device workspace of the block's two calls (host call), or 0 for sizes
+ * they do not take. */
+size_t ep_gated_ffn_workspace_bytes(int64_t num_tokens, int32_t inter, int backward);
+
+/* ep_gated_ffn - the block's forward pass.
+ *
+ *   x          device bf16 [T, H], H % 8 == 0.
+ *   w1         device bf16 [2 I, H], gate rows first, I % 8 == 0.
+ *   w2         device bf16 [H, I].
+ *   act        EP_ACT_SWIGLU or EP_ACT_GEGLU.
+ *   residual   device bf16 [T, H] or NULL; it may be out.
+ *   z          device bf16 [T, 2 I] or NULL: z kept for ep_gated_ffn_backward.
+ *   workspace  device, >= ep_gated_ffn_workspace_bytes(T, I, 0); scratch of this
+ *              call (h).
+ *   out        device bf16 [T, H].
+ * All 16-byte aligned; outputs must not overlap inputs, except as named.  Sums are
+ * fp32; z, h and out are rounded to bf16 (h is formed from the sums, not from the
+ * rounded z).  Two calls on the same inputs give the same bits; with another number
+ * of rows, or with z, sums may be formed in another order.  Errors:
+ * EP_ERR_INVALID_ARG (T < 0 or 2^31 and more among them), EP_ERR_WORKSPACE,
+ * EP_ERR_UNSUPPORTED (H or 2 I above EP_MAX_HIDDEN, a matrix of 2^31 - 4096 bytes
+ * or more). */
+int ep_gated_ffn(const void *x, int64_t num_tokens, int32_t hidden, int32_t inter, const void *w1,
+                 const void *w2, int act, const void *residual, void *z, void *workspace,
+                 size_t workspace_bytes, void *out, void *stream);
+
+/* ep_gated_ffn_backward - the block's gradients.  With dh = dout W2:
+ *   dz = [dh * up * f'(gate) | dh * f(gate)],  dw2 = dout^T h (+ dw2_in),
+ *   dw1 = dz^T x (+ dw1_in),  dx = dz W1   (the residual's gradient is dout).
+ *
+ *   dout, x    device bf16 [T, H].
+ *   z          device bf16 [T, 2 I], as the forward pass kept it.
+ *   w1, w2, act  as in the forward pass.
+ *   dw1_in, dw2_in  gradients to add to, of dw's type, or NULL each; they may be
+ *              dw1 and dw2 themselves.
+ *   workspace  device, >= ep_gated_ffn_workspace_bytes(T, I, 1); scratch (dz, h).
+ *   dx         device bf16 [T, H] or NULL.
+ *   dw1, dw2   device [2 I, H], [H, I]: float (dw_bf16 = 0) or bf16 (1).  Without
+ *              tokens they are zeros (or dw1_in, dw2_in).
+ * dh stays in fp32; dz and h are rounded to bf16 (2^-8 of the value at most, the
+ * matrix instructions' type), everything is summed in fp32 and rounded once.  No
+ * atomics: two calls on the same inputs give the same bits.  All 16-byte aligned;
+ * outputs must not overlap inputs, except as named.  Errors as ep_gated_ffn. */
+int ep_gated_ffn_backward(const void *dout, const void *x, const void *z, int64_t num_tokens,
+                          int32_t hidden, int32_t inter, const void *w1, const void *w2, int act,
+                          const void *dw1_in, const void *dw2_in, void *workspace,
+                          size_t workspace_bytes, void *dx, void *dw1, void *dw2, int dw_bf16,
+                          void *stream);
+
 /* ep_probe_dispatch_stores - a measurement aid, not a step of the method:
  * the stores of ep_dispatch for bf16 rows (the same row kernel, grid and
  * store order) with each token's row replaced by a fixed pattern held in
