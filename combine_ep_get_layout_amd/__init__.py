@@ -1156,12 +1156,18 @@ def ep_block_linear(x: Tuple[torch.Tensor, torch.Tensor], w: Tuple[torch.Tensor,
     if out is None:
         out = torch.empty((rows, M), dtype=torch.bfloat16, device=dev)
     _check(out, "out", _BF16, M, min_rows=rows)
-    params = None if layout is None else ctypes.byref(layout.params)
-    ptrs = None if layout is None else ctypes.byref(layout.ptrs())
+    params = ptrs = ws = None
+    nbytes = 0
+    if layout is None:
+        nbytes = int(lib.ep_block_linear_workspace_bytes(rows, N, K))
+        if nbytes:
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    else:
+        params, ptrs = ctypes.byref(layout.params), ctypes.byref(layout.ptrs())
     _launch("ep_block_linear", dev, lib.ep_block_linear,
             [x_scales, w, w_scales, bias, residual, out, None if layout is None else layout.status],
             _ptr(x), _ptr(x_scales), _ptr(w), _ptr(w_scales), N, K, _ptr(bias), act,
-            _ptr(residual), params, ptrs, rows, _ptr(out), _stream(dev))
+            _ptr(residual), params, ptrs, rows, _ptr(ws), nbytes, _ptr(out), _stream(dev))
     return out
 
 
@@ -1202,7 +1208,7 @@ def ep_gated_ffn(x: torch.Tensor, w1: torch.Tensor, w2: torch.Tensor, activation
     _check(z, "z", _BF16, 2 * inter, rows=T)
     _check(residual, "residual", _BF16, H, rows=T)
     _check(out, "out", _BF16, H, rows=T)
-    nbytes = int(lib.ep_gated_ffn_workspace_bytes(T, inter, 0))
+    nbytes = int(lib.ep_gated_ffn_workspace_bytes(T, H, inter, 0))
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     _launch("ep_gated_ffn", dev, lib.ep_gated_ffn, [w1, w2, residual, z, out],
             _ptr(x), T, H, inter, _ptr(w1), _ptr(w2), act, _ptr(residual), _ptr(z), _ptr(ws),
@@ -1243,7 +1249,7 @@ def ep_gated_ffn_backward(dout: torch.Tensor, x: torch.Tensor, z: torch.Tensor, 
                            ("dw2", dw2, (H, inter)), ("accumulate dw2", in2, (H, inter))):
         if t is not None:
             _check3(t, name, (dtype,), shape)
-    nbytes = int(lib.ep_gated_ffn_workspace_bytes(T, inter, 1))
+    nbytes = int(lib.ep_gated_ffn_workspace_bytes(T, H, inter, 1))
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     _launch("ep_gated_ffn_backward", dev, lib.ep_gated_ffn_backward,
             [dout, z, w1, w2, in1, in2, dx, dw1, dw2],

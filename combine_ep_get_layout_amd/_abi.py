@@ -43,7 +43,7 @@ EXPORTS = ("ep_get_layout_workspace_bytes", "ep_worst_case_recv_rows", "ep_get_l
            "ep_logfmt_decode", "ep_combine_logfmt", "ep_probe_dispatch_stores",
            "ep_expert_linear", "ep_expert_wgrad", "ep_expert_activation_backward",
            "ep_moe_decode_workspace_bytes", "ep_moe_decode", "ep_cast_fp8_blocks",
-           "ep_block_linear", "ep_gated_ffn_workspace_bytes", "ep_gated_ffn",
+           "ep_block_linear_workspace_bytes", "ep_block_linear", "ep_gated_ffn_workspace_bytes", "ep_gated_ffn",
            "ep_gated_ffn_backward", "ep_status_string")
 
 
@@ -146,9 +146,11 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.ep_cast_fp8_blocks.argtypes = [vp, i32, i32, i32, vp, vp, vp, vp, vp]
     lib.ep_cast_fp8_blocks.restype = ctypes.c_int
     lib.ep_block_linear.argtypes = [vp, vp, vp, vp, i32, i32, vp, ctypes.c_int, vp,
-                                    P(LayoutParams), P(LayoutPtrs), i64, vp, vp]
+                                    P(LayoutParams), P(LayoutPtrs), i64, vp, sz, vp, vp]
     lib.ep_block_linear.restype = ctypes.c_int
-    lib.ep_gated_ffn_workspace_bytes.argtypes = [i64, i32, ctypes.c_int]
+    lib.ep_block_linear_workspace_bytes.argtypes = [i64, i32, i32]
+    lib.ep_block_linear_workspace_bytes.restype = sz
+    lib.ep_gated_ffn_workspace_bytes.argtypes = [i64, i32, i32, ctypes.c_int]
     lib.ep_gated_ffn_workspace_bytes.restype = sz
     lib.ep_gated_ffn.argtypes = [vp, i64, i32, i32, vp, vp, ctypes.c_int, vp, vp, vp, sz, vp, vp]
     lib.ep_gated_ffn.restype = ctypes.c_int

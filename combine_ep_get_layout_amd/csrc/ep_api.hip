@@ -756,10 +756,17 @@ static void dense_rows(int64_t num_rows, ep::SegmentRows *seg) {
     seg->num_rows = seg->pairs = seg->each = num_rows;
 }
 
+size_t ep_block_linear_workspace_bytes(int64_t num_rows, int32_t n, int32_t k) {
+    if (num_rows < 0 || num_rows >= ((int64_t)1 << 31) || n < 8 || n > EP_MAX_HIDDEN ||
+        k < ep::kFp8Group || k > EP_MAX_HIDDEN)
+        return 0;
+    return ep::block_linear_sums_bytes(num_rows, n, k);
+}
+
 int ep_block_linear(const void *x, const float *x_scales, const void *w, const float *w_scales,
                     int32_t n, int32_t k, const void *bias, int act, const void *residual,
                     const ep_layout_params *p, const ep_layout *layout, int64_t num_rows,
-                    void *out, void *stream) {
+                    void *workspace, size_t workspace_bytes, void *out, void *stream) {
     ep::BlockLinearArgs a = {};
     if ((p == nullptr) != (layout == nullptr)) return EP_ERR_INVALID_ARG;
     if (p) {
@@ -779,12 +786,16 @@ int ep_block_linear(const void *x, const float *x_scales, const void *w, const f
     if (!x_scales || !aligned4(x_scales) || !w_scales || !aligned4(w_scales))
         return EP_ERR_INVALID_ARG;
     if (!aligned16(bias) || !aligned16(residual)) return EP_ERR_INVALID_ARG;
+    const size_t sums = p ? 0 : ep::block_linear_sums_bytes(num_rows, n, k);
+    if (sums > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < sums))
+        return EP_ERR_WORKSPACE;
     a.x = x;
     a.x_scales = x_scales;
     a.w = w;
     a.w_scales = w_scales;
     a.bias = bias;
     a.residual = residual;
+    a.sums = (float *)workspace;
     a.out = out;
     a.n = n;
     a.k = k;
@@ -792,16 +803,19 @@ int ep_block_linear(const void *x, const float *x_scales, const void *w, const f
     return to_status(ep::launch_block_linear(a, (hipStream_t)stream));
 }
 
-// Bytes of h (backward: and dz), each begun on a line.
+// The parts of the block's workspace, each begun on a line: h, dz (backward), sums.
 static size_t ffn_part(int64_t num_tokens, int64_t columns) {
     return ((size_t)num_tokens * columns * 2 + 255) / 256 * 256;
 }
 
-size_t ep_gated_ffn_workspace_bytes(int64_t num_tokens, int32_t inter, int backward) {
-    if (num_tokens < 0 || num_tokens >= ((int64_t)1 << 31) || inter < 1 ||
-        inter > EP_MAX_HIDDEN / 2 || (backward != 0 && backward != 1))
+size_t ep_gated_ffn_workspace_bytes(int64_t num_tokens, int32_t hidden, int32_t inter,
+                                    int backward) {
+    if (num_tokens < 0 || num_tokens >= ((int64_t)1 << 31) || hidden < 8 ||
+        hidden > EP_MAX_HIDDEN || inter < 8 || inter > EP_MAX_HIDDEN / 2 ||
+        (backward != 0 && backward != 1))
         return 0;
-    return ffn_part(num_tokens, inter) + (backward ? ffn_part(num_tokens, 2 * (int64_t)inter) : 0) + 256;
+    return ffn_part(num_tokens, inter) + (backward ? ffn_part(num_tokens, 2 * (int64_t)inter) : 0) +
+           ep::gated_ffn_sums_bytes(num_tokens, hidden, inter, backward == 1) + 256;
 }
 
 static int ffn_checks(int64_t num_tokens, int32_t hidden, int32_t inter, int act) {
@@ -823,7 +837,7 @@ int ep_gated_ffn(const void *x, int64_t num_tokens, int32_t hidden, int32_t inte
         !aligned16(out) || !aligned16(residual) || !aligned16(z))
         return EP_ERR_INVALID_ARG;
     if (!workspace || !aligned16(workspace) ||
-        workspace_bytes < ep_gated_ffn_workspace_bytes(num_tokens, inter, 0))
+        workspace_bytes < ep_gated_ffn_workspace_bytes(num_tokens, hidden, inter, 0))
         return EP_ERR_WORKSPACE;
     ep::FfnArgs a = {};
     a.x = x;
@@ -832,6 +846,7 @@ int ep_gated_ffn(const void *x, int64_t num_tokens, int32_t hidden, int32_t inte
     a.residual = residual;
     a.z = z;
     a.h = workspace;
+    a.sums = (float *)((uint8_t *)workspace + ffn_part(num_tokens, inter));
     a.out = out;
     a.rows = num_tokens;
     a.hidden = hidden;
@@ -855,7 +870,7 @@ int ep_gated_ffn_backward(const void *dout, const void *x, const void *z, int64_
             !aligned16(w1) || !w2 || !aligned16(w2) || !aligned16(dx))
             return EP_ERR_INVALID_ARG;
         if (!workspace || !aligned16(workspace) ||
-            workspace_bytes < ep_gated_ffn_workspace_bytes(num_tokens, inter, 1))
+            workspace_bytes < ep_gated_ffn_workspace_bytes(num_tokens, hidden, inter, 1))
             return EP_ERR_WORKSPACE;
     }
     ep::FfnBackwardArgs a = {};
@@ -868,6 +883,7 @@ int ep_gated_ffn_backward(const void *dout, const void *x, const void *z, int64_
     a.dw2_in = dw2_in;
     a.h = workspace;
     a.dz = (uint8_t *)workspace + ffn_part(num_tokens, inter);
+    a.sums = (float *)((uint8_t *)a.dz + ffn_part(num_tokens, 2 * (int64_t)inter));
     a.dx = dx;
     a.dw1 = dw1;
     a.dw2 = dw2;

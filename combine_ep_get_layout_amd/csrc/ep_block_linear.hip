@@ -30,7 +30,7 @@ struct BlockK {
     const float *ws;       // [E, ceil(n/128), k/128]
 };
 
-template <int BM, int WM, int WN, int NS, bool GATED>
+template <int BM, int WM, int WN, int NS, bool GATED, int MODE = kPlain>
 __global__ __launch_bounds__(64 * WN * WM, 2) void block_linear_kernel(BlockK p) {
     constexpr int kWaves = WN * WM;
     constexpr int BN = 64 * WN;
@@ -88,13 +88,15 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void block_linear_kernel(BlockK p)
         if (c < N) wsoff = (uint32_t)(c / kFp8Group * groups + sk) * 4;
     }
     const uint32_t lds0 = lds_offset(lds), slds0 = lds_offset(slds);
-    const int steps = groups;
+    const int begin = MODE == kSums ? blockIdx.y * a.split : 0;
+    const int steps = MODE == kSums ? min(groups, begin + a.split) : groups;
     auto copy = [&](int s, int stage) {
-        if ((s & 3) == 0) {
+        if ((s & 3) == 0 || (MODE == kSums && s == begin)) {
             const uint32_t base = slds0 + (s >> 2 & 1) * kScales + wave * 256;
-            const uint32_t past = s + sk >= groups ? kOutOfRange : 0;
-            for (int j = 0; j < SL; ++j) dma4(xsb, base + j * kWaves * 256, soff[j] | past, s * 4);
-            dma4(wsb, base + kXScales, wsoff | past, s * 4);
+            const int s4 = s & ~3;
+            const uint32_t past = s4 + sk >= groups ? kOutOfRange : 0;
+            for (int j = 0; j < SL; ++j) dma4(xsb, base + j * kWaves * 256, soff[j] | past, s4 * 4);
+            dma4(wsb, base + kXScales, wsoff | past, s4 * 4);
         }
         const uint32_t base = lds0 + stage * kStage + wave * 1024;
         for (int j = 0; j < WL; ++j) dma16(wb, base + j * kWaves * 1024, woff[j], s * 128);
@@ -150,13 +152,13 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void block_linear_kernel(BlockK p)
     };
 
     for (int s = 0; s < NS - 1; ++s)
-        if (s < steps) copy(s, s);
+        if (begin + s < steps) copy(begin + s, s);
     // stage s has landed once at most the copies of the steps after it are in
     // flight, with the scales of those that begin a group of four; near the end
     // there are none, and all are waited for
     constexpr int kAhead = NS - 2;                     // whole steps that may be in flight
     int stage = 0;
-    for (int s = 0; s < steps; ++s) {
+    for (int s = begin; s < steps; ++s) {
         if (kAhead == 0 || s + kAhead >= steps) {
             dma_wait<0>();
         } else {
@@ -172,6 +174,11 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void block_linear_kernel(BlockK p)
         stage = stage + 1 == NS ? 0 : stage + 1;
     }
     dma_wait<0>();
+    if constexpr (MODE == kSums) {
+        store_sums<GATED, 4, MT>(a, row0 + wm * 16, WM * 16, rows - wm * 16, acc,
+                                 [&](int t) { return column(wn * 64 + t * 16); });
+        return;
+    }
     barrier_only();                                    // the stages are the epilogue's now
     constexpr int BT = MT > 4 ? MT / 2 : MT;           // row tiles of an epilogue batch
     static_assert(kWaves * BT * 4096 <= NS * kStage && MT % BT == 0, "a batch must fit the stages");
@@ -182,17 +189,40 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void block_linear_kernel(BlockK p)
                                                 rows - wm * 16, column(wn * 64), acc, o);
 }
 
-template <int BM, int WM, int WN, int NS>
-hipError_t launch_tiles(const BlockK &k, bool gated, hipStream_t stream) {
+template <int BM, int WM, int WN, int NS, int MODE = kPlain>
+hipError_t launch_tiles(BlockK &k, bool gated, int parts, hipStream_t stream) {
+    const int per = gated ? WN * 32 : WN * 64;
+    k.l.col_tiles = (k.l.m + per - 1) / per;
     const int64_t grid = grid_of(k.l.seg, k.l.col_tiles, BM);
     if (grid > 0x7fffffff) return hipErrorInvalidConfiguration;
-    const dim3 g((unsigned)grid), t(64 * WN * WM);
-    if (gated) block_linear_kernel<BM, WM, WN, NS, true><<<g, t, 0, stream>>>(k);
-    else block_linear_kernel<BM, WM, WN, NS, false><<<g, t, 0, stream>>>(k);
+    const dim3 g((unsigned)grid, parts), t(64 * WN * WM);
+    if (gated) block_linear_kernel<BM, WM, WN, NS, true, MODE><<<g, t, 0, stream>>>(k);
+    else block_linear_kernel<BM, WM, WN, NS, false, MODE><<<g, t, 0, stream>>>(k);
     return hipGetLastError();
 }
 
+DensePlan plan_of(int64_t rows, int n, int k) { return dense_plan(rows, n, k / kFp8Group, false); }
+
+hipError_t launch_dense(BlockK &k, bool gated, hipStream_t stream) {
+    const DensePlan p = plan_of(k.l.seg.num_rows, k.l.n, k.l.k);
+    if (p.rows == 256) return launch_tiles<256, 2, 4, 2>(k, gated, 1, stream);
+    if (p.cols == 64) return launch_tiles<64, 4, 1, 4>(k, gated, 1, stream);
+    if (p.parts == 1)
+        return p.rows == 128 ? launch_tiles<128, 2, 2, 2>(k, gated, 1, stream)
+                             : launch_tiles<64, 2, 2, 3>(k, gated, 1, stream);
+    k.l.split = p.split;
+    const hipError_t rc = p.rows == 128 ? launch_tiles<128, 2, 2, 2, kSums>(k, gated, p.parts, stream)
+                                        : launch_tiles<64, 2, 2, 3, kSums>(k, gated, p.parts, stream);
+    if (rc != hipSuccess) return rc;
+    return gated ? launch_finish<kPlain, true>(k.l, p.parts, stream)
+                 : launch_finish<kPlain, false>(k.l, p.parts, stream);
+}
+
 }  // namespace
+
+size_t block_linear_sums_bytes(int64_t rows, int n, int k) {
+    return rows <= kFewRows ? 0 : sums_bytes(plan_of(rows, n, k), rows, n);
+}
 
 hipError_t launch_block_linear(const BlockLinearArgs &a, hipStream_t stream) {
     if (!a.seg.offsets && a.seg.num_rows <= kFewRows) {
@@ -224,12 +254,13 @@ hipError_t launch_block_linear(const BlockLinearArgs &a, hipStream_t stream) {
     const bool gated = act_gated(a.act);
     k.l.m = gated ? a.n / 2 : a.n;
     k.l.kind = act_kind(a.act);
+    k.l.sums = a.sums;
+    if (!a.seg.offsets) return launch_dense(k, gated, stream);
     const RowTile tile = row_tile(a.seg, k.l.m, gated, false);
-    k.l.col_tiles = (k.l.m + tile.cols - 1) / tile.cols;
-    if (tile.rows == 64) return launch_tiles<64, 4, 1, 4>(k, gated, stream);
-    if (tile.rows == 256) return launch_tiles<256, 2, 4, 2>(k, gated, stream);
-    if (tile.rows == 192) return launch_tiles<192, 2, 4, 2>(k, gated, stream);
-    return launch_tiles<128, 2, 4, 3>(k, gated, stream);
+    if (tile.rows == 64) return launch_tiles<64, 4, 1, 4>(k, gated, 1, stream);
+    if (tile.rows == 256) return launch_tiles<256, 2, 4, 2>(k, gated, 1, stream);
+    if (tile.rows == 192) return launch_tiles<192, 2, 4, 2>(k, gated, 1, stream);
+    return launch_tiles<128, 2, 4, 3>(k, gated, 1, stream);
 }
 
 }  // namespace ep

@@ -114,10 +114,14 @@ struct BlockLinearArgs {
     const float *w_scales;       // [E, ceil(n/128), k/128]
     const void *bias;            // bf16 [E, n] or NULL
     const void *residual;        // bf16 [num_rows, m] or NULL
+    float *sums;                 // workspace: block_linear_sums_bytes
     void *out;                   // bf16 [num_rows, m]
     int n, k;
     int act;                     // EP_ACT_*
 };
+
+// Bytes that a product of dense rows needs for the sums of its parts.
+size_t block_linear_sums_bytes(int64_t rows, int n, int k);
 
 hipError_t launch_block_linear(const BlockLinearArgs &a, hipStream_t stream);
 
@@ -139,10 +143,14 @@ struct FfnArgs {
     const void *residual;        // bf16 [rows, hidden] or NULL
     void *z;                     // bf16 [rows, 2 inter] or NULL
     void *h;                     // workspace: bf16 [rows, inter]
+    float *sums;                 // workspace: gated_ffn_sums_bytes
     void *out;                   // bf16 [rows, hidden]
     int64_t rows;
     int hidden, inter, act;
 };
+
+// Bytes that the products of a pass need for the sums of their parts.
+size_t gated_ffn_sums_bytes(int64_t rows, int hidden, int inter, bool backward);
 
 hipError_t launch_gated_ffn(const FfnArgs &a, hipStream_t stream);
 
@@ -151,6 +159,7 @@ struct FfnBackwardArgs {
     const void *w1, *w2;
     const void *dw1_in, *dw2_in; // dw's type, or NULL
     void *dz, *h;                // workspace: bf16 [rows, 2 inter], [rows, inter]
+    float *sums;                 // workspace: gated_ffn_sums_bytes
     void *dx;                    // bf16 [rows, hidden] or NULL
     void *dw1, *dw2;             // fp32 or bf16
     int64_t rows;

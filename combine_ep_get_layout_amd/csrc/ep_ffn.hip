@@ -14,83 +14,105 @@ namespace ep {
 
 namespace {
 
-SegmentRows dense(int64_t rows) {
-    SegmentRows s = {};
-    s.E = 1;
-    s.num_rows = s.pairs = s.each = rows;
-    return s;
+constexpr int kStep = 64;        // channels of a step of the matrix kernels
+
+DensePlan plan_of(int64_t rows, int n, int k, bool transposed) {
+    return dense_plan(rows, n, (k + kStep - 1) / kStep, transposed);
 }
 
-// A product with an epilogue of its own: z kept (gated columns), or dz and h
-// from transposed weights.
-template <bool WT, bool GATED, int MODE>
-hipError_t launch_mode(LinearK &k, hipStream_t stream) {
-    const RowTile tile = row_tile(k.seg, k.m, GATED, WT);
-    k.col_tiles = (k.m + tile.cols - 1) / tile.cols;
-    const int64_t grid = grid_of(k.seg, k.col_tiles, tile.rows);
+template <int BM, int WM, int WN, int NS, bool WT, bool GATED, int MODE>
+hipError_t launch_tiles(LinearK &k, int parts, hipStream_t stream) {
+    const int per = GATED ? WN * 32 : WN * 64;
+    k.col_tiles = (k.m + per - 1) / per;
+    const int64_t grid = grid_of(k.seg, k.col_tiles, BM);
     if (grid > 0x7fffffff) return hipErrorInvalidConfiguration;
-    const dim3 g((unsigned)grid);
-    if (tile.rows == 256) expert_linear_wide_kernel<kBf16, WT, GATED, MODE><<<g, 256, 0, stream>>>(k);
-    else if (tile.rows == 192) expert_linear_kernel<192, 2, 4, 2, kBf16, WT, GATED, MODE><<<g, 512, 0, stream>>>(k);
-    else if (tile.rows == 128) expert_linear_kernel<128, 2, 4, 3, kBf16, WT, GATED, MODE><<<g, 512, 0, stream>>>(k);
-    else if constexpr (!WT) expert_linear_kernel<64, 4, 1, 4, kBf16, WT, GATED, MODE><<<g, 256, 0, stream>>>(k);
+    expert_linear_kernel<BM, WM, WN, NS, kBf16, WT, GATED, MODE>
+        <<<dim3((unsigned)grid, parts), 64 * WM * WN, 0, stream>>>(k);
     return hipGetLastError();
 }
 
-hipError_t product(const void *x, const void *w, int n, int k, int act, const void *residual,
-                   bool transposed, int64_t rows, void *out, hipStream_t stream) {
-    if (!transposed && rows <= kFewRows) {
-        FewRowsArgs f = {};
-        f.x = x;
-        f.w = w;
-        f.residual = residual;
-        f.out = out;
-        f.rows = (int)rows;
-        f.n = n;
-        f.k = k;
-        f.act = act;
-        return launch_few_rows(f, stream);
+// A product of dense rows with the epilogue MODE; `sums` holds what its plan asks for.
+template <bool WT, bool GATED, int MODE>
+hipError_t product(LinearK k, int64_t rows, float *sums, hipStream_t stream) {
+    k.seg = {};
+    k.seg.E = 1;
+    k.seg.num_rows = k.seg.pairs = k.seg.each = rows;
+    const DensePlan p = plan_of(rows, k.n, k.k, WT);
+    if (p.rows == 256) {
+        const int per = GATED ? kBN / 2 : kBN;
+        k.col_tiles = (k.m + per - 1) / per;
+        const int64_t grid = grid_of(k.seg, k.col_tiles, 256);
+        if (grid > 0x7fffffff) return hipErrorInvalidConfiguration;
+        expert_linear_wide_kernel<kBf16, WT, GATED, MODE><<<dim3((unsigned)grid), 256, 0, stream>>>(k);
+        return hipGetLastError();
     }
-    LinearArgs a = {};
-    a.seg = dense(rows);
-    a.x = x;
-    a.w = w;
-    a.residual = residual;
-    a.out = out;
-    a.n = n;
-    a.k = k;
-    a.act = act;
-    a.transposed = transposed;
-    return launch_expert_linear(a, stream);
+    if constexpr (!WT) {
+        if (p.cols == 64) return launch_tiles<64, 4, 1, 4, WT, GATED, MODE>(k, 1, stream);
+    }
+    if (p.parts == 1)
+        return p.rows == 128 ? launch_tiles<128, 2, 2, 2, WT, GATED, MODE>(k, 1, stream)
+                             : launch_tiles<64, 2, 2, 3, WT, GATED, MODE>(k, 1, stream);
+    k.sums = sums;
+    k.split = p.split;
+    const hipError_t rc = p.rows == 128 ? launch_tiles<128, 2, 2, 2, WT, GATED, kSums>(k, p.parts, stream)
+                                        : launch_tiles<64, 2, 2, 3, WT, GATED, kSums>(k, p.parts, stream);
+    if (rc != hipSuccess) return rc;
+    return launch_finish<MODE, GATED>(k, p.parts, stream);
+}
+
+hipError_t few_rows(const void *x, const void *w, int n, int k, int act, const void *residual,
+                    int64_t rows, void *out, hipStream_t stream) {
+    FewRowsArgs f = {};
+    f.x = x;
+    f.w = w;
+    f.residual = residual;
+    f.out = out;
+    f.rows = (int)rows;
+    f.n = n;
+    f.k = k;
+    f.act = act;
+    return launch_few_rows(f, stream);
 }
 
 }  // namespace
 
+size_t gated_ffn_sums_bytes(int64_t rows, int hidden, int inter, bool backward) {
+    const auto of = [&](int n, int k) { return sums_bytes(plan_of(rows, n, k, backward), rows, n); };
+    return backward ? std::max(of(inter, hidden), of(hidden, 2 * inter))
+                    : std::max(of(2 * inter, hidden), of(hidden, inter));
+}
+
 hipError_t launch_gated_ffn(const FfnArgs &a, hipStream_t stream) {
-    hipError_t rc;
-    if (a.z) {
-        LinearK k = {};
-        k.seg = dense(a.rows);
-        k.x = (const uint8_t *)a.x;
-        k.w = (const uint8_t *)a.w1;
-        k.out = (uint16_t *)a.h;
-        k.kept = (uint16_t *)a.z;
-        k.n = 2 * a.inter;
-        k.k = a.hidden;
-        k.m = a.inter;
-        k.kind = act_kind(a.act);
-        rc = launch_mode<false, true, kKeep>(k, stream);
-    } else {
-        rc = product(a.x, a.w1, 2 * a.inter, a.hidden, a.act, nullptr, false, a.rows, a.h, stream);
+    if (!a.z && a.rows <= kFewRows) {
+        const hipError_t rc = few_rows(a.x, a.w1, 2 * a.inter, a.hidden, a.act, nullptr, a.rows, a.h, stream);
+        if (rc != hipSuccess) return rc;
+        return few_rows(a.h, a.w2, a.hidden, a.inter, EP_ACT_NONE, a.residual, a.rows, a.out, stream);
     }
+    LinearK k = {};
+    k.x = (const uint8_t *)a.x;
+    k.w = (const uint8_t *)a.w1;
+    k.out = (uint16_t *)a.h;
+    k.kept = (uint16_t *)a.z;
+    k.n = 2 * a.inter;
+    k.k = a.hidden;
+    k.m = a.inter;
+    k.kind = act_kind(a.act);
+    const hipError_t rc = a.z ? product<false, true, kKeep>(k, a.rows, a.sums, stream)
+                              : product<false, true, kPlain>(k, a.rows, a.sums, stream);
     if (rc != hipSuccess) return rc;
-    return product(a.h, a.w2, a.hidden, a.inter, EP_ACT_NONE, a.residual, false, a.rows, a.out, stream);
+    LinearK d = {};
+    d.x = (const uint8_t *)a.h;
+    d.w = (const uint8_t *)a.w2;
+    d.residual = (const uint16_t *)a.residual;
+    d.out = (uint16_t *)a.out;
+    d.n = d.m = a.hidden;
+    d.k = a.inter;
+    return product<false, false, kPlain>(d, a.rows, a.sums, stream);
 }
 
 hipError_t launch_gated_ffn_backward(const FfnBackwardArgs &a, hipStream_t stream) {
     if (a.rows > 0) {
         LinearK k = {};
-        k.seg = dense(a.rows);
         k.x = (const uint8_t *)a.dout;
         k.w = (const uint8_t *)a.w2;
         k.out = (uint16_t *)a.dz;
@@ -99,12 +121,13 @@ hipError_t launch_gated_ffn_backward(const FfnBackwardArgs &a, hipStream_t strea
         k.n = k.m = a.inter;
         k.k = a.hidden;
         k.kind = act_kind(a.act);
-        const hipError_t rc = launch_mode<true, false, kBackward>(k, stream);
+        const hipError_t rc = product<true, false, kBackward>(k, a.rows, a.sums, stream);
         if (rc != hipSuccess) return rc;
     }
     auto wgrad = [&](const void *dy, int n, const void *x, int k, const void *dw_in, void *dw) {
         WgradArgs g = {};
-        g.seg = dense(a.rows);
+        g.seg.E = 1;
+        g.seg.num_rows = g.seg.pairs = g.seg.each = a.rows;
         g.dy = dy;
         g.x = x;
         g.dw_in = dw_in;
@@ -118,7 +141,13 @@ hipError_t launch_gated_ffn_backward(const FfnBackwardArgs &a, hipStream_t strea
     if (rc != hipSuccess) return rc;
     rc = wgrad(a.dz, 2 * a.inter, a.x, a.hidden, a.dw1_in, a.dw1);
     if (rc != hipSuccess || !a.dx || a.rows == 0) return rc;
-    return product(a.dz, a.w1, a.hidden, 2 * a.inter, EP_ACT_NONE, nullptr, true, a.rows, a.dx, stream);
+    LinearK d = {};
+    d.x = (const uint8_t *)a.dz;
+    d.w = (const uint8_t *)a.w1;
+    d.out = (uint16_t *)a.dx;
+    d.n = d.m = a.hidden;
+    d.k = 2 * a.inter;
+    return product<true, false, kPlain>(d, a.rows, a.sums, stream);
 }
 
 }  // namespace ep

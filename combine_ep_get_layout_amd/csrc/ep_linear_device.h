@@ -45,11 +45,35 @@ struct LinearK {
     uint16_t *kept;       // kKeep: z [num_rows, n]
     const uint16_t *pre;  // kBackward: z = [gate | up] [num_rows, 2 m]
     uint16_t *h;          // kBackward: act(gate) * up [num_rows, m]
+    float *sums;          // kSums: [parts, num_rows, n] of dense rows
+    int split;            // kSums: steps of a part of the contraction
 };
 
 // What the epilogue writes: act(z) + residual; z in bf16 with it; or, z being the
-// gradient dh of h = f(gate) * up, d[gate | up] (out, 2 m wide) and h itself.
-enum { kPlain, kKeep, kBackward };
+// gradient dh of h = f(gate) * up, d[gate | up] (out, 2 m wide) and h itself.  kSums:
+// the fp32 sums of part blockIdx.y of the contraction, for finish_kernel.
+enum { kPlain, kKeep, kBackward, kSums };
+
+// A wave's sums, tile (t, i) at columns column(t) + 4 q and row first + i * stride
+// + lane % 16 of dense rows.  (A gated tile's gate columns behind the half are up
+// columns, which another tile stores.)
+template <bool GATED, int NT, int MT, typename F>
+__device__ __forceinline__ void store_sums(const LinearK &a, int first, int stride, int live_rows,
+                                           ep_f32x4 (*acc)[MT], F column) {
+    const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
+    float *const out = a.sums + (int64_t)blockIdx.y * a.seg.num_rows * a.n;
+    each<MT>([&](auto ii) __attribute__((always_inline)) {
+        constexpr int i = decltype(ii)::value;
+        const int r = i * stride + l16;
+        each<NT>([&](auto tt) __attribute__((always_inline)) {
+            constexpr int t = decltype(tt)::value;
+            ep_f32x4 v = acc[t][i];
+            pin(v);
+            const int c = column(t) + 4 * q;
+            if (r < live_rows && c < (GATED && t < NT / 2 ? a.m : a.n)) *(ep_f32x4 *)(out + (int64_t)(first + r) * a.n + c) = v;
+        });
+    });
+}
 
 // Four consecutive scale bytes of a row from step s on, as far as the row has them.
 __device__ __forceinline__ int scales4(const uint8_t *row, int s, int groups) {
@@ -149,6 +173,27 @@ struct Output {
     }
 };
 
+// kBackward of 8 columns of a row: dgate = dh up f'(gate), dup = dh f(gate), h.
+__device__ __forceinline__ void write_backward(const LinearK &a, int64_t row, int col, const float *dh,
+                                               ep_u32x4 gate, ep_u32x4 up, int kind) {
+    ep_u32x4 dg, du, hv;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        float f[2], df[2];
+        act_both(bf16_lo(gate[j]), kind, &f[0], &df[0]);
+        act_both(bf16_hi(gate[j]), kind, &f[1], &df[1]);
+        const float u0 = bf16_lo(up[j]), u1 = bf16_hi(up[j]);
+        const float d0 = dh[2 * j], d1 = dh[2 * j + 1];
+        dg[j] = pack_bf16(d0 * u0 * df[0], d1 * u1 * df[1]);
+        du[j] = pack_bf16(d0 * f[0], d1 * f[1]);
+        hv[j] = pack_bf16(f[0] * u0, f[1] * u1);
+    }
+    uint16_t *p = a.out + row * 2 * a.m + col;
+    *(ep_u32x4 *)p = dg;
+    *(ep_u32x4 *)(p + a.m) = du;
+    *(ep_u32x4 *)(a.h + row * a.m + col) = hv;
+}
+
 template <int KIND, int NT, int MT, int BT, int STRIDE, bool GATED, int MODE>
 __device__ __forceinline__ void epilogue_of(const LinearK &a, const TileAt &at, uint8_t *lds,
                                             int first, int live_rows, int c0,
@@ -245,26 +290,7 @@ __device__ __forceinline__ void epilogue_of(const LinearK &a, const TileAt &at, 
                 }
             }
             if constexpr (MODE == kBackward) {
-                // z[0] is dh, in fp32: dgate = dh up f'(gate), dup = dh f(gate)
-                ep_u32x4 dg, du, hv;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    float f[2], df[2], u[2];
-                    act_both(bf16_lo(gate[i & 1][j]), KIND, &f[0], &df[0]);
-                    act_both(bf16_hi(gate[i & 1][j]), KIND, &f[1], &df[1]);
-                    u[0] = bf16_lo(up[i & 1][j]);
-                    u[1] = bf16_hi(up[i & 1][j]);
-                    const float d0 = z[0][2 * j], d1 = z[0][2 * j + 1];
-                    dg[j] = pack_bf16(d0 * u[0] * df[0], d1 * u[1] * df[1]);
-                    du[j] = pack_bf16(d0 * f[0], d1 * f[1]);
-                    hv[j] = pack_bf16(f[0] * u[0], f[1] * u[1]);
-                }
-                if (live) {
-                    uint16_t *p = a.out + row * 2 * m + col;
-                    *(ep_u32x4 *)p = dg;
-                    *(ep_u32x4 *)(p + m) = du;
-                    *(ep_u32x4 *)(a.h + row * m + col) = hv;
-                }
+                if (live) write_backward(a, row, col, z[0], gate[i & 1], up[i & 1], KIND);
                 continue;
             }
             float y[8];
@@ -309,7 +335,7 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void expert_linear_kernel(LinearK 
     constexpr bool FP8 = IN != kBf16, EXACT = IN == kFp8Exact;
     constexpr int kWaves = WN * WM;
     constexpr int BN = 64 * WN;
-    static_assert(!WT || BN == 256, "transposed weights lie in rows of 256 columns");
+    static_assert(!WT || BN >= 128, "transposed weights lie in rows of 8 granules or more");
     constexpr int MT = BM / WM / 16;               // 16-row tiles of a wave
     constexpr int kWStage = BN * 128, kXStage = BM * 128;
     constexpr int kStage = kWStage + kXStage;
@@ -357,8 +383,9 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void expert_linear_kernel(LinearK 
             // behind the matrix: their products are not stored
             if (c >= N) woff[j] = kOutOfRange;
         } else {
-            const int kr = (j * kWaves + wave) * 2 + (lane >> 5);
-            const int c16 = lane & 31;
+            constexpr int kLanes = BN / 8;             // lanes of a row
+            const int kr = (j * kWaves + wave) * (64 / kLanes) + lane / kLanes;
+            const int c16 = lane % kLanes;
             const int c = column(((c16 >> 1) ^ granule_of(kr)) * 16 + (c16 & 1) * 8);
             wk[j] = kr;
             woff[j] = (uint32_t)kr * (uint32_t)N * 2 + (uint32_t)c * 2;
@@ -366,7 +393,8 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void expert_linear_kernel(LinearK 
         }
     }
     const uint32_t lds0 = lds_offset(lds);
-    const int steps = (K + BK - 1) / BK;
+    const int begin = MODE == kSums ? blockIdx.y * a.split : 0;
+    const int steps = MODE == kSums ? min((K + BK - 1) / BK, begin + a.split) : (K + BK - 1) / BK;
     // copies of x that hold a row, of this wave's: the others are left out, and
     // the rows behind the segment are what the LDS holds (they go nowhere)
     const int xl = max(0, min(XL, ((rows + 7) / 8 - wave + kWaves - 1) / kWaves));
@@ -425,7 +453,7 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void expert_linear_kernel(LinearK 
         for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int t = 0; t < 4; ++t)
-                wf[t][h] = WT ? transposed_operand<512>(wl, wn * 4 + t, h)
+                wf[t][h] = WT ? transposed_operand<BN * 2>(wl, wn * 4 + t, h)
                               : *(const ep_u32x4 *)(wl + (wn * 4 + t) * 2048 + (slot ^ (h * 64)));
         auto read_x = [&](int i) __attribute__((always_inline)) {
 #pragma unroll
@@ -470,7 +498,7 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void expert_linear_kernel(LinearK 
     };
 
     for (int s = 0; s < NS - 1; ++s)
-        if (s < steps) copy(s, s);
+        if (begin + s < steps) copy(begin + s, s);
     int stage = 0;
     auto step = [&](int s, auto sb) {
         // stage s has landed once at most the copies of the steps after it
@@ -495,9 +523,14 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void expert_linear_kernel(LinearK 
             if (s + 3 < steps) step(s + 3, std::integral_constant<int, 3>{});
         }
     } else {
-        for (int s = 0; s < steps; ++s) step(s, std::integral_constant<int, 0>{});
+        for (int s = begin; s < steps; ++s) step(s, std::integral_constant<int, 0>{});
     }
     dma_wait<0>();
+    if constexpr (MODE == kSums) {
+        store_sums<GATED, 4, MT>(a, row0 + wm * 16, WM * 16, rows - wm * 16, acc,
+                          [&](int t) { return column(wn * 64 + t * 16); });
+        return;
+    }
     barrier_only();                                    // the stages are the epilogue's now
     constexpr int BT = MT > 4 ? MT / 2 : MT;           // row tiles of an epilogue batch
     static_assert(kWaves * BT * 4096 <= NS * kStage && MT % BT == 0, "a batch must fit the stages");
@@ -774,6 +807,113 @@ inline int64_t grid_of(const SegmentRows &seg, int col_tiles, int BM) {
     const int64_t most = seg.pairs < seg.num_rows ? seg.pairs : seg.num_rows;
     const int64_t some = most < seg.E ? most : seg.E;
     return ((most / BM + some) * col_tiles + 7) / 8 * 8;
+}
+
+// What the epilogue does, from the fp32 sums that the parts of a contraction left:
+// they are added in order.  A thread takes 8 columns of out.
+template <int MODE, bool GATED>
+__global__ __launch_bounds__(256) void finish_kernel(LinearK a, int parts) {
+    constexpr int NK = GATED ? 2 : 1;
+    const int per = a.m / 8;
+    const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t row = at / per;
+    if (row >= a.seg.num_rows) return;
+    const int col = (int)(at - row * per) * 8;
+    const int m = a.m;
+    const int64_t part = a.seg.num_rows * a.n;
+    float z[NK][8];
+#pragma unroll
+    for (int k = 0; k < NK; ++k) {
+        const float *p = a.sums + row * a.n + k * m + col;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) z[k][j] = 0.0f;
+#pragma unroll 4
+        for (int s = 0; s < parts; ++s) {
+            const ep_f32x4 lo = *(const ep_f32x4 *)(p + s * part), hi = *(const ep_f32x4 *)(p + s * part + 4);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                z[k][j] += lo[j];
+                z[k][4 + j] += hi[j];
+            }
+        }
+        if (a.bias) {
+            const ep_u32x4 b = *(const ep_u32x4 *)(a.bias + k * m + col);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                z[k][2 * j] += bf16_lo(b[j]);
+                z[k][2 * j + 1] += bf16_hi(b[j]);
+            }
+        }
+    }
+    if constexpr (MODE == kBackward) {
+        write_backward(a, row, col, z[0], *(const ep_u32x4 *)(a.pre + row * 2 * m + col),
+                       *(const ep_u32x4 *)(a.pre + row * 2 * m + m + col), a.kind);
+        return;
+    }
+    if constexpr (MODE == kKeep) {
+#pragma unroll
+        for (int k = 0; k < NK; ++k)
+            *(ep_u32x4 *)(a.kept + row * a.n + k * m + col) =
+                ep_u32x4{pack_bf16(z[k][0], z[k][1]), pack_bf16(z[k][2], z[k][3]),
+                         pack_bf16(z[k][4], z[k][5]), pack_bf16(z[k][6], z[k][7])};
+    }
+    float y[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        y[j] = a.kind == 0 ? z[0][j] : a.kind == 1 ? act_value<1>(z[0][j]) : act_value<2>(z[0][j]);
+        if (GATED) y[j] *= z[NK - 1][j];
+    }
+    if (a.residual) {
+        const ep_u32x4 r = *(const ep_u32x4 *)(a.residual + row * m + col);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            y[2 * j] += bf16_lo(r[j]);
+            y[2 * j + 1] += bf16_hi(r[j]);
+        }
+    }
+    *(ep_u32x4 *)(a.out + row * m + col) = ep_u32x4{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]),
+                                                    pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7])};
+}
+
+template <int MODE, bool GATED>
+hipError_t launch_finish(const LinearK &k, int parts, hipStream_t stream) {
+    const int64_t threads = k.seg.num_rows * (k.m / 8);
+    finish_kernel<MODE, GATED><<<dim3((unsigned)((threads + 255) / 256)), 256, 0, stream>>>(k, parts);
+    return hipGetLastError();
+}
+
+// How a product of dense rows, whose number the host knows, is divided: tiles of
+// `rows` x `cols` columns of z, and the contraction in `parts` of `split` steps whose
+// fp32 sums pass through memory (finish_kernel), where few tiles would leave compute
+// units idle.
+//   256 x 256   from 112 tiles on: 1500 rows, 2048 to 7168 (168 tiles) 46 us, in 128 x
+//               128 tiles 73; 4096 to 7168 on transposed weights 83 and 130; but 7168 to
+//               4096 (96 tiles) 124 and 118
+//   64 x 64     weights as they lie, short contractions, all tiles at once (512):
+//               512 to 512, 64 rows 6.5 us, in parts 7.4; 2048 to 7168, 64 rows 15.5
+//               and 14.1
+//   128 x 128   from 150 tiles on (700 rows, 7168 to 4096, 2 parts: 62 us, in 64 x 128
+//               tiles 69), else
+//   64 x 128    (333 rows, 7168 to 2048 on transposed weights, 96 tiles in 4 parts: 26.7
+//               us, in 128 x 128 tiles 28.4, whole in 256 x 256 tiles 126)
+// Parts: as many as make 400 workgroups of the tiles (two run on a compute unit), at
+// most 8 (more only move more sums) of at least 4 steps.
+struct DensePlan { int rows, cols, parts, split; };
+
+inline DensePlan dense_plan(int64_t rows, int n, int steps, bool transposed) {
+    auto tiles = [&](int r, int c) { return (rows + r - 1) / r * ((n + c - 1) / c); };
+    if (tiles(256, 256) >= 112) return {256, 256, 1, steps};
+    if (!transposed && steps < 32 && tiles(64, 64) <= 512) return {64, 64, 1, steps};
+    const int r = tiles(128, 128) >= 150 ? 128 : 64;
+    int64_t parts = std::min<int64_t>(400 / std::max<int64_t>(1, tiles(r, 128)), std::min(8, steps / 4));
+    parts = std::max<int64_t>(parts, 1);
+    const int split = (int)((steps + parts - 1) / parts);
+    return {r, 128, (steps + split - 1) / split, split};
+}
+
+// Bytes of the sums.
+inline size_t sums_bytes(const DensePlan &p, int64_t rows, int n) {
+    return p.parts > 1 ? (size_t)p.parts * rows * n * 4 : 0;
 }
 
 // The rows of a tile and the columns of out that it covers.

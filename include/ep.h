@@ -594,6 +594,10 @@ int ep_moe_decode(const void *x, const int64_t *topk_idx, const float *topk_weig
 int ep_cast_fp8_blocks(const void *w, int32_t num, int32_t n, int32_t k, uint8_t *codes,
                        float *scales, uint8_t *codes_t, float *scales_t, void *stream);
 
+/* Bytes of device workspace a product of dense rows needs (host call; 0: none, or
+ * sizes it does not take).  With a layout none is needed. */
+size_t ep_block_linear_workspace_bytes(int64_t num_rows, int32_t n, int32_t k);
+
 /* ep_block_linear - the matrix product with these scales and its epilogue: with
  * b = k/128 blocks,
  *   z[r, c] = sum_b x_scales[r, b] w_scales[c/128, b] sum over the block's k of x[r, k] w[c, k]
@@ -611,18 +615,21 @@ int ep_cast_fp8_blocks(const void *w, int32_t num, int32_t n, int32_t k, uint8_t
  *   params, layout  the receive layout of the rows (expert-major), as for
  *              ep_expert_linear: of x, x_scales, residual and out only rows that hold
  *              a pair are read or written; or both NULL: num_rows dense rows, E = 1.
+ *   workspace  device, 16-byte aligned, >= ep_block_linear_workspace_bytes for
+ *              dense rows (scratch of this call), else unused.
  *   out        device bf16 [num_rows, m], 16-byte aligned.
  * A block's sum is the fp8 instruction's (fp32; it cuts products below 2^-13 of
  * the largest of their 8 channels); the blocks are scaled and added in fp32.  The
  * data gradient is the same call on gradient rows cast to 8 bits and the codes_t of
  * the weights.  Two calls on the same inputs give the same bits; a row's result does
  * not depend on the others' values, but with another number of rows its sums may be
- * formed in another order.  Errors: EP_ERR_INVALID_ARG; EP_ERR_UNSUPPORTED (k or n
- * above EP_MAX_HIDDEN, a matrix of 2^31 - 4096 bytes or more). */
+ * formed in another order.  Errors: EP_ERR_INVALID_ARG; EP_ERR_WORKSPACE;
+ * EP_ERR_UNSUPPORTED (k or n above EP_MAX_HIDDEN, a matrix of 2^31 - 4096 bytes or
+ * more). */
 int ep_block_linear(const void *x, const float *x_scales, const void *w, const float *w_scales,
                     int32_t n, int32_t k, const void *bias, int act, const void *residual,
                     const ep_layout_params *params, const ep_layout *layout, int64_t num_rows,
-                    void *out, void *stream);
+                    void *workspace, size_t workspace_bytes, void *out, void *stream);
 
 /* The gated feed-forward block that every token passes (a shared expert; its
  * output, or that of the routed experts, is the other's bias or residual):
@@ -630,7 +637,8 @@ int ep_block_linear(const void *x, const float *x_scales, const void *w, const f
 
 /* Bytes of device workspace of the block's two calls (host call), or 0 for sizes
  * they do not take. */
-size_t ep_gated_ffn_workspace_bytes(int64_t num_tokens, int32_t inter, int backward);
+size_t ep_gated_ffn_workspace_bytes(int64_t num_tokens, int32_t hidden, int32_t inter,
+                                    int backward);
 
 /* ep_gated_ffn - the block's forward pass.
  *
@@ -640,8 +648,8 @@ size_t ep_gated_ffn_workspace_bytes(int64_t num_tokens, int32_t inter, int backw
  *   act        EP_ACT_SWIGLU or EP_ACT_GEGLU.
  *   residual   device bf16 [T, H] or NULL; it may be out.
  *   z          device bf16 [T, 2 I] or NULL: z kept for ep_gated_ffn_backward.
- *   workspace  device, >= ep_gated_ffn_workspace_bytes(T, I, 0); scratch of this
- *              call (h).
+ *   workspace  device, >= ep_gated_ffn_workspace_bytes(T, H, I, 0); scratch of this
+ *              call.
  *   out        device bf16 [T, H].
  * All 16-byte aligned; outputs must not overlap inputs, except as named.  Sums are
  * fp32; z, h and out are rounded to bf16 (h is formed from the sums, not from the
@@ -663,7 +671,7 @@ int ep_gated_ffn(const void *x, int64_t num_tokens, int32_t hidden, int32_t inte
  *   w1, w2, act  as in the forward pass.
  *   dw1_in, dw2_in  gradients to add to, of dw's type, or NULL each; they may be
  *              dw1 and dw2 themselves.
- *   workspace  device, >= ep_gated_ffn_workspace_bytes(T, I, 1); scratch (dz, h).
+ *   workspace  device, >= ep_gated_ffn_workspace_bytes(T, H, I, 1); scratch.
  *   dx         device bf16 [T, H] or NULL.
  *   dw1, dw2   device [2 I, H], [H, I]: float (dw_bf16 = 0) or bf16 (1).  Without
  *              tokens they are zeros (or dw1_in, dw2_in).

@@ -34,11 +34,11 @@ def test_cast(kw, code):
 
 
 def linear(x=16, xs=16, w=16, ws=16, n=64, k=128, b=None, act=0, res=None, p=None, lay=None,
-           rows=32, out=16):
+           rows=32, wk=None, nb=0, out=16):
     return _abi.load().ep_block_linear(V(x), V(xs), V(w), V(ws), n, k, V(b), act, V(res),
                                        None if p is None else ctypes.byref(p),
-                                       None if lay is None else ctypes.byref(lay), rows, V(out),
-                                       None)
+                                       None if lay is None else ctypes.byref(lay), rows, V(wk), nb,
+                                       V(out), None)
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -53,6 +53,8 @@ def linear(x=16, xs=16, w=16, ws=16, n=64, k=128, b=None, act=0, res=None, p=Non
     (dict(p=_params(), lay=_abi.LayoutPtrs(None, *([16] * 6))), INV),
     (dict(p=_params(), lay=PTRS, rows=-1), INV),
     (dict(n=(1 << 20) + 8), UNS), (dict(k=(1 << 20) + 128), UNS), (dict(n=1 << 20, k=1 << 11), UNS),
+    (dict(rows=100, k=8192), WS), (dict(rows=100, k=8192, wk=8, nb=1 << 30), WS),
+    (dict(rows=100, k=8192, wk=16, nb=100 * 64 * 4), WS),
     (dict(rows=0, x=None, xs=None, w=None, ws=None, out=None), OK),
     (dict(p=_params(T=0), lay=PTRS, x=None, out=None), OK),
 ])
@@ -99,14 +101,18 @@ def test_ffn_backward(kw, code):
     assert ffn_backward(**kw) == code
 
 
-def test_ffn_workspace():
+def test_workspaces():
     f = _abi.load().ep_gated_ffn_workspace_bytes
-    for T, inter in [(1, 8), (7, 1408), (128, 2048), (1 << 20, 4096)]:
-        assert f(T, inter, 0) >= 2 * T * inter and f(T, inter, 1) >= 6 * T * inter
-    assert f(0, 8, 0) > 0
+    for T, H, inter in [(1, 64, 8), (7, 128, 1408), (128, 7168, 2048), (1 << 20, 4096, 4096)]:
+        assert f(T, H, inter, 0) >= 2 * T * inter and f(T, H, inter, 1) >= 6 * T * inter
+    assert f(0, 8, 8, 0) > 0
     assert ffn(T=7, I=1408, nb=2 * 7 * 1408 - 1) == WS
     assert ffn_backward(T=7, I=1408, nb=6 * 7 * 1408 - 1) == WS
-    assert f(-1, 8, 0) == f(1, 0, 0) == f(1, 8, 2) == f(1 << 31, 8, 0) == f(1, (1 << 19) + 8, 0) == 0
+    assert f(-1, 8, 8, 0) == f(1, 8, 0, 0) == f(1, 0, 8, 0) == f(1, 8, 8, 2) == f(1 << 31, 8, 8, 0) == 0
+    assert f(1, 8, (1 << 19) + 8, 0) == 0
+    g = _abi.load().ep_block_linear_workspace_bytes
+    assert g(100, 64, 8192) >= 2 * 100 * 64 * 4 and g(0, 64, 128) == g(100000, 4096, 128) == 0
+    assert g(-1, 64, 128) == g(100, 0, 128) == g(100, 64, 0) == g(1 << 31, 64, 128) == 0
 
 
 def test_binding_refuses():
