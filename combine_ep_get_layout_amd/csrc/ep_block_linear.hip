@@ -206,13 +206,14 @@ DensePlan plan_of(int64_t rows, int n, int k) { return dense_plan(rows, n, k / k
 hipError_t launch_dense(BlockK &k, bool gated, hipStream_t stream) {
     const DensePlan p = plan_of(k.l.seg.num_rows, k.l.n, k.l.k);
     if (p.rows == 256) return launch_tiles<256, 2, 4, 2>(k, gated, 1, stream);
-    if (p.cols == 64) return launch_tiles<64, 4, 1, 4>(k, gated, 1, stream);
+    if (p.parts == 1 && p.cols == 64) return launch_tiles<64, 4, 1, 4>(k, gated, 1, stream);
     if (p.parts == 1)
         return p.rows == 128 ? launch_tiles<128, 2, 2, 2>(k, gated, 1, stream)
                              : launch_tiles<64, 2, 2, 3>(k, gated, 1, stream);
     k.l.split = p.split;
-    const hipError_t rc = p.rows == 128 ? launch_tiles<128, 2, 2, 2, kSums>(k, gated, p.parts, stream)
-                                        : launch_tiles<64, 2, 2, 3, kSums>(k, gated, p.parts, stream);
+    const hipError_t rc = p.cols == 64 ? launch_tiles<64, 4, 1, 4, kSums>(k, gated, p.parts, stream)
+                          : p.rows == 128 ? launch_tiles<128, 2, 2, 2, kSums>(k, gated, p.parts, stream)
+                                          : launch_tiles<64, 2, 2, 3, kSums>(k, gated, p.parts, stream);
     if (rc != hipSuccess) return rc;
     return gated ? launch_finish<kPlain, true>(k.l, p.parts, stream)
                  : launch_finish<kPlain, false>(k.l, p.parts, stream);
@@ -221,11 +222,11 @@ hipError_t launch_dense(BlockK &k, bool gated, hipStream_t stream) {
 }  // namespace
 
 size_t block_linear_sums_bytes(int64_t rows, int n, int k) {
-    return rows <= kFewRows ? 0 : sums_bytes(plan_of(rows, n, k), rows, n);
+    return few_rows(rows, k) ? 0 : sums_bytes(plan_of(rows, n, k), rows, n);
 }
 
 hipError_t launch_block_linear(const BlockLinearArgs &a, hipStream_t stream) {
-    if (!a.seg.offsets && a.seg.num_rows <= kFewRows) {
+    if (!a.seg.offsets && few_rows(a.seg.num_rows, a.k)) {
         FewRowsArgs f = {};
         f.x = a.x;
         f.x_scales = a.x_scales;

@@ -88,8 +88,14 @@ inline int act_kind(int act) {
 }
 inline bool act_gated(int act) { return act == EP_ACT_SWIGLU || act == EP_ACT_GEGLU; }
 
-// Dense rows, at most kFewRows of them.
+// Dense rows, at most kFewRows of them.  Taken up to 16 rows, and for more while
+// they have few bytes, since every workgroup reads them: 7168 to 4096, gated, bf16, 24
+// rows 18.9 us, in tiles and parts 18.2, 64 rows 34 and 21; 2048 to 7168 32 rows 13.7
+// and 12.4; but 1024 to 4096, gated, 64 rows 7.5 and 9.2.
 constexpr int kFewRows = 64;
+inline bool few_rows(int64_t rows, int64_t row_bytes) {
+    return rows <= 16 || (rows <= kFewRows && rows * row_bytes <= 128 * 1024);
+}
 struct FewRowsArgs {
     const void *x;               // [rows, k]
     const float *x_scales;       // e4m3: [rows, k/128], bf16: NULL

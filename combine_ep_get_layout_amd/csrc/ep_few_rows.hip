@@ -2,12 +2,18 @@
 // + residual[t] for up to 64 rows, bf16, or e4m3 codes with one fp32 scale per
 // 128 channels of x and per 128 x 128 block of W.
 //
-// The weights are read once and little else, so what counts is how much of them
-// is in flight: a workgroup takes 16 rows of W (gated: 8 gate rows and the 8 up
-// rows that go with them), its eight waves split the contraction, and every wave
-// has several units of 16 rows x 128 bytes on their way to registers, in the
-// matrix instruction's layout.  The rows of x are its other operand, 16 columns
-// a group.  The eight partial sums meet in LDS and are added in wave order.
+// The weights are read once; the rows of x, from the caches, once per workgroup.  A
+// workgroup takes 16 rows of W (gated: 8 gate rows and the 8 up rows that go with
+// them), its four waves split the contraction, and each has its next units of 16
+// rows x 128 bytes on their way to registers, in the matrix instruction's layout.
+// The rows of x are its other operand, 16 columns a group.  The partial sums meet in
+// LDS and are added in wave order.
+//
+// Many small workgroups hide the latency better than deep rings: four waves with two
+// units each, where eight waves with eight units took (back to back) 13.6 us for one
+// row of 7168 to 4096, gated, in bf16, these take 11.0 (5.3 TB/s); 13.9 and 7.2 for
+// 2048 to 7168; e4m3 9.7 and 8.1, 12.5 and 5.2.  Bound by reading the weights up to about
+// 8 rows, then by reading x: 16 rows 15.0, 64 rows 34 us.
 #include "ep_expert_device.h"
 
 namespace ep {
@@ -16,7 +22,6 @@ namespace {
 
 typedef __amdgpu_buffer_rsrc_t Buffer;
 
-constexpr int kWaves = 8;
 constexpr int kUnit = 128;          // bytes of a row that a wave takes at once
 
 struct FewK {
@@ -31,10 +36,12 @@ struct Unit {
     float sw, sx[MT];
 };
 
+constexpr int kWaves = 4;
+
 template <bool FP8, bool GATED, int MT>
-__global__ __launch_bounds__(64 * kWaves, 2) void few_rows_kernel(FewK p) {
+__global__ __launch_bounds__(64 * kWaves) void few_rows_kernel(FewK p) {
     constexpr int ES = FP8 ? 1 : 2;
-    constexpr int D = MT == 1 ? 8 : MT == 2 ? 6 : 4;       // units on their way
+    constexpr int D = MT == 1 ? 2 : 1;                     // units on their way
     constexpr int COLS = GATED ? 8 : 16;
     const FewRowsArgs &a = p.a;
     __shared__ float red[kWaves][MT][16][16];              // [wave][group][row of W][row of x]
@@ -72,17 +79,21 @@ __global__ __launch_bounds__(64 * kWaves, 2) void few_rows_kernel(FewK p) {
 
     Unit<MT> ring[D];
     auto load = [&](Unit<MT> &v, int u) __attribute__((always_inline)) {
+        // past the row (or this wave's part): zeros
+        uint32_t out[2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            // past the row (or this wave's part): zeros
-            const uint32_t out = u >= u1 || (uint32_t)u * kUnit + h * 64 + q * 16 >= ld ? kOutOfRange : 0;
+        for (int h = 0; h < 2; ++h)
+            out[h] = u >= u1 || (uint32_t)u * kUnit + h * 64 + q * 16 >= ld ? kOutOfRange : 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
             v.w[h] = __builtin_bit_cast(ep_u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                wb, (wat + (uint32_t)u * kUnit + h * 64) | out, 0, 0));
+                wb, (wat + (uint32_t)u * kUnit + h * 64) | out[h], 0, 0));
 #pragma unroll
-            for (int i = 0; i < MT; ++i)
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
                 v.x[i][h] = __builtin_bit_cast(ep_u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                    xb, (xat[i] + (uint32_t)u * kUnit + h * 64) | out, 0, 0));
-        }
+                    xb, (xat[i] + (uint32_t)u * kUnit + h * 64) | out[h], 0, 0));
         if (FP8) {
             const uint32_t out = u >= u1 ? kOutOfRange : 0;
             v.sw = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(swb, (swat + u * 4) | out, 0, 0));

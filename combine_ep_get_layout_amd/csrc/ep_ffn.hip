@@ -46,30 +46,35 @@ hipError_t product(LinearK k, int64_t rows, float *sums, hipStream_t stream) {
         expert_linear_wide_kernel<kBf16, WT, GATED, MODE><<<dim3((unsigned)grid), 256, 0, stream>>>(k);
         return hipGetLastError();
     }
+    k.sums = sums;
+    k.split = p.split;
     if constexpr (!WT) {
-        if (p.cols == 64) return launch_tiles<64, 4, 1, 4, WT, GATED, MODE>(k, 1, stream);
+        if (p.cols == 64) {
+            if (p.parts == 1) return launch_tiles<64, 4, 1, 4, WT, GATED, MODE>(k, 1, stream);
+            const hipError_t rc = launch_tiles<64, 4, 1, 4, WT, GATED, kSums>(k, p.parts, stream);
+            return rc != hipSuccess ? rc : launch_finish<MODE, GATED>(k, p.parts, stream);
+        }
     }
     if (p.parts == 1)
         return p.rows == 128 ? launch_tiles<128, 2, 2, 2, WT, GATED, MODE>(k, 1, stream)
                              : launch_tiles<64, 2, 2, 3, WT, GATED, MODE>(k, 1, stream);
-    k.sums = sums;
-    k.split = p.split;
     const hipError_t rc = p.rows == 128 ? launch_tiles<128, 2, 2, 2, WT, GATED, kSums>(k, p.parts, stream)
                                         : launch_tiles<64, 2, 2, 3, WT, GATED, kSums>(k, p.parts, stream);
-    if (rc != hipSuccess) return rc;
-    return launch_finish<MODE, GATED>(k, p.parts, stream);
+    return rc != hipSuccess ? rc : launch_finish<MODE, GATED>(k, p.parts, stream);
 }
 
-hipError_t few_rows(const void *x, const void *w, int n, int k, int act, const void *residual,
-                    int64_t rows, void *out, hipStream_t stream) {
+// The same on weights as they lie, through the kernel for few rows where it is the faster.
+template <bool GATED>
+hipError_t forward_product(const LinearK &k, int act, int64_t rows, float *sums, hipStream_t stream) {
+    if (!few_rows(rows, (int64_t)k.k * 2)) return product<false, GATED, kPlain>(k, rows, sums, stream);
     FewRowsArgs f = {};
-    f.x = x;
-    f.w = w;
-    f.residual = residual;
-    f.out = out;
+    f.x = k.x;
+    f.w = k.w;
+    f.residual = k.residual;
+    f.out = k.out;
     f.rows = (int)rows;
-    f.n = n;
-    f.k = k;
+    f.n = k.n;
+    f.k = k.k;
     f.act = act;
     return launch_few_rows(f, stream);
 }
@@ -83,11 +88,6 @@ size_t gated_ffn_sums_bytes(int64_t rows, int hidden, int inter, bool backward) 
 }
 
 hipError_t launch_gated_ffn(const FfnArgs &a, hipStream_t stream) {
-    if (!a.z && a.rows <= kFewRows) {
-        const hipError_t rc = few_rows(a.x, a.w1, 2 * a.inter, a.hidden, a.act, nullptr, a.rows, a.h, stream);
-        if (rc != hipSuccess) return rc;
-        return few_rows(a.h, a.w2, a.hidden, a.inter, EP_ACT_NONE, a.residual, a.rows, a.out, stream);
-    }
     LinearK k = {};
     k.x = (const uint8_t *)a.x;
     k.w = (const uint8_t *)a.w1;
@@ -98,7 +98,7 @@ hipError_t launch_gated_ffn(const FfnArgs &a, hipStream_t stream) {
     k.m = a.inter;
     k.kind = act_kind(a.act);
     const hipError_t rc = a.z ? product<false, true, kKeep>(k, a.rows, a.sums, stream)
-                              : product<false, true, kPlain>(k, a.rows, a.sums, stream);
+                              : forward_product<true>(k, a.act, a.rows, a.sums, stream);
     if (rc != hipSuccess) return rc;
     LinearK d = {};
     d.x = (const uint8_t *)a.h;
@@ -107,7 +107,7 @@ hipError_t launch_gated_ffn(const FfnArgs &a, hipStream_t stream) {
     d.out = (uint16_t *)a.out;
     d.n = d.m = a.hidden;
     d.k = a.inter;
-    return product<false, false, kPlain>(d, a.rows, a.sums, stream);
+    return forward_product<false>(d, EP_ACT_NONE, a.rows, a.sums, stream);
 }
 
 hipError_t launch_gated_ffn_backward(const FfnBackwardArgs &a, hipStream_t stream) {

@@ -889,9 +889,10 @@ hipError_t launch_finish(const LinearK &k, int parts, hipStream_t stream) {
 //   256 x 256   from 112 tiles on: 1500 rows, 2048 to 7168 (168 tiles) 46 us, in 128 x
 //               128 tiles 73; 4096 to 7168 on transposed weights 83 and 130; but 7168 to
 //               4096 (96 tiles) 124 and 118
-//   64 x 64     weights as they lie, short contractions, all tiles at once (512):
-//               512 to 512, 64 rows 6.5 us, in parts 7.4; 2048 to 7168, 64 rows 15.5
-//               and 14.1
+//   64 x 64     weights as they lie: whole for short contractions while all tiles run at
+//               once (512 to 512, 64 rows 6.5 us, in parts 7.4; 2048 to 7168 15.4 and
+//               14.7); in parts up to 112 tiles of 64 x 128 (7168 to 4096, gated, 64 rows
+//               20.8 us, in 64 x 128 tiles 22.5, 128 rows 22.7 and 24.4, whole 43)
 //   128 x 128   from 150 tiles on (700 rows, 7168 to 4096, 2 parts: 62 us, in 64 x 128
 //               tiles 69), else
 //   64 x 128    (333 rows, 7168 to 2048 on transposed weights, 96 tiles in 4 parts: 26.7
@@ -905,10 +906,11 @@ inline DensePlan dense_plan(int64_t rows, int n, int steps, bool transposed) {
     if (tiles(256, 256) >= 112) return {256, 256, 1, steps};
     if (!transposed && steps < 32 && tiles(64, 64) <= 512) return {64, 64, 1, steps};
     const int r = tiles(128, 128) >= 150 ? 128 : 64;
-    int64_t parts = std::min<int64_t>(400 / std::max<int64_t>(1, tiles(r, 128)), std::min(8, steps / 4));
+    const int c = !transposed && tiles(64, 128) <= 112 ? 64 : 128;
+    int64_t parts = std::min<int64_t>(400 / std::max<int64_t>(1, tiles(r, c)), std::min(8, steps / 4));
     parts = std::max<int64_t>(parts, 1);
     const int split = (int)((steps + parts - 1) / parts);
-    return {r, 128, (steps + split - 1) / split, split};
+    return {r, c, (steps + split - 1) / split, split};
 }
 
 // Bytes of the sums.
