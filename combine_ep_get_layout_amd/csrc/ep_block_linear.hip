@@ -12,6 +12,11 @@
 // lie in ordinary registers, so eight waves of 64 columns x 128 rows share a tile of
 // 256 x 256, not four of 128 x 128.
 //
+// Bound by the matrix instructions under the power limit: 32768 rows, 7168 to 4096 with
+// swiglu 0.80 to 0.84 ms (2.3 to 2.4 PFLOP/s, 1.7 to 1.8 GHz; without the scales' instructions
+// 0.68 to 0.77, and what saves cycles costs clock), 2048 to 7168 0.47 ms (2.0: 7 of a
+// tile's 34 us are its ends).
+//
 // The weights are the instruction's first operand: a lane's values are consecutive
 // columns of one row, with one row scale, and a wave's 64 columns lie in one block
 // of the weights (gated: 32 gate and 32 up columns in one each).
@@ -58,9 +63,10 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void block_linear_kernel(BlockK p)
     const int rows = min(BM, at.rows - row0);
     const int groups = K / kFp8Group;
 
-    const ep_i32x4 xb = buffer_of(a.x + ((int64_t)at.row0 + row0) * K, (uint32_t)rows * K);
+    const uint32_t x_bytes = (uint32_t)rows * K;
+    ep_i32x4 xb = buffer_of(a.x + ((int64_t)at.row0 + row0) * K, x_bytes);
     const uint32_t w_bytes = (uint32_t)N * K;
-    const ep_i32x4 wb = buffer_of(a.w + (int64_t)at.e * w_bytes, w_bytes);
+    ep_i32x4 wb = buffer_of(a.w + (int64_t)at.e * w_bytes, w_bytes);
     const int wblocks = (N + kFp8Group - 1) / kFp8Group;
     const ep_i32x4 xsb = buffer_of(p.xs + ((int64_t)at.row0 + row0) * groups, (uint32_t)(rows * groups) * 4);
     const ep_i32x4 wsb = buffer_of(p.ws + (int64_t)at.e * wblocks * groups, (uint32_t)(wblocks * groups) * 4);
@@ -87,20 +93,30 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void block_linear_kernel(BlockK p)
         const int c = column(wn * 64 + (lane >> 2) * 32);
         if (c < N) wsoff = (uint32_t)(c / kFp8Group * groups + sk) * 4;
     }
-    const uint32_t lds0 = lds_offset(lds), slds0 = lds_offset(slds);
+    const uint32_t lds0 = lds_offset(lds), slds0 = lds0 + NS * kStage;
     const int begin = MODE == kSums ? blockIdx.y * a.split : 0;
     const int steps = MODE == kSums ? min(groups, begin + a.split) : groups;
-    auto copy = [&](int s, int stage) {
+    // The scales of the group of four steps that begins with step s (kSums: the rest of
+    // the group that the part begins in).
+    auto copy_scales = [&](int s) __attribute__((always_inline)) {
         if ((s & 3) == 0 || (MODE == kSums && s == begin)) {
             const uint32_t base = slds0 + (s >> 2 & 1) * kScales + wave * 256;
             const int s4 = s & ~3;
             const uint32_t past = s4 + sk >= groups ? kOutOfRange : 0;
-            for (int j = 0; j < SL; ++j) dma4(xsb, base + j * kWaves * 256, soff[j] | past, s4 * 4);
+            for (int i = 0; i < SL; ++i) dma4(xsb, base + i * kWaves * 256, soff[i] | past, s4 * 4);
             dma4(wsb, base + kXScales, wsoff | past, s4 * 4);
         }
-        const uint32_t base = lds0 + stage * kStage + wave * 1024;
-        for (int j = 0; j < WL; ++j) dma16(wb, base + j * kWaves * 1024, woff[j], s * 128);
-        for (int j = 0; j < XL; ++j) dma16(xb, base + kWStage + j * kWaves * 1024, xoff[j], s * 128);
+    };
+    // Copies behind the last step go on from empty buffers (they write zeros), so that
+    // the number in flight, which the waits count, stays the same.
+    uint32_t ws_off = 0, xs_off = 0;
+    auto copy_w = [&](int s, int stage, int j) __attribute__((always_inline)) {
+        if (j == 0) range_of(s, steps, w_bytes, s * 128, wb, &ws_off);
+        dma16(wb, lds0 + stage * kStage + (j * kWaves + wave) * 1024, woff[j], ws_off);
+    };
+    auto copy_x = [&](int s, int stage, int j) __attribute__((always_inline)) {
+        if (j == 0) range_of(s, steps, x_bytes, s * 128, xb, &xs_off);
+        dma16(xb, lds0 + stage * kStage + kWStage + (j * kWaves + wave) * 1024, xoff[j], xs_off);
     };
 
     ep_f32x4 acc[4][MT];
@@ -109,69 +125,126 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void block_linear_kernel(BlockK p)
 #pragma unroll
         for (int i = 0; i < MT; ++i) acc[t][i] = ep_f32x4{0, 0, 0, 0};
 
-    const int slot = l16 * 128 + (q ^ (l16 >> 1)) * 16;
-    auto compute = [&](int s, int stage) {
-        const uint8_t *wl = lds + stage * kStage;
-        const uint8_t *xl = wl + kWStage + wm * 2048;
-        const uint8_t *sl = slds + (s >> 2 & 1) * kScales + (s & 3) * 4;
-        ep_u32x4 wf[4][2], xf[2][2];
-        auto read_x = [&](int i) __attribute__((always_inline)) {
+    // A step multiplies its row tiles in turn, each by the four weight tiles, the last
+    // two together.  When their operands are in registers, nothing more is read of the
+    // stage: the wait for the next one and the barrier stand there, and the rows' copies
+    // for step s + NS and the first reads of the next step go among the last products,
+    // the weights' copies among the first ones of the next step, so that the matrix
+    // instructions run on across the steps.  (A compute unit takes 16 cycles for the
+    // addresses of each copy: all 64 of a step behind the barrier held the waves up, 3400
+    // cycles a step where these take 2930, 2048 of them matrix instructions.)
+    constexpr int kLast = MT >= 2 ? 2 : 1;             // row tiles behind the barrier
+    constexpr int kFirst = 4 * (MT - kLast);           // products before it
+    constexpr int kSlots = MT == 4 ? 4 : 3;            // x tiles in registers
+    // (The last two lie in slots 0 and 1, or 2 and 3 of four; tile 0 not in the second's.)
+    auto slot_of = [](int i) constexpr { return MT == 4 ? i : (i + 24 - (MT - kLast)) % 3; };
+    auto row_of = [](int n) constexpr {
+        return n < kFirst ? n / 4 : kLast == 1 ? 0 : MT - 2 + (0xCA >> (n - kFirst) & 1);
+    };
+    auto col_of = [](int n) constexpr {
+        return n < kFirst || kLast == 1 ? n % 4 : (int)(0x32321100u >> (4 * (n - kFirst)) & 3);
+    };
+    const int place = l16 * 128 + (q ^ (l16 >> 1)) * 16;
+    ep_u32x4 wf[4][2], xf[kSlots][2];
+    float sx[kSlots], sw[2];
+    auto read_w = [&](int stage, int t) __attribute__((always_inline)) {
+        const uint8_t *p = lds + stage * kStage + (wn * 4 + t) * 2048;
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-                xf[i & 1][h] = *(const ep_u32x4 *)(xl + i * WM * 2048 + (slot ^ (h * 64)));
-        };
+        for (int h = 0; h < 2; ++h) wf[t][h] = *(const ep_u32x4 *)(p + (place ^ (h * 64)));
+    };
+    auto read_x = [&](int stage, int i) __attribute__((always_inline)) {
+        const uint8_t *p = lds + stage * kStage + kWStage + (i * WM + wm) * 2048;
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+        for (int h = 0; h < 2; ++h) xf[slot_of(i)][h] = *(const ep_u32x4 *)(p + (place ^ (h * 64)));
+    };
+    auto scale_at = [&](int s, int offset) __attribute__((always_inline)) {
+        return *(const float *)(slds + (s >> 2 & 1) * kScales + (s & 3) * 4 + offset);
+    };
+    auto x_scale = [&](int s, int i) { return scale_at(s, ((i * WM + wm) * 16 + l16) * 16); };
+    auto w_scale = [&](int s, int g) { return scale_at(s, kXScales + wave * 256 + (GATED ? g * 16 : 0)); };
+    // all but the newest copies have landed: those of the `ahead` steps behind step s
+    auto landed = [&](int s, auto nn) {
+        constexpr int ahead = decltype(nn)::value;
+        bool scales = false;                           // those of a group of four among them
+        for (int j = 1; j <= ahead; ++j) scales |= ((s + j) & 3) == 0;
+        if (scales) dma_wait<ahead * (WL + XL) + SL + 1>();
+        else dma_wait<ahead * (WL + XL)>();
+        barrier_only();
+    };
+
+    // (the weights of the last stage are copied in the first step)
+    for (int s = 0; s < NS; ++s) {
+        if (kFirst == 0 || s < NS - 1)
+            for (int j = 0; j < WL; ++j) copy_w(begin + s, s, j);
+        copy_scales(begin + s);
+        for (int j = 0; j < XL; ++j) copy_x(begin + s, s, j);
+    }
+    dma_wait<0>();
+    barrier_only();
+    read_x(0, 0);
+    if (MT == 2) read_x(0, 1);
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-                wf[t][h] = *(const ep_u32x4 *)(wl + (wn * 4 + t) * 2048 + (slot ^ (h * 64)));
-        read_x(0);
-        float sx[MT], sw[2];
-        sw[0] = *(const float *)(sl + kXScales + wave * 256);
-        sw[1] = GATED ? *(const float *)(sl + kXScales + wave * 256 + 16) : sw[0];
-#pragma unroll
-        for (int i = 0; i < MT; ++i) sx[i] = *(const float *)(sl + ((i * WM + wm) * 16 + l16) * 16);
-        __builtin_amdgcn_sched_barrier(0);
-        // the product of tile n is added to the sums two tiles later
+    for (int t = 0; t < 4; ++t) read_w(0, t);
+    sx[slot_of(0)] = x_scale(begin, 0);
+    sw[0] = w_scale(begin, 0);
+    sw[1] = w_scale(begin, 1);
+    int stage = 0;
+    for (int s = begin; s < steps; ++s) {
+        const int next = stage + 1 == NS ? 0 : stage + 1, before = stage == 0 ? NS - 1 : stage - 1;
+        float sx_next = 0.0f, sw_next[2] = {0.0f, 0.0f};
+        if (MT == 2) sx[slot_of(1)] = x_scale(s, 1);
+        // a product is added to the sums two products later
         ep_f32x4 part[3];
         auto add = [&](auto nn) __attribute__((always_inline)) {
-            constexpr int n = decltype(nn)::value, i = n >> 2, t = n & 3;
-            const float f = sx[i] * sw[t >> 1];
+            constexpr int n = decltype(nn)::value, i = row_of(n), t = col_of(n);
+            const float f = sx[slot_of(i)] * sw[t >> 1];
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[t][i][j] = __builtin_fmaf(part[n % 3][j], f, acc[t][i][j]);
+            pin(acc[t][i]);    // (the compiler would put all of them behind the products)
         };
         each<4 * MT>([&](auto nn) __attribute__((always_inline)) {
-            constexpr int n = decltype(nn)::value, i = n >> 2, t = n & 3;
-            if constexpr (t == 0 && i + 1 < MT) read_x(i + 1);
-            part[n % 3] = mfma_fp8_plain(wf[t], xf[i & 1], ep_f32x4{0, 0, 0, 0});
+            constexpr int n = decltype(nn)::value, i = row_of(n), t = col_of(n);
+            if constexpr (n == kFirst) {
+                landed(s + 1, std::integral_constant<int, NS - 2>{});
+                copy_scales(s + NS);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            part[n % 3] = mfma_fp8_plain(wf[t], xf[slot_of(i)], ep_f32x4{0, 0, 0, 0});
+            if constexpr (n < kFirst) {
+                constexpr int kEvery = kFirst >= 16 ? 3 : 1;
+                if constexpr (n % kEvery == 0 && n / kEvery < WL) copy_w(s + NS - 1, before, n / kEvery);
+                // the next tile's operands (and, before the barrier, the one's after it)
+                if constexpr (t == 0) {
+                    read_x(stage, i + 1);
+                    sx[slot_of(i + 1)] = x_scale(s, i + 1);
+                }
+                if constexpr (t == 2 && i == MT - 3) {
+                    read_x(stage, MT - 1);
+                    sx[slot_of(MT - 1)] = x_scale(s, MT - 1);
+                }
+            } else {
+                constexpr int m = n - kFirst, kEvery = 4 * kLast / XL;
+                if constexpr (kFirst == 0 && m == 0)
+                    for (int j = 0; j < WL; ++j) copy_w(s + NS, stage, j);
+                if constexpr (m % kEvery == 0 && m / kEvery < XL) copy_x(s + NS, stage, m / kEvery);
+                if constexpr (i == MT - 1) read_w(next, t);         // the tile's last product
+                if constexpr (m == (kLast == 2 ? 5 : 3)) {
+                    read_x(next, 0);
+                    sx_next = x_scale(s + 1, 0);
+                    sw_next[0] = w_scale(s + 1, 0);
+                    sw_next[1] = w_scale(s + 1, 1);
+                }
+            }
             if constexpr (n >= 2) add(std::integral_constant<int, n - 2>{});
             __builtin_amdgcn_sched_barrier(0);
         });
+        if (MT == 2) read_x(next, 1);
         add(std::integral_constant<int, 4 * MT - 2>{});
         add(std::integral_constant<int, 4 * MT - 1>{});
-    };
-
-    for (int s = 0; s < NS - 1; ++s)
-        if (begin + s < steps) copy(begin + s, s);
-    // stage s has landed once at most the copies of the steps after it are in
-    // flight, with the scales of those that begin a group of four; near the end
-    // there are none, and all are waited for
-    constexpr int kAhead = NS - 2;                     // whole steps that may be in flight
-    int stage = 0;
-    for (int s = begin; s < steps; ++s) {
-        if (kAhead == 0 || s + kAhead >= steps) {
-            dma_wait<0>();
-        } else {
-            bool first = false;
-            for (int j = 1; j <= kAhead; ++j) first |= (s + j & 3) == 0;
-            if (first) dma_wait<kAhead * (WL + XL) + SL + 1>();
-            else dma_wait<kAhead * (WL + XL)>();
-        }
-        barrier_only();
-        const int next = stage == 0 ? NS - 1 : stage - 1;
-        if (s + NS - 1 < steps) copy(s + NS - 1, next);
-        compute(s, stage);
-        stage = stage + 1 == NS ? 0 : stage + 1;
+        sx[slot_of(0)] = sx_next;
+        sw[0] = sw_next[0];
+        sw[1] = sw_next[1];
+        stage = next;
     }
     dma_wait<0>();
     if constexpr (MODE == kSums) {
@@ -182,7 +255,7 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void block_linear_kernel(BlockK p)
     barrier_only();                                    // the stages are the epilogue's now
     constexpr int BT = MT > 4 ? MT / 2 : MT;           // row tiles of an epilogue batch
     static_assert(kWaves * BT * 4096 <= NS * kStage && MT % BT == 0, "a batch must fit the stages");
-    static_assert(NS - 1 <= 4, "a group's scales are read before the copies of the group after the next");
+    static_assert(NS <= 4, "a group's scales are read before the copies of the group after the next");
     Output<4, BT, WM * 16, GATED> o;
     o.load(a, at, row0 + wm * 16, rows - wm * 16, column(wn * 64), 0);
     epilogue<4, MT, BT, WM * 16, GATED, kPlain>(a, at, lds + wave * BT * 4096, row0 + wm * 16,
@@ -257,11 +330,15 @@ hipError_t launch_block_linear(const BlockLinearArgs &a, hipStream_t stream) {
     k.l.kind = act_kind(a.act);
     k.l.sums = a.sums;
     if (!a.seg.offsets) return launch_dense(k, gated, stream);
+    // Small products as the experts' other ones.  Then by the rows an expert can expect:
+    // 64 experts of 7168 x 4096, 128 rows each, uniform routing, 430 us in tiles of 128,
+    // 441 of 192, 467 of 256 rows; 144 rows 512, 450, 473; 176 rows 487 of 256 rows.
     const RowTile tile = row_tile(a.seg, k.l.m, gated, false);
     if (tile.rows == 64) return launch_tiles<64, 4, 1, 4>(k, gated, 1, stream);
-    if (tile.rows == 256) return launch_tiles<256, 2, 4, 2>(k, gated, 1, stream);
-    if (tile.rows == 192) return launch_tiles<192, 2, 4, 2>(k, gated, 1, stream);
-    return launch_tiles<128, 2, 4, 3>(k, gated, 1, stream);
+    const int64_t avg = a.seg.pairs / a.seg.E;
+    if (avg <= 136) return launch_tiles<128, 2, 4, 3>(k, gated, 1, stream);
+    if (avg <= 168) return launch_tiles<192, 2, 4, 2>(k, gated, 1, stream);
+    return launch_tiles<256, 2, 4, 2>(k, gated, 1, stream);
 }
 
 }  // namespace ep
