@@ -9,6 +9,8 @@
 //
 // fp8 rows of x (kept in 8 bits by the forward pass) become bf16 on the way:
 // exact, the scales are powers of two.
+#include <algorithm>
+
 #include "ep_expert_device.h"
 
 namespace ep {
@@ -35,9 +37,9 @@ struct WgradK {
 // workgroup.  Runs of 32 tiles (8 x 4 of them where the grid has them) go to one
 // XCD, the runs to the XCDs in turn: the operands of a run meet in one L2, and
 // an expert with more rows than others spreads over all XCDs.
-__device__ __forceinline__ bool tile_of(const WgradK &a, int T, int *e, int *n0, int *k0) {
-    const int j = blockIdx.x >> 3;
-    const uint32_t t = ((uint32_t)(j >> 5) * 8 + (blockIdx.x & 7)) * 32 + (j & 31);
+__device__ __forceinline__ bool tile_of(const WgradK &a, int T, int block, int *e, int *n0, int *k0) {
+    const int j = block >> 3;
+    const uint32_t t = ((uint32_t)(j >> 5) * 8 + (block & 7)) * 32 + (j & 31);
     const uint32_t per_e = (uint32_t)a.tiles_n * (uint32_t)a.tiles_k;
     *e = (int)(t / per_e);
     if (*e >= a.seg.E) return false;
@@ -134,10 +136,10 @@ constexpr int kOperand = kRows * kT * 2;
 constexpr int kStage = 2 * kOperand;
 
 template <bool FP8, bool BIAS>
-__global__ __launch_bounds__(256, 2) void expert_wgrad_kernel(WgradK a) {
+__device__ __forceinline__ void wgrad_tile(const WgradK &a, int block) {
     __shared__ __align__(1024) uint8_t lds[2 * kStage];
     int e, n0, k0;
-    if (!tile_of(a, kT, &e, &n0, &k0)) return;
+    if (!tile_of(a, kT, block, &e, &n0, &k0)) return;
     int row0 = 0;
     const int rows = wave_uniform(segment_rows(a.seg, e, &row0));
     row0 = wave_uniform(row0);
@@ -264,6 +266,23 @@ __global__ __launch_bounds__(256, 2) void expert_wgrad_kernel(WgradK a) {
     }
 }
 
+template <bool FP8, bool BIAS>
+__global__ __launch_bounds__(256, 2) void expert_wgrad_kernel(WgradK a) {
+    wgrad_tile<FP8, BIAS>(a, blockIdx.x);
+}
+
+// Two products in one launch, the second's tiles from workgroup `first` on.
+struct WgradPair {
+    WgradK a, b;
+    int first;
+};
+
+__global__ __launch_bounds__(256, 2) void wgrad_pair_kernel(WgradPair p) {
+    const bool second = (int)blockIdx.x >= p.first;
+    const WgradK a = second ? p.b : p.a;
+    wgrad_tile<false, false>(a, second ? blockIdx.x - p.first : blockIdx.x);
+}
+
 // Tiles of 256 x 256, for many rows an expert: bound by the matrix instructions.
 // Four waves of 128 x 128 in phases as in the linear kernel's wide tiles: regions
 // X0, X1 (the waves' first and second 64 channels of x) and Y0, Y1 (of dy's
@@ -283,7 +302,7 @@ constexpr int kWT = 256;
 constexpr int kRegion = kRows * 128 * 2;
 
 template <bool FP8, bool BIAS>
-__global__ __launch_bounds__(256, 1) void expert_wgrad_wide_kernel(WgradK a) {
+__device__ __forceinline__ void wgrad_wide_tile(const WgradK &a, int block) {
     constexpr int kX = FP8 ? 2 * kRegion : 4 * kRegion;          // x regions of all stages
     constexpr int kRaw = kRows * kWT, kRawStages = 3;
     constexpr int kScales = 4 * 256;                              // a wave's 64 bytes as dwords
@@ -291,7 +310,7 @@ __global__ __launch_bounds__(256, 1) void expert_wgrad_wide_kernel(WgradK a) {
     uint8_t *const xlds = lds + 4 * kRegion;
     uint8_t *const raw = xlds + kX;
     int e, n0, k0;
-    if (!tile_of(a, kWT, &e, &n0, &k0)) return;
+    if (!tile_of(a, kWT, block, &e, &n0, &k0)) return;
     int row0 = 0;
     const int rows = wave_uniform(segment_rows(a.seg, e, &row0));
     row0 = wave_uniform(row0);
@@ -478,9 +497,77 @@ __global__ __launch_bounds__(256, 1) void expert_wgrad_wide_kernel(WgradK a) {
     }
 }
 
-}  // namespace
+template <bool FP8, bool BIAS>
+__global__ __launch_bounds__(256, 1) void expert_wgrad_wide_kernel(WgradK a) {
+    wgrad_wide_tile<FP8, BIAS>(a, blockIdx.x);
+}
 
-hipError_t launch_expert_wgrad(const WgradArgs &a, hipStream_t stream) {
+__global__ __launch_bounds__(256, 1) void wgrad_wide_pair_kernel(WgradPair p) {
+    const bool second = (int)blockIdx.x >= p.first;
+    const WgradK a = second ? p.b : p.a;
+    wgrad_wide_tile<false, false>(a, second ? blockIdx.x - p.first : blockIdx.x);
+}
+
+// The gradients from the parts that runs of rows left in fp32, added in order: 8
+// elements a thread, of the first product, then of the second.
+struct WgradSums {
+    const float *sums[2];        // [parts, count]
+    const void *dw_in[2];
+    void *dw[2];
+    int64_t count[2];            // elements of a gradient, a multiple of 8
+    int parts, bf16_out;
+};
+
+__global__ __launch_bounds__(256) void wgrad_finish_kernel(WgradSums a) {
+    int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+    const bool second = at >= a.count[0];
+    if (second) at -= a.count[0];
+    const int64_t count = second ? a.count[1] : a.count[0];
+    if (at >= count) return;
+    const float *p = (second ? a.sums[1] : a.sums[0]) + at;
+    const void *in = second ? a.dw_in[1] : a.dw_in[0];
+    void *out = second ? a.dw[1] : a.dw[0];
+    ep_f32x4 lo = {0, 0, 0, 0}, hi = {0, 0, 0, 0};
+#pragma unroll 4
+    for (int s = 0; s < a.parts; ++s) {
+        lo += *(const ep_f32x4 *)(p + s * count);
+        hi += *(const ep_f32x4 *)(p + s * count + 4);
+    }
+    if (a.bf16_out) {
+        if (in) {
+            const ep_u32x4 v = *(const ep_u32x4 *)((const uint16_t *)in + at);
+            lo += ep_f32x4{bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y)};
+            hi += ep_f32x4{bf16_lo(v.z), bf16_hi(v.z), bf16_lo(v.w), bf16_hi(v.w)};
+        }
+        *(ep_u32x4 *)((uint16_t *)out + at) =
+            ep_u32x4{pack_bf16(lo[0], lo[1]), pack_bf16(lo[2], lo[3]), pack_bf16(hi[0], hi[1]), pack_bf16(hi[2], hi[3])};
+    } else {
+        if (in) {
+            lo += *(const ep_f32x4 *)((const float *)in + at);
+            hi += *(const ep_f32x4 *)((const float *)in + at + 4);
+        }
+        *(ep_f32x4 *)((float *)out + at) = lo;
+        *(ep_f32x4 *)((float *)out + at + 4) = hi;
+    }
+}
+
+// How the two gradients of dense rows are divided.  Tiles of 256 x 256 from 192 of
+// them on (16384 rows, 4096 x 7168 and 7168 x 2048: PLACE).  Else tiles
+// of 128 x 128, and while those are few, runs of rows whose sums pass through memory:
+// as many as make 512 workgroups, at most 8 of at least 256 rows.
+struct PairPlan { bool wide; int parts; int64_t each; };
+
+PairPlan pair_plan(int64_t rows, int n0, int k0, int n1, int k1) {
+    auto tiles = [](int n, int k, int t) { return (int64_t)((n + t - 1) / t) * ((k + t - 1) / t); };
+    if (rows > 384 && tiles(n0, k0, kWT) + tiles(n1, k1, kWT) >= 192) return {true, 1, rows};
+    int64_t parts = std::min<int64_t>(512 / (tiles(n0, k0, kT) + tiles(n1, k1, kT)), std::min<int64_t>(8, rows / 256));
+    if (rows < 1024) parts = 1;
+    parts = std::max<int64_t>(parts, 1);
+    const int64_t each = parts == 1 ? rows : ((rows + parts - 1) / parts + kRows - 1) / kRows * kRows;
+    return {false, (int)(each > 0 ? (rows + each - 1) / each : 1), each};
+}
+
+WgradK kernel_args(const WgradArgs &a, int T) {
     WgradK k = {};
     k.seg = a.seg;
     k.dy = (const uint8_t *)a.dy;
@@ -493,6 +580,19 @@ hipError_t launch_expert_wgrad(const WgradArgs &a, hipStream_t stream) {
     k.n = a.n;
     k.k = a.k;
     k.bf16_out = a.bf16_out ? 1 : 0;
+    k.tiles_n = (a.n + T - 1) / T;
+    k.tiles_k = (a.k + T - 1) / T;
+    return k;
+}
+
+// Workgroups of a product's tiles: whole rounds of 8 runs of 32.
+int64_t grid_of(const WgradK &k) {
+    return ((int64_t)k.seg.E * k.tiles_n * k.tiles_k + 255) / 256 * 256;
+}
+
+}  // namespace
+
+hipError_t launch_expert_wgrad(const WgradArgs &a, hipStream_t stream) {
     // 256 x 256 tiles where they keep every compute unit busy and an expert's rows
     // pay for filling and draining them: 16 experts of 2048 x 2048, bf16, 1024 rows
     // each 165 us against 210 of the 128 x 128 tiles, 512 rows 113 against 125, 256
@@ -501,10 +601,8 @@ hipError_t launch_expert_wgrad(const WgradArgs &a, hipStream_t stream) {
     const int64_t wide_tiles = (int64_t)a.seg.E * ((a.n + kWT - 1) / kWT) * ((a.k + kWT - 1) / kWT);
     const bool wide = wide_tiles >= 256 && a.seg.pairs / a.seg.E > 384;
     const int T = wide ? kWT : kT;
-    k.tiles_n = (a.n + T - 1) / T;
-    k.tiles_k = (a.k + T - 1) / T;
-    const int64_t tiles = (int64_t)a.seg.E * k.tiles_n * k.tiles_k;
-    const int64_t grid = (tiles + 255) / 256 * 256;   // whole rounds of 8 runs of 32
+    const WgradK k = kernel_args(a, T);
+    const int64_t grid = grid_of(k);
     if (grid > 0x7fffffff) return hipErrorInvalidConfiguration;
     const dim3 g((unsigned)grid), t(256);
     if (wide) {
@@ -522,6 +620,50 @@ hipError_t launch_expert_wgrad(const WgradArgs &a, hipStream_t stream) {
         if (a.db) expert_wgrad_kernel<false, true><<<g, t, 0, stream>>>(k);
         else expert_wgrad_kernel<false, false><<<g, t, 0, stream>>>(k);
     }
+    return hipGetLastError();
+}
+
+size_t wgrad_pair_sums_bytes(int64_t rows, int n0, int k0, int n1, int k1) {
+    const PairPlan p = pair_plan(rows, n0, k0, n1, k1);
+    return p.parts > 1 ? (size_t)p.parts * ((size_t)n0 * k0 + (size_t)n1 * k1) * 4 : 0;
+}
+
+hipError_t launch_wgrad_pair(const WgradArgs &a, const WgradArgs &b, float *sums, hipStream_t stream) {
+    const int64_t rows = a.seg.num_rows;
+    const PairPlan plan = pair_plan(rows, a.n, a.k, b.n, b.k);
+    const int T = plan.wide ? kWT : kT;
+    WgradPair p = {};
+    p.a = kernel_args(a, T);
+    p.b = kernel_args(b, T);
+    WgradSums f = {};
+    if (plan.parts > 1) {
+        f.count[0] = (int64_t)a.n * a.k;
+        f.count[1] = (int64_t)b.n * b.k;
+        f.parts = plan.parts;
+        f.bf16_out = a.bf16_out ? 1 : 0;
+        f.sums[0] = sums;
+        f.sums[1] = sums + plan.parts * f.count[0];
+        WgradK *k[2] = {&p.a, &p.b};
+        for (int i = 0; i < 2; ++i) {
+            f.dw_in[i] = k[i]->dw_in;
+            f.dw[i] = k[i]->dw;
+            k[i]->seg.E = plan.parts;
+            k[i]->seg.each = plan.each;
+            k[i]->dw_in = nullptr;
+            k[i]->dw = (void *)f.sums[i];
+            k[i]->bf16_out = 0;
+        }
+    }
+    const int64_t first = grid_of(p.a), grid = first + grid_of(p.b);
+    if (grid > 0x7fffffff) return hipErrorInvalidConfiguration;
+    p.first = (int)first;
+    const dim3 g((unsigned)grid), t(256);
+    if (plan.wide) wgrad_wide_pair_kernel<<<g, t, 0, stream>>>(p);
+    else wgrad_pair_kernel<<<g, t, 0, stream>>>(p);
+    const hipError_t rc = hipGetLastError();
+    if (rc != hipSuccess || plan.parts == 1) return rc;
+    const int64_t threads = (f.count[0] + f.count[1]) / 8;
+    wgrad_finish_kernel<<<dim3((unsigned)((threads + 255) / 256)), t, 0, stream>>>(f);
     return hipGetLastError();
 }
 

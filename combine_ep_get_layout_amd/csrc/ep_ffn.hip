@@ -83,7 +83,8 @@ hipError_t forward_product(const LinearK &k, int act, int64_t rows, float *sums,
 
 size_t gated_ffn_sums_bytes(int64_t rows, int hidden, int inter, bool backward) {
     const auto of = [&](int n, int k) { return sums_bytes(plan_of(rows, n, k, backward), rows, n); };
-    return backward ? std::max(of(inter, hidden), of(hidden, 2 * inter))
+    return backward ? std::max({of(inter, hidden), of(hidden, 2 * inter),
+                                wgrad_pair_sums_bytes(rows, 2 * inter, hidden, hidden, inter)})
                     : std::max(of(2 * inter, hidden), of(hidden, inter));
 }
 
@@ -135,11 +136,10 @@ hipError_t launch_gated_ffn_backward(const FfnBackwardArgs &a, hipStream_t strea
         g.n = n;
         g.k = k;
         g.bf16_out = a.bf16_out;
-        return launch_expert_wgrad(g, stream);
+        return g;
     };
-    hipError_t rc = wgrad(a.dout, a.hidden, a.h, a.inter, a.dw2_in, a.dw2);
-    if (rc != hipSuccess) return rc;
-    rc = wgrad(a.dz, 2 * a.inter, a.x, a.hidden, a.dw1_in, a.dw1);
+    const hipError_t rc = launch_wgrad_pair(wgrad(a.dz, 2 * a.inter, a.x, a.hidden, a.dw1_in, a.dw1),
+                                            wgrad(a.dout, a.hidden, a.h, a.inter, a.dw2_in, a.dw2), a.sums, stream);
     if (rc != hipSuccess || !a.dx || a.rows == 0) return rc;
     LinearK d = {};
     d.x = (const uint8_t *)a.dz;
