@@ -1058,11 +1058,16 @@ def ep_moe_decode(x: torch.Tensor, topk_idx: torch.Tensor, topk_weights: Optiona
     return out
 
 
-def _codes_and_scales(v, name):
-    """(e4m3 codes, fp32 scales) of 8-bit rows or weights; the scales' shape is
-    checked by the caller."""
-    if not isinstance(v, (tuple, list)) or len(v) != 2:
-        raise ValueError(f"{name} must be (fp8 codes, float32 scales)")
+# The calls below are short against their checks, so each first asks all of them at
+# once (_is), and goes through the ones that name the fault only when that fails.
+def _is(t: Optional[torch.Tensor], dtype, shape, device: int) -> bool:
+    """Whether a buffer (None: not given) is as its kernel takes it."""
+    return t is None or (t.dtype is dtype and t.shape == shape and t.get_device() == device
+                         and t.is_contiguous())
+
+
+def _check_codes(v, name):
+    """The shapes of 8-bit rows or weights are checked by the caller."""
     codes, scales = v
     _need_cuda(codes, name)
     _need_cuda(scales, f"{name} scales")
@@ -1072,7 +1077,12 @@ def _codes_and_scales(v, name):
         raise ValueError(f"{name} needs a multiple of {_FP8_ROW_GROUP} channels")
     if scales.dtype != torch.float32:
         raise ValueError(f"{name}'s scales must be float32 (scale_fmt 'fp32' or 'pow2')")
-    return codes, scales
+
+
+def _pair(v, name):
+    if not isinstance(v, (tuple, list)) or len(v) != 2:
+        raise ValueError(f"{name} must be (fp8 codes, float32 scales)")
+    return v
 
 
 def _scale_blocks(n: int) -> int:
@@ -1137,37 +1147,48 @@ def ep_block_linear(x: Tuple[torch.Tensor, torch.Tensor], w: Tuple[torch.Tensor,
     the transposed pair of ep_cast_fp8_blocks."""
     lib = load_library()
     act, gated = _activation(activation)
-    x, x_scales = _codes_and_scales(x, "x")
-    w, w_scales = _codes_and_scales(w, "w")
+    x, x_scales = _pair(x, "x")
+    w, w_scales = _pair(w, "w")
     lead = () if layout is None else (layout.num_experts,)
+    dev, on = x.device, x.get_device()
     if x.dim() != 2 or w.dim() != 2 + len(lead):
+        _check_codes((x, x_scales), "x")
+        _check_codes((w, w_scales), "w")
         raise ValueError("x must be [rows, K] and w [E, N, K], or [N, K] without a layout")
     rows, K = x.shape
     N = w.shape[-2]
-    _check3(w, "w", _F8, (*lead, N, K))
-    _check3(x_scales, "x scales", _F32, (rows, K // _FP8_ROW_GROUP))
-    _check3(w_scales, "w scales", _F32, (*lead, _scale_blocks(N), K // _FP8_ROW_GROUP))
     M = N // 2 if gated else N
-    dev = x.device
-    if bias is not None:
-        _check3(bias, "bias", _BF16, (*lead, N))
-    if residual is not None:
+    G, B = K // _FP8_ROW_GROUP, _scale_blocks(N)
+    if not (on >= 0 and x.is_contiguous() and x.dtype in _F8 and K % _FP8_ROW_GROUP == 0
+            and w.dtype in _F8 and _is(w, w.dtype, (*lead, N, K), on)
+            and _is(x_scales, torch.float32, (rows, G), on)
+            and _is(w_scales, torch.float32, (*lead, B, G), on)
+            and _is(bias, torch.bfloat16, (*lead, N), on)
+            and _is(residual, torch.bfloat16, (rows, M), on)
+            and _is(out, torch.bfloat16, (rows, M), on)):
+        _check_codes((x, x_scales), "x")
+        _check_codes((w, w_scales), "w")
+        _check3(w, "w", _F8, (*lead, N, K))
+        _check3(x_scales, "x scales", _F32, (rows, G))
+        _check3(w_scales, "w scales", _F32, (*lead, B, G))
+        if bias is not None:
+            _check3(bias, "bias", _BF16, (*lead, N))
         _check(residual, "residual", _BF16, M, min_rows=rows)
+        _check(out, "out", _BF16, M, min_rows=rows)
     if out is None:
         out = torch.empty((rows, M), dtype=torch.bfloat16, device=dev)
-    _check(out, "out", _BF16, M, min_rows=rows)
     params = ptrs = ws = None
     nbytes = 0
     if layout is None:
-        nbytes = int(lib.ep_block_linear_workspace_bytes(rows, N, K))
+        nbytes = lib.ep_block_linear_workspace_bytes(rows, N, K)
         if nbytes:
             ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     else:
         params, ptrs = ctypes.byref(layout.params), ctypes.byref(layout.ptrs())
     _launch("ep_block_linear", dev, lib.ep_block_linear,
-            [x_scales, w, w_scales, bias, residual, out, None if layout is None else layout.status],
-            _ptr(x), _ptr(x_scales), _ptr(w), _ptr(w_scales), N, K, _ptr(bias), act,
-            _ptr(residual), params, ptrs, rows, _ptr(ws), nbytes, _ptr(out), _stream(dev))
+            (x_scales, w, w_scales, bias, residual, out, None if layout is None else layout.status),
+            x.data_ptr(), x_scales.data_ptr(), w.data_ptr(), w_scales.data_ptr(), N, K, _ptr(bias),
+            act, _ptr(residual), params, ptrs, rows, _ptr(ws), nbytes, out.data_ptr(), _stream(dev))
     return out
 
 
@@ -1175,15 +1196,19 @@ def _ffn_sizes(x: torch.Tensor, w1: torch.Tensor, w2: torch.Tensor, activation: 
     act, gated = _activation(activation)
     if not gated:
         raise ValueError('the block\'s activation must be "swiglu" or "geglu"')
-    _need_cuda(x, "x")
     if x.dim() != 2 or w2.dim() != 2:
+        _need_cuda(x, "x")
         raise ValueError("x must be [T, H], w1 [2 I, H] and w2 [H, I]")
     T, H = x.shape
     inter = w2.shape[1]
-    _check(x, "x", _BF16, H)
-    _check3(w1, "w1", _BF16, (2 * inter, H))
-    _check3(w2, "w2", _BF16, (H, inter))
-    return act, T, H, inter
+    on = x.get_device()
+    if not (on >= 0 and _is(x, torch.bfloat16, (T, H), on)
+            and _is(w1, torch.bfloat16, (2 * inter, H), on)
+            and _is(w2, torch.bfloat16, (H, inter), on)):
+        _check(x, "x", _BF16, H)
+        _check3(w1, "w1", _BF16, (2 * inter, H))
+        _check3(w2, "w2", _BF16, (H, inter))
+    return act, T, H, inter, on
 
 
 def ep_gated_ffn(x: torch.Tensor, w1: torch.Tensor, w2: torch.Tensor, activation: str = "swiglu",
@@ -1198,21 +1223,23 @@ def ep_gated_ffn(x: torch.Tensor, w1: torch.Tensor, w2: torch.Tensor, activation
     bf16 [T, 2 I]) also keeps z for ep_gated_ffn_backward.  Returns (out bf16
     [T, H], z or None)."""
     lib = load_library()
-    act, T, H, inter = _ffn_sizes(x, w1, w2, activation)
+    act, T, H, inter, on = _ffn_sizes(x, w1, w2, activation)
     dev = x.device
     z = save if isinstance(save, torch.Tensor) else None
+    if not (_is(z, torch.bfloat16, (T, 2 * inter), on) and _is(residual, torch.bfloat16, (T, H), on)
+            and _is(out, torch.bfloat16, (T, H), on)):
+        _check(z, "z", _BF16, 2 * inter, rows=T)
+        _check(residual, "residual", _BF16, H, rows=T)
+        _check(out, "out", _BF16, H, rows=T)
     if z is None and save:
         z = torch.empty((T, 2 * inter), dtype=torch.bfloat16, device=dev)
     if out is None:
         out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
-    _check(z, "z", _BF16, 2 * inter, rows=T)
-    _check(residual, "residual", _BF16, H, rows=T)
-    _check(out, "out", _BF16, H, rows=T)
-    nbytes = int(lib.ep_gated_ffn_workspace_bytes(T, H, inter, 0))
+    nbytes = lib.ep_gated_ffn_workspace_bytes(T, H, inter, 0)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    _launch("ep_gated_ffn", dev, lib.ep_gated_ffn, [w1, w2, residual, z, out],
-            _ptr(x), T, H, inter, _ptr(w1), _ptr(w2), act, _ptr(residual), _ptr(z), _ptr(ws),
-            nbytes, _ptr(out), _stream(dev))
+    _launch("ep_gated_ffn", dev, lib.ep_gated_ffn, (w1, w2, residual, z, out),
+            x.data_ptr(), T, H, inter, w1.data_ptr(), w2.data_ptr(), act, _ptr(residual), _ptr(z),
+            ws.data_ptr(), nbytes, out.data_ptr(), _stream(dev))
     return out, z
 
 
@@ -1232,28 +1259,36 @@ def ep_gated_ffn_backward(dout: torch.Tensor, x: torch.Tensor, z: torch.Tensor, 
     lib = load_library()
     if dtype not in (torch.float32, torch.bfloat16):
         raise ValueError("dtype must be float32 or bfloat16")
-    act, T, H, inter = _ffn_sizes(x, w1, w2, activation)
-    _check(dout, "dout", _BF16, H, rows=T)
-    _check(z, "z", _BF16, 2 * inter, rows=T)
+    act, T, H, inter, on = _ffn_sizes(x, w1, w2, activation)
     dev = x.device
     dx, dw1, dw2 = (list(out) + [None] * 3)[:3] if out is not None else (None, None, None)
     in1, in2 = (list(accumulate) + [None, None])[:2] if accumulate is not None else (None, None)
+    shape1, shape2 = (2 * inter, H), (H, inter)
+    if not (dout is not None and _is(dout, torch.bfloat16, (T, H), on)
+            and z is not None and _is(z, torch.bfloat16, (T, 2 * inter), on)
+            and _is(dx, torch.bfloat16, (T, H), on)
+            and _is(dw1, dtype, shape1, on) and _is(in1, dtype, shape1, on)
+            and _is(dw2, dtype, shape2, on) and _is(in2, dtype, shape2, on)):
+        if dout is None or z is None:
+            raise ValueError("dout and z must be given")
+        _check(dout, "dout", _BF16, H, rows=T)
+        _check(z, "z", _BF16, 2 * inter, rows=T)
+        _check(dx, "dx", _BF16, H, rows=T)
+        for name, t, shape in (("dw1", dw1, shape1), ("accumulate dw1", in1, shape1),
+                               ("dw2", dw2, shape2), ("accumulate dw2", in2, shape2)):
+            if t is not None:
+                _check3(t, name, (dtype,), shape)
     if dx is None:
         dx = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
     if dw1 is None:
-        dw1 = torch.empty((2 * inter, H), dtype=dtype, device=dev)
+        dw1 = torch.empty(shape1, dtype=dtype, device=dev)
     if dw2 is None:
-        dw2 = torch.empty((H, inter), dtype=dtype, device=dev)
-    _check(dx, "dx", _BF16, H, rows=T)
-    for name, t, shape in (("dw1", dw1, (2 * inter, H)), ("accumulate dw1", in1, (2 * inter, H)),
-                           ("dw2", dw2, (H, inter)), ("accumulate dw2", in2, (H, inter))):
-        if t is not None:
-            _check3(t, name, (dtype,), shape)
-    nbytes = int(lib.ep_gated_ffn_workspace_bytes(T, H, inter, 1))
+        dw2 = torch.empty(shape2, dtype=dtype, device=dev)
+    nbytes = lib.ep_gated_ffn_workspace_bytes(T, H, inter, 1)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     _launch("ep_gated_ffn_backward", dev, lib.ep_gated_ffn_backward,
-            [dout, z, w1, w2, in1, in2, dx, dw1, dw2],
-            _ptr(dout), _ptr(x), _ptr(z), T, H, inter, _ptr(w1), _ptr(w2), act, _ptr(in1),
-            _ptr(in2), _ptr(ws), nbytes, _ptr(dx), _ptr(dw1), _ptr(dw2),
-            1 if dtype == torch.bfloat16 else 0, _stream(dev))
+            (dout, z, w1, w2, in1, in2, dx, dw1, dw2),
+            dout.data_ptr(), x.data_ptr(), z.data_ptr(), T, H, inter, w1.data_ptr(), w2.data_ptr(),
+            act, _ptr(in1), _ptr(in2), ws.data_ptr(), nbytes, dx.data_ptr(), dw1.data_ptr(),
+            dw2.data_ptr(), 1 if dtype == torch.bfloat16 else 0, _stream(dev))
     return dx, dw1, dw2

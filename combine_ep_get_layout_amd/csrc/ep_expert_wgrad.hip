@@ -33,13 +33,8 @@ struct WgradK {
     int bf16_out;
 };
 
-// The tile (of edge T, the tile grid tiles_n x tiles_k per expert) of a
-// workgroup.  Runs of 32 tiles (8 x 4 of them where the grid has them) go to one
-// XCD, the runs to the XCDs in turn: the operands of a run meet in one L2, and
-// an expert with more rows than others spreads over all XCDs.
-__device__ __forceinline__ bool tile_of(const WgradK &a, int T, int block, int *e, int *n0, int *k0) {
-    const int j = block >> 3;
-    const uint32_t t = ((uint32_t)(j >> 5) * 8 + (block & 7)) * 32 + (j & 31);
+// Tile t (of edge T, the tile grid tiles_n x tiles_k per expert).
+__device__ __forceinline__ bool tile_of(const WgradK &a, int T, uint32_t t, int *e, int *n0, int *k0) {
     const uint32_t per_e = (uint32_t)a.tiles_n * (uint32_t)a.tiles_k;
     *e = (int)(t / per_e);
     if (*e >= a.seg.E) return false;
@@ -50,6 +45,14 @@ __device__ __forceinline__ bool tile_of(const WgradK &a, int T, int block, int *
     *n0 = (g * 8 + rem % gm) * T;
     *k0 = (rem / gm) * T;
     return true;
+}
+
+// The tile of a workgroup.  Runs of 32 tiles (8 x 4 of them where the grid has them)
+// go to one XCD, the runs to the XCDs in turn: the operands of a run meet in one L2,
+// and an expert with more rows than others spreads over all XCDs.
+__device__ __forceinline__ uint32_t tile_in_runs() {
+    const int j = blockIdx.x >> 3;
+    return ((uint32_t)(j >> 5) * 8 + (blockIdx.x & 7)) * 32 + (j & 31);
 }
 
 typedef __amdgpu_buffer_rsrc_t Buffer;
@@ -136,10 +139,10 @@ constexpr int kOperand = kRows * kT * 2;
 constexpr int kStage = 2 * kOperand;
 
 template <bool FP8, bool BIAS>
-__device__ __forceinline__ void wgrad_tile(const WgradK &a, int block) {
+__device__ __forceinline__ void wgrad_tile(const WgradK &a, uint32_t tile) {
     __shared__ __align__(1024) uint8_t lds[2 * kStage];
     int e, n0, k0;
-    if (!tile_of(a, kT, block, &e, &n0, &k0)) return;
+    if (!tile_of(a, kT, tile, &e, &n0, &k0)) return;
     int row0 = 0;
     const int rows = wave_uniform(segment_rows(a.seg, e, &row0));
     row0 = wave_uniform(row0);
@@ -268,19 +271,37 @@ __device__ __forceinline__ void wgrad_tile(const WgradK &a, int block) {
 
 template <bool FP8, bool BIAS>
 __global__ __launch_bounds__(256, 2) void expert_wgrad_kernel(WgradK a) {
-    wgrad_tile<FP8, BIAS>(a, blockIdx.x);
+    wgrad_tile<FP8, BIAS>(a, tile_in_runs());
 }
 
-// Two products in one launch, the second's tiles from workgroup `first` on.
+// Two products in one launch: the tiles of both in one sequence, in runs of 32 as
+// above, or, few of them, cut into 8 equal runs (192 tiles in runs of 32 took two
+// rounds on six XCDs, 771 us where one round takes 430).
 struct WgradPair {
     WgradK a, b;
-    int first;
+    uint32_t first, tiles;       // tiles of the first product, of both
 };
 
+// This workgroup's product and its tile there; false without one.
+__device__ __forceinline__ bool pick(const WgradPair &p, WgradK *a, uint32_t *tile) {
+    uint32_t t;
+    if (p.tiles > 256) {
+        t = tile_in_runs();
+    } else {
+        const uint32_t run = (p.tiles + 7) >> 3, at = blockIdx.x >> 3;
+        t = at < run ? (blockIdx.x & 7) * run + at : p.tiles;
+    }
+    if (t >= p.tiles) return false;
+    const bool second = t >= p.first;
+    *a = second ? p.b : p.a;
+    *tile = second ? t - p.first : t;
+    return true;
+}
+
 __global__ __launch_bounds__(256, 2) void wgrad_pair_kernel(WgradPair p) {
-    const bool second = (int)blockIdx.x >= p.first;
-    const WgradK a = second ? p.b : p.a;
-    wgrad_tile<false, false>(a, second ? blockIdx.x - p.first : blockIdx.x);
+    WgradK a;
+    uint32_t tile;
+    if (pick(p, &a, &tile)) wgrad_tile<false, false>(a, tile);
 }
 
 // Tiles of 256 x 256, for many rows an expert: bound by the matrix instructions.
@@ -302,7 +323,7 @@ constexpr int kWT = 256;
 constexpr int kRegion = kRows * 128 * 2;
 
 template <bool FP8, bool BIAS>
-__device__ __forceinline__ void wgrad_wide_tile(const WgradK &a, int block) {
+__device__ __forceinline__ void wgrad_wide_tile(const WgradK &a, uint32_t tile) {
     constexpr int kX = FP8 ? 2 * kRegion : 4 * kRegion;          // x regions of all stages
     constexpr int kRaw = kRows * kWT, kRawStages = 3;
     constexpr int kScales = 4 * 256;                              // a wave's 64 bytes as dwords
@@ -310,7 +331,7 @@ __device__ __forceinline__ void wgrad_wide_tile(const WgradK &a, int block) {
     uint8_t *const xlds = lds + 4 * kRegion;
     uint8_t *const raw = xlds + kX;
     int e, n0, k0;
-    if (!tile_of(a, kWT, block, &e, &n0, &k0)) return;
+    if (!tile_of(a, kWT, tile, &e, &n0, &k0)) return;
     int row0 = 0;
     const int rows = wave_uniform(segment_rows(a.seg, e, &row0));
     row0 = wave_uniform(row0);
@@ -499,13 +520,13 @@ __device__ __forceinline__ void wgrad_wide_tile(const WgradK &a, int block) {
 
 template <bool FP8, bool BIAS>
 __global__ __launch_bounds__(256, 1) void expert_wgrad_wide_kernel(WgradK a) {
-    wgrad_wide_tile<FP8, BIAS>(a, blockIdx.x);
+    wgrad_wide_tile<FP8, BIAS>(a, tile_in_runs());
 }
 
 __global__ __launch_bounds__(256, 1) void wgrad_wide_pair_kernel(WgradPair p) {
-    const bool second = (int)blockIdx.x >= p.first;
-    const WgradK a = second ? p.b : p.a;
-    wgrad_wide_tile<false, false>(a, second ? blockIdx.x - p.first : blockIdx.x);
+    WgradK a;
+    uint32_t tile;
+    if (pick(p, &a, &tile)) wgrad_wide_tile<false, false>(a, tile);
 }
 
 // The gradients from the parts that runs of rows left in fp32, added in order: 8
@@ -551,20 +572,36 @@ __global__ __launch_bounds__(256) void wgrad_finish_kernel(WgradSums a) {
     }
 }
 
-// How the two gradients of dense rows are divided.  Tiles of 256 x 256 from 192 of
-// them on (16384 rows, 4096 x 7168 and 7168 x 2048: PLACE).  Else tiles
-// of 128 x 128, and while those are few, runs of rows whose sums pass through memory:
-// as many as make 512 workgroups, at most 8 of at least 256 rows.
-struct PairPlan { bool wide; int parts; int64_t each; };
+// How the two gradients of dense rows are divided: tiles of 256 or of 128 rows and
+// columns, and, where tiles are few, runs of rows whose sums pass through memory.  By
+// what they are expected to take, from measured times: a round of 256 tiles of 256 x
+// 256 takes 1.55 us a step of 64 rows and 13 us for its ends, a round of 512 of 128 x
+// 128 (two on a compute unit) 1.6 us and 4.5 us, 256 or fewer of them 1.0 us; the sums
+// 5 us for their launch and 4 bytes an element and run, written and read, at 4 TB/s.
+struct PairPlan { int edge, parts; int64_t each; };
 
 PairPlan pair_plan(int64_t rows, int n0, int k0, int n1, int k1) {
-    auto tiles = [](int n, int k, int t) { return (int64_t)((n + t - 1) / t) * ((k + t - 1) / t); };
-    if (rows > 384 && tiles(n0, k0, kWT) + tiles(n1, k1, kWT) >= 192) return {true, 1, rows};
-    int64_t parts = std::min<int64_t>(512 / (tiles(n0, k0, kT) + tiles(n1, k1, kT)), std::min<int64_t>(8, rows / 256));
-    if (rows < 1024) parts = 1;
-    parts = std::max<int64_t>(parts, 1);
-    const int64_t each = parts == 1 ? rows : ((rows + parts - 1) / parts + kRows - 1) / kRows * kRows;
-    return {false, (int)(each > 0 ? (rows + each - 1) / each : 1), each};
+    const double elements = (double)n0 * k0 + (double)n1 * k1;
+    PairPlan best = {kT, 1, rows};
+    double least = 1e300;
+    for (const int T : {kT, kWT}) {
+        auto tiles = [&](int n, int k) { return (int64_t)((n + T - 1) / T) * ((k + T - 1) / T); };
+        const int64_t all = tiles(n0, k0) + tiles(n1, k1);
+        for (const int parts : {1, 2, 3, 4, 6, 8}) {
+            const int64_t each = parts == 1 ? rows : ((rows + parts - 1) / parts + kRows - 1) / kRows * kRows;
+            if (parts > 1 && (each < 256 || (rows + each - 1) / each != parts || parts * elements > 64e6)) continue;
+            const int64_t total = all * parts, round = T == kWT ? 256 : 512;
+            const double steps = (double)((each + kRows - 1) / kRows);
+            const double step = T == kWT ? 1.55 : total <= 256 ? 1.0 : 1.6;
+            double us = (double)((total + round - 1) / round) * (steps * step + (T == kWT ? 13.0 : 4.5));
+            if (parts > 1) us += 5.0 + parts * elements * 8.0 / 4e6;
+            if (us < least) {
+                least = us;
+                best = {T, parts, each};
+            }
+        }
+    }
+    return best;
 }
 
 WgradK kernel_args(const WgradArgs &a, int T) {
@@ -631,7 +668,7 @@ size_t wgrad_pair_sums_bytes(int64_t rows, int n0, int k0, int n1, int k1) {
 hipError_t launch_wgrad_pair(const WgradArgs &a, const WgradArgs &b, float *sums, hipStream_t stream) {
     const int64_t rows = a.seg.num_rows;
     const PairPlan plan = pair_plan(rows, a.n, a.k, b.n, b.k);
-    const int T = plan.wide ? kWT : kT;
+    const int T = plan.edge;
     WgradPair p = {};
     p.a = kernel_args(a, T);
     p.b = kernel_args(b, T);
@@ -654,11 +691,13 @@ hipError_t launch_wgrad_pair(const WgradArgs &a, const WgradArgs &b, float *sums
             k[i]->bf16_out = 0;
         }
     }
-    const int64_t first = grid_of(p.a), grid = first + grid_of(p.b);
+    const auto tiles = [](const WgradK &k) { return (int64_t)k.seg.E * k.tiles_n * k.tiles_k; };
+    const int64_t first = tiles(p.a), all = first + tiles(p.b), grid = (all + 255) / 256 * 256;
     if (grid > 0x7fffffff) return hipErrorInvalidConfiguration;
-    p.first = (int)first;
+    p.first = (uint32_t)first;
+    p.tiles = (uint32_t)all;
     const dim3 g((unsigned)grid), t(256);
-    if (plan.wide) wgrad_wide_pair_kernel<<<g, t, 0, stream>>>(p);
+    if (T == kWT) wgrad_wide_pair_kernel<<<g, t, 0, stream>>>(p);
     else wgrad_pair_kernel<<<g, t, 0, stream>>>(p);
     const hipError_t rc = hipGetLastError();
     if (rc != hipSuccess || plan.parts == 1) return rc;

@@ -171,6 +171,23 @@ struct Output {
             if (c0 + lc * 8 < a.m && r + lr < live_rows) res[i] = *(const ep_u32x4 *)(p + (int64_t)r * a.m);
         }
     }
+    // kBackward: gates (in res) and ups of PG iterations from i0 on
+    static constexpr int PG = IT < 8 ? IT : 8;
+    ep_u32x4 up[PG];
+    __device__ __forceinline__ void load_pre(const LinearK &a, const TileAt &at, int first,
+                                             int live_rows, int c0, int batch, int i0) {
+        const int lane = threadIdx.x & 63, lc = lane % LANES, lr = lane / LANES;
+        const uint16_t *p = a.pre + ((int64_t)at.row0 + first + lr) * 2 * a.m + c0 + lc * 8;
+#pragma unroll
+        for (int i = 0; i < PG; ++i) {
+            const int r = row_of(batch, i0 + i);
+            res[i] = up[i] = ep_u32x4{0, 0, 0, 0};
+            if (c0 + lc * 8 < a.m && r + lr < live_rows) {
+                res[i] = *(const ep_u32x4 *)(p + (int64_t)r * 2 * a.m);
+                up[i] = *(const ep_u32x4 *)(p + (int64_t)r * 2 * a.m + a.m);
+            }
+        }
+    }
 };
 
 // kBackward of 8 columns of a row: dgate = dh up f'(gate), dup = dh f(gate), h.
@@ -219,20 +236,9 @@ __device__ __forceinline__ void epilogue_of(const LinearK &a, const TileAt &at, 
             b[k][2 * j + 1] = bf16_hi(v[j]);
         }
     }
-    // kBackward: the gates and ups of two iterations of a batch, one ahead
-    ep_u32x4 gate[2], up[2];
-    auto load_pre = [&](int batch, int i) __attribute__((always_inline)) {
-        const int at_row = O::row_of(batch, i);
-        gate[i & 1] = up[i & 1] = ep_u32x4{0, 0, 0, 0};
-        if (there && at_row + lr < live_rows) {
-            const uint16_t *p = a.pre + (row0 + at_row) * 2 * m + col;
-            gate[i & 1] = *(const ep_u32x4 *)p;
-            up[i & 1] = *(const ep_u32x4 *)(p + m);
-        }
-    };
     each<MT / BT>([&](auto bb) __attribute__((always_inline)) {
         constexpr int batch = decltype(bb)::value;
-        if constexpr (MODE == kBackward) load_pre(batch, 0);
+        if constexpr (MODE == kBackward && batch > 0) now.load_pre(a, at, first, live_rows, c0, batch, 0);
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -242,7 +248,7 @@ __device__ __forceinline__ void epilogue_of(const LinearK &a, const TileAt &at, 
                 *(ep_f32x4 *)(lds + (i * 16 + l16) * COLS * 4 + ((t * 4 + q) ^ l16) * 16) = s;
             }
         O next;
-        if (batch + 1 < MT / BT) next.load(a, at, first, live_rows, c0, batch + 1);
+        if (MODE != kBackward && batch + 1 < MT / BT) next.load(a, at, first, live_rows, c0, batch + 1);
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
             const int at_row = O::row_of(batch, i);
@@ -251,7 +257,7 @@ __device__ __forceinline__ void epilogue_of(const LinearK &a, const TileAt &at, 
             const int64_t row = row0 + at_row;
             float z[NK][8];
             if constexpr (MODE == kBackward) {
-                if (i + 1 < IT) load_pre(batch, i + 1);
+                if (i > 0 && i % O::PG == 0) now.load_pre(a, at, first, live_rows, c0, batch, i);
             }
 #pragma unroll
             for (int k = 0; k < NK; ++k) {
@@ -290,7 +296,7 @@ __device__ __forceinline__ void epilogue_of(const LinearK &a, const TileAt &at, 
                 }
             }
             if constexpr (MODE == kBackward) {
-                if (live) write_backward(a, row, col, z[0], gate[i & 1], up[i & 1], KIND);
+                if (live) write_backward(a, row, col, z[0], now.res[i % O::PG], now.up[i % O::PG], KIND);
                 continue;
             }
             float y[8];
@@ -311,7 +317,7 @@ __device__ __forceinline__ void epilogue_of(const LinearK &a, const TileAt &at, 
                     ep_u32x4{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]),
                              pack_bf16(y[6], y[7])};
         }
-        if (batch + 1 < MT / BT) now = next;
+        if (MODE != kBackward && batch + 1 < MT / BT) now = next;
     });
 }
 
@@ -497,6 +503,11 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void expert_linear_kernel(LinearK 
         }
     };
 
+    constexpr int BT = MT > 4 ? MT / 2 : MT;           // row tiles of an epilogue batch
+    Output<4, BT, WM * 16, GATED> o;
+    constexpr bool kPreEarly = MT <= 2;                // z is on its way since before the product
+    if constexpr (MODE == kBackward && kPreEarly)
+        o.load_pre(a, at, row0 + wm * 16, rows - wm * 16, column(wn * 64), 0, 0);
     for (int s = 0; s < NS - 1; ++s)
         if (begin + s < steps) copy(begin + s, s);
     int stage = 0;
@@ -532,10 +543,12 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void expert_linear_kernel(LinearK 
         return;
     }
     barrier_only();                                    // the stages are the epilogue's now
-    constexpr int BT = MT > 4 ? MT / 2 : MT;           // row tiles of an epilogue batch
     static_assert(kWaves * BT * 4096 <= NS * kStage && MT % BT == 0, "a batch must fit the stages");
-    Output<4, BT, WM * 16, GATED> o;
-    o.load(a, at, row0 + wm * 16, rows - wm * 16, column(wn * 64), 0);
+    if constexpr (MODE == kBackward) {
+        if (!kPreEarly) o.load_pre(a, at, row0 + wm * 16, rows - wm * 16, column(wn * 64), 0, 0);
+    } else {
+        o.load(a, at, row0 + wm * 16, rows - wm * 16, column(wn * 64), 0);
+    }
     epilogue<4, MT, BT, WM * 16, GATED, MODE>(a, at, lds + wave * BT * 4096, row0 + wm * 16,
                                         rows - wm * 16, column(wn * 64), acc, o);
 }
@@ -725,7 +738,7 @@ __global__ __launch_bounds__(256, 1) void expert_linear_wide_kernel(LinearK a) {
     };
 
     Output<8, 4, 16, GATED> o;
-    if (!EXACT) o.load(a, at, row0 + wm * 128, rows - wm * 128, column(wn, 0), 0);
+    if (!EXACT && MODE != kBackward) o.load(a, at, row0 + wm * 128, rows - wm * 128, column(wn, 0), 0);
     for (int s = 0; s < 2; ++s) {
         each<4>([&](auto j) { copy_x(s, s, 0, j); });
         each<4>([&](auto j) { copy_w(s, s, 0, j); });
@@ -797,6 +810,7 @@ __global__ __launch_bounds__(256, 1) void expert_linear_wide_kernel(LinearK a) {
     barrier_only();                                    // the stages are the epilogue's now
     // exact: the registers for it hold the converted pieces until here
     if (EXACT) o.load(a, at, row0 + wm * 128, rows - wm * 128, column(wn, 0), 0);
+    if constexpr (MODE == kBackward) o.load_pre(a, at, row0 + wm * 128, rows - wm * 128, column(wn, 0), 0, 0);
     static_assert(kWaves * 32768 <= 2 * kStage, "a batch must fit the stages");
     epilogue<8, 8, 4, 16, GATED, MODE>(a, at, lds + wave * 32768, row0 + wm * 128, rows - wm * 128,
                              column(wn, 0), acc, o);
@@ -890,27 +904,27 @@ hipError_t launch_finish(const LinearK &k, int parts, hipStream_t stream) {
 //               128 tiles 73; 4096 to 7168 on transposed weights 83 and 130; but 7168 to
 //               4096 (96 tiles) 124 and 118
 //   64 x 64     weights as they lie: whole for short contractions while all tiles run at
-//               once (512 to 512, 64 rows 6.5 us, in parts 7.4; 2048 to 7168 15.4 and
-//               14.7); in parts up to 112 tiles of 64 x 128 (7168 to 4096, gated, 64 rows
+//               once (512 to 512, 64 rows 6.5 us, in parts 7.4); in parts up to 112 tiles of 64 x 128 (7168 to 4096, gated, 64 rows
 //               20.8 us, in 64 x 128 tiles 22.5, 128 rows 22.7 and 24.4, whole 43)
 //   128 x 128   from 150 tiles on (700 rows, 7168 to 4096, 2 parts: 62 us, in 64 x 128
 //               tiles 69), else
 //   64 x 128    (333 rows, 7168 to 2048 on transposed weights, 96 tiles in 4 parts: 26.7
 //               us, in 128 x 128 tiles 28.4, whole in 256 x 256 tiles 126)
 // Parts: as many as make 400 workgroups of the tiles (two run on a compute unit), at
-// most 8 (more only move more sums) of at least 4 steps.
+// most 8 (more only move more sums), where that saves 16 steps of 0.3 to 0.6 us: the
+// second launch takes about 5 us.
 struct DensePlan { int rows, cols, parts, split; };
 
 inline DensePlan dense_plan(int64_t rows, int n, int steps, bool transposed) {
     auto tiles = [&](int r, int c) { return (rows + r - 1) / r * ((n + c - 1) / c); };
     if (tiles(256, 256) >= 112) return {256, 256, 1, steps};
-    if (!transposed && steps < 32 && tiles(64, 64) <= 512) return {64, 64, 1, steps};
     const int r = tiles(128, 128) >= 150 ? 128 : 64;
     const int c = !transposed && tiles(64, 128) <= 112 ? 64 : 128;
-    int64_t parts = std::min<int64_t>(400 / std::max<int64_t>(1, tiles(r, c)), std::min(8, steps / 4));
+    int64_t parts = std::min<int64_t>(400 / std::max<int64_t>(1, tiles(r, c)), 8);
     parts = std::max<int64_t>(parts, 1);
     const int split = (int)((steps + parts - 1) / parts);
-    return {r, c, (steps + split - 1) / split, split};
+    if (steps - split >= 16) return {r, c, (steps + split - 1) / split, split};
+    return {r, !transposed && tiles(64, 64) <= 512 ? 64 : 128, 1, steps};
 }
 
 // Bytes of the sums.
