@@ -911,8 +911,8 @@ hipError_t launch_finish(const LinearK &k, int parts, hipStream_t stream) {
 //   64 x 128    (333 rows, 7168 to 2048 on transposed weights, 96 tiles in 4 parts: 26.7
 //               us, in 128 x 128 tiles 28.4, whole in 256 x 256 tiles 126)
 // Parts: as many as make 400 workgroups of the tiles (two run on a compute unit), at
-// most 8 (more only move more sums), where that saves 16 steps of 0.3 to 0.6 us: the
-// second launch takes about 5 us.
+// most 8 (more only move more sums) of at least 4 steps, where that saves 14 steps of
+// 0.3 to 0.6 us: the second launch takes 3 to 5 us, and 2.5 us of the host.
 struct DensePlan { int rows, cols, parts, split; };
 
 inline DensePlan dense_plan(int64_t rows, int n, int steps, bool transposed) {
@@ -920,10 +920,10 @@ inline DensePlan dense_plan(int64_t rows, int n, int steps, bool transposed) {
     if (tiles(256, 256) >= 112) return {256, 256, 1, steps};
     const int r = tiles(128, 128) >= 150 ? 128 : 64;
     const int c = !transposed && tiles(64, 128) <= 112 ? 64 : 128;
-    int64_t parts = std::min<int64_t>(400 / std::max<int64_t>(1, tiles(r, c)), 8);
+    int64_t parts = std::min<int64_t>(400 / std::max<int64_t>(1, tiles(r, c)), std::min(8, steps / 4));
     parts = std::max<int64_t>(parts, 1);
     const int split = (int)((steps + parts - 1) / parts);
-    if (steps - split >= 16) return {r, c, (steps + split - 1) / split, split};
+    if (steps - split >= 14) return {r, c, (steps + split - 1) / split, split};
     return {r, !transposed && tiles(64, 64) <= 512 ? 64 : 128, 1, steps};
 }
 
