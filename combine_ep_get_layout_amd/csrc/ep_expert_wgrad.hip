@@ -57,54 +57,70 @@ __device__ __forceinline__ uint32_t tile_in_runs() {
 
 typedef __amdgpu_buffer_rsrc_t Buffer;
 
+// Rows 1 and 3 (16 lanes each) of the first two dwords change places with rows 0 and
+// 2 of the last two.
+__device__ __forceinline__ ep_u32x4 swap_rows(ep_u32x4 o) {
+    const auto x = __builtin_amdgcn_permlane16_swap(o.x, o.z, false, false);
+    const auto y = __builtin_amdgcn_permlane16_swap(o.y, o.w, false, false);
+    return ep_u32x4{(uint32_t)x[0], (uint32_t)y[0], (uint32_t)x[1], (uint32_t)y[1]};
+}
+
 // A wave's NT x KT accumulator tiles: tile (t, i) holds dW rows n0 + 16 i +
 // lane % 16, channels k0 + 16 t + 4 q .. + 3.  Row tile by row tile, what is
 // added to the next one loaded while this one is stored; buffer accesses, so
-// rows and channels that are not there need no branch.
+// rows and channels that are not there need no branch.  bf16: two tiles' lanes
+// change halves first, so that a lane has 8 consecutive channels of tile t + (q & 1)
+// and a row's 64 bytes leave together (one row 7168/2048, both gradients of 88 MB:
+// 37 us by 8 bytes a lane, 26 so).
 template <bool BF16, int KT, int NT>
 __device__ __forceinline__ void write_tiles_as(const WgradK &a, int e, int n0, int k0,
                                                ep_f32x4 (*acc)[NT]) {
-    typedef int i32x2 __attribute__((ext_vector_type(2)));
-    constexpr int ES = BF16 ? 2 : 4;
+    constexpr int ES = BF16 ? 2 : 4, TW = BF16 ? 2 : 1;          // tiles of an access
     const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
     const int rows = max(0, min(NT * 16, a.n - n0));
     const int64_t from = ((int64_t)e * a.n + n0) * a.k * ES;
     const int bytes = wave_uniform(rows * a.k * ES);
     const Buffer out = __builtin_amdgcn_make_buffer_rsrc((uint8_t *)a.dw + from, 0, bytes, 0x00020000);
     const Buffer in = __builtin_amdgcn_make_buffer_rsrc((uint8_t *)a.dw_in + from, 0, a.dw_in ? bytes : 0, 0x00020000);
-    const uint32_t at = ((uint32_t)l16 * a.k + k0 + 4 * q) * ES;
+    const int c0 = k0 + (BF16 ? (q & 1) * 16 + (q >> 1) * 8 : 4 * q);
+    const uint32_t at = ((uint32_t)l16 * a.k + c0) * ES;
     const uint32_t step = 16 * (uint32_t)a.k * ES;
     // (everything in the lane's offset: the range check subtracts a scalar one
     // from the size, which rows that are not there would make negative)
-    auto off = [&](int i, int t) { return k0 + t * 16 + 4 * q < a.k ? at + i * step + t * 16 * ES : kOutOfRange; };
-    ep_f32x4 add[2][KT];
+    auto off = [&](int i, int t) { return c0 + t * 16 < a.k ? at + i * step + t * 16 * ES : kOutOfRange; };
+    ep_u32x4 add[2][KT / TW];
     auto load = [&](int i) {
 #pragma unroll
-        for (int t = 0; t < KT; ++t) {
-            ep_f32x4 &v = add[i & 1][t];
-            if (BF16) {
-                const ep_u32x2 o = __builtin_bit_cast(ep_u32x2, __builtin_amdgcn_raw_buffer_load_b64(in, off(i, t), 0, 0));
-                v = ep_f32x4{bf16_lo(o.x), bf16_hi(o.x), bf16_lo(o.y), bf16_hi(o.y)};
-            } else {
-                v = __builtin_bit_cast(ep_f32x4, __builtin_amdgcn_raw_buffer_load_b128(in, off(i, t), 0, 0));
-            }
-        }
+        for (int t = 0; t < KT; t += TW)
+            add[i & 1][t / TW] = __builtin_bit_cast(ep_u32x4, __builtin_amdgcn_raw_buffer_load_b128(in, off(i, t), 0, 0));
     };
     if (a.dw_in) load(0);
     each<NT>([&](auto ii) __attribute__((always_inline)) {
         constexpr int i = decltype(ii)::value;
         if (a.dw_in && i + 1 < NT) load(i + 1);
 #pragma unroll
-        for (int t = 0; t < KT; ++t) {
-            ep_f32x4 v = acc[t][i];
-            pin(v);
-            if (a.dw_in) v += add[i & 1][t];
-            if (BF16) {
-                const ep_u32x2 o = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
-                __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(i32x2, o), out, off(i, t), 0, 0);
-            } else {
-                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(ep_i32x4, v), out, off(i, t), 0, 0);
+        for (int t = 0; t < KT; t += TW) {
+            ep_u32x4 o = add[i & 1][t / TW];
+            ep_f32x4 v[TW];
+#pragma unroll
+            for (int h = 0; h < TW; ++h) {
+                v[h] = acc[t + h][i];
+                pin(v[h]);
             }
+            if (BF16) {
+                if (a.dw_in) {
+                    o = swap_rows(o);
+                    v[0] += ep_f32x4{bf16_lo(o.x), bf16_hi(o.x), bf16_lo(o.y), bf16_hi(o.y)};
+                    v[TW - 1] += ep_f32x4{bf16_lo(o.z), bf16_hi(o.z), bf16_lo(o.w), bf16_hi(o.w)};
+                }
+                o = swap_rows(ep_u32x4{pack_bf16(v[0][0], v[0][1]), pack_bf16(v[0][2], v[0][3]),
+                                       pack_bf16(v[TW - 1][0], v[TW - 1][1]),
+                                       pack_bf16(v[TW - 1][2], v[TW - 1][3])});
+            } else {
+                if (a.dw_in) v[0] += __builtin_bit_cast(ep_f32x4, o);
+                o = __builtin_bit_cast(ep_u32x4, v[0]);
+            }
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(ep_i32x4, o), out, off(i, t), 0, 0);
         }
         __builtin_amdgcn_sched_barrier(0);
     });
