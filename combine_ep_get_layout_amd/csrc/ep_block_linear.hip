@@ -248,7 +248,7 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void block_linear_kernel(BlockK p)
     }
     dma_wait<0>();
     if constexpr (MODE == kSums) {
-        store_sums<GATED, 4, MT>(a, row0 + wm * 16, WM * 16, rows - wm * 16, acc,
+        store_sums<GATED, 4, MT>(a, blockIdx.y, row0 + wm * 16, WM * 16, rows - wm * 16, acc,
                                  [&](int t) { return column(wn * 64 + t * 16); });
         return;
     }

@@ -62,11 +62,6 @@ struct WgradArgs {
 
 hipError_t launch_expert_wgrad(const WgradArgs &a, hipStream_t stream);
 
-// Two gradients of the same dense rows (bf16, of one output type, without biases);
-// `sums` holds wgrad_pair_sums_bytes.
-size_t wgrad_pair_sums_bytes(int64_t rows, int n0, int k0, int n1, int k1);
-hipError_t launch_wgrad_pair(const WgradArgs &a, const WgradArgs &b, float *sums, hipStream_t stream);
-
 struct ActBackwardArgs {
     const int32_t *src_of_slot;  // [entries] >= 0 where a row holds a pair
     const int32_t *total_rows;   // rows in use

@@ -51,17 +51,17 @@ struct LinearK {
 
 // What the epilogue writes: act(z) + residual; z in bf16 with it; or, z being the
 // gradient dh of h = f(gate) * up, d[gate | up] (out, 2 m wide) and h itself.  kSums:
-// the fp32 sums of part blockIdx.y of the contraction, for finish_kernel.
+// the fp32 sums of a part of the contraction, for finish_kernel.
 enum { kPlain, kKeep, kBackward, kSums };
 
 // A wave's sums, tile (t, i) at columns column(t) + 4 q and row first + i * stride
 // + lane % 16 of dense rows.  (A gated tile's gate columns behind the half are up
 // columns, which another tile stores.)
 template <bool GATED, int NT, int MT, typename F>
-__device__ __forceinline__ void store_sums(const LinearK &a, int first, int stride, int live_rows,
+__device__ __forceinline__ void store_sums(const LinearK &a, int part, int first, int stride, int live_rows,
                                            ep_f32x4 (*acc)[MT], F column) {
     const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
-    float *const out = a.sums + (int64_t)blockIdx.y * a.seg.num_rows * a.n;
+    float *const out = a.sums + (int64_t)part * a.seg.num_rows * a.n;
     each<MT>([&](auto ii) __attribute__((always_inline)) {
         constexpr int i = decltype(ii)::value;
         const int r = i * stride + l16;
@@ -336,8 +336,13 @@ __device__ __forceinline__ void epilogue(const LinearK &a, const TileAt &at, uin
 // of a step.
 // The ring of NS stages keeps NS - 1 steps in flight; row tiles that hold no row
 // are not multiplied.
-template <int BM, int WM, int WN, int NS, int IN, bool WT, bool GATED, int MODE = kPlain>
-__global__ __launch_bounds__(64 * WN * WM, 2) void expert_linear_kernel(LinearK a) {
+template <int BM, int WM, int WN, int NS>
+constexpr int kLinearLds = NS * (64 * WN + BM) * 128;
+
+// Tile `block` of the product, part `part` of the contraction (kSums).  `lds`:
+// kLinearLds bytes on a kilobyte; `red`: 16 ints of LDS.
+template <int BM, int WM, int WN, int NS, int IN, bool WT, bool GATED, int MODE>
+__device__ __forceinline__ void linear_tile(const LinearK &a, int block, int part, uint8_t *lds, int *red) {
     constexpr bool FP8 = IN != kBf16, EXACT = IN == kFp8Exact;
     constexpr int kWaves = WN * WM;
     constexpr int BN = 64 * WN;
@@ -349,11 +354,8 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void expert_linear_kernel(LinearK 
     constexpr int XL = kXStage / 1024 / kWaves;
     constexpr int ES = FP8 ? 1 : 2;
     constexpr int BK = 128 / ES;
-    __shared__ __align__(1024) uint8_t lds[NS * kStage];
-    __shared__ int red[16];
-
     TileAt at;
-    if (!find_tile<64 * kWaves>(a.seg, BM, a.col_tiles, blockIdx.x, red, &at)) return;
+    if (!find_tile<64 * kWaves>(a.seg, BM, a.col_tiles, block, red, &at)) return;
 
     const int lane = threadIdx.x & 63, wave = wave_uniform(threadIdx.x >> 6);
     const int l16 = lane & 15, q = lane >> 4;
@@ -399,7 +401,7 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void expert_linear_kernel(LinearK 
         }
     }
     const uint32_t lds0 = lds_offset(lds);
-    const int begin = MODE == kSums ? blockIdx.y * a.split : 0;
+    const int begin = MODE == kSums ? part * a.split : 0;
     const int steps = MODE == kSums ? min((K + BK - 1) / BK, begin + a.split) : (K + BK - 1) / BK;
     // copies of x that hold a row, of this wave's: the others are left out, and
     // the rows behind the segment are what the LDS holds (they go nowhere)
@@ -538,7 +540,7 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void expert_linear_kernel(LinearK 
     }
     dma_wait<0>();
     if constexpr (MODE == kSums) {
-        store_sums<GATED, 4, MT>(a, row0 + wm * 16, WM * 16, rows - wm * 16, acc,
+        store_sums<GATED, 4, MT>(a, part, row0 + wm * 16, WM * 16, rows - wm * 16, acc,
                           [&](int t) { return column(wn * 64 + t * 16); });
         return;
     }
@@ -551,6 +553,13 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void expert_linear_kernel(LinearK 
     }
     epilogue<4, MT, BT, WM * 16, GATED, MODE>(a, at, lds + wave * BT * 4096, row0 + wm * 16,
                                         rows - wm * 16, column(wn * 64), acc, o);
+}
+
+template <int BM, int WM, int WN, int NS, int IN, bool WT, bool GATED, int MODE = kPlain>
+__global__ __launch_bounds__(64 * WN * WM, 2) void expert_linear_kernel(LinearK a) {
+    __shared__ __align__(1024) uint8_t lds[kLinearLds<BM, WM, WN, NS>];
+    __shared__ int red[16];
+    linear_tile<BM, WM, WN, NS, IN, WT, GATED, MODE>(a, blockIdx.x, blockIdx.y, lds, red);
 }
 
 // Tiles of 256 rows, bound by the matrix instructions.  Four waves of 128 x 128:
@@ -580,18 +589,18 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void expert_linear_kernel(LinearK 
 // the epilogue and the first copies the rest), fp8 7168 to 4096 0.82 ms (2.3).  A
 // library product of 32768 x 4096 x 7168 without an
 // epilogue reaches 1.56 (bf16) and 3.2 (fp8) on the same card.
-template <int IN, bool WT, bool GATED, int MODE = kPlain>
-__global__ __launch_bounds__(256, 1) void expert_linear_wide_kernel(LinearK a) {
+constexpr int kLinearWideLds = 2 * 4 * 128 * 128;
+
+// Tile `block` of the product; `lds`: kLinearWideLds bytes on a kilobyte; `red`: 16 ints.
+template <int IN, bool WT, bool GATED, int MODE>
+__device__ __forceinline__ void linear_wide_tile(const LinearK &a, int block, uint8_t *lds, int *red) {
     constexpr bool FP8 = IN != kBf16, EXACT = IN == kFp8Exact;
     constexpr int BM = 256, kWaves = 4;
     constexpr int kRegion = 128 * 128, kStage = 4 * kRegion;     // W0, W1, X0, X1
     constexpr int ES = FP8 ? 1 : 2;
     constexpr int BK = 128 / ES;
-    __shared__ __align__(1024) uint8_t lds[2 * kStage];
-    __shared__ int red[16];
-
     TileAt at;
-    if (!find_tile<64 * kWaves>(a.seg, BM, a.col_tiles, blockIdx.x, red, &at)) return;
+    if (!find_tile<64 * kWaves>(a.seg, BM, a.col_tiles, block, red, &at)) return;
 
     const int lane = threadIdx.x & 63, wave = wave_uniform(threadIdx.x >> 6);
     const int l16 = lane & 15, q = lane >> 4;
@@ -814,6 +823,13 @@ __global__ __launch_bounds__(256, 1) void expert_linear_wide_kernel(LinearK a) {
     static_assert(kWaves * 32768 <= 2 * kStage, "a batch must fit the stages");
     epilogue<8, 8, 4, 16, GATED, MODE>(a, at, lds + wave * 32768, row0 + wm * 128, rows - wm * 128,
                              column(wn, 0), acc, o);
+}
+
+template <int IN, bool WT, bool GATED, int MODE = kPlain>
+__global__ __launch_bounds__(256, 1) void expert_linear_wide_kernel(LinearK a) {
+    __shared__ __align__(1024) uint8_t lds[kLinearWideLds];
+    __shared__ int red[16];
+    linear_wide_tile<IN, WT, GATED, MODE>(a, blockIdx.x, lds, red);
 }
 
 // Workgroups for row tiles of BM rows: each segment's last one may be partial.
