@@ -2,12 +2,16 @@
 // its gradients: dense rows through the matrix kernels of the experts.
 //
 // Forward: h = f(x Wg^T) * (x Wu^T) by one product whose tiles hold gate and up
-// columns together, then out = h W2^T + residual.  Up to 64 rows go through the
-// kernel for few rows, bound by reading the weights.
+// columns together, then out = h W2^T + residual.  Few rows go through a kernel of
+// their own, bound by reading the weights.
 // Backward: the product dout W2 makes dh in its accumulators; its epilogue reads z
 // and writes dz = [dgate | dup] and h, so that dh is never stored or rounded.  Then
 // dW2 = dout^T h, dW1 = dz^T x and dx = dz W1.  dz and h are rounded to bf16, the
 // type that the matrix instructions of these products take.
+//
+// 16384 tokens 7168/2048, back to back on one card: forward 1.02 to 1.06 ms (1.36 to
+// 1.41 PFLOP/s; a library product reaches 1.54), backward 2.26 to 2.34 (1.23 to 1.28), bound by
+// the matrix instructions under the power limit.
 #include "ep_linear_device.h"
 #include "ep_wgrad_device.h"
 

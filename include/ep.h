@@ -587,7 +587,8 @@ int ep_moe_decode(const void *x, const int64_t *topk_idx, const float *topk_weig
  *   codes_t   device uint8 [num, k, n], 8-byte aligned, and
  *   scales_t  device float [num, ceil(k/128), ceil(n/128)]; both or neither.
  * Per block (the last ones of a matrix may be partial) s = max(amax, 1e-4f) /
- * 448, code = e4m3_rne(w / s), as ep_cast_fp8 forms them; NaN is left out of amax.
+ * 448, code = e4m3_rne(w / s), as ep_cast_fp8 forms them.  NaN is left out of amax
+ * and keeps to itself; a block that holds an infinity has a NaN scale and NaN codes.
  * codes_t holds the same codes and scales transposed.  EP_ERR_INVALID_ARG (num < 0,
  * sizes, pointers; neither pair); EP_ERR_UNSUPPORTED (n or k above EP_MAX_HIDDEN,
  * 2^31 blocks or more). */

@@ -66,6 +66,22 @@ def test_cast_into_buffers_on_a_stream(gpu):
         gpu.ep_cast_fp8_blocks(w[:, :, :196].contiguous())
 
 
+def test_cast_of_infinities_and_nan(gpu):
+    """NaN keeps to itself; a block that holds an infinity has a NaN scale and NaN codes."""
+    announce("cast blocks, non-finite")
+    w = torch.randn((256, 256), device=DEV).bfloat16()
+    want, _ = gpu.ep_cast_fp8_blocks(w)
+    w[3, 5] = float("nan")
+    w[200, 130] = float("-inf")
+    (c, s), (ct, st) = gpu.ep_cast_fp8_blocks(w, transposed=True)
+    top = w[:128, :128].double().nan_to_num(0.0).abs().max()
+    assert s[0, 0].item() == (top / 448).float().item()
+    assert torch.equal(s[0, 1], want[1][0, 1]) and torch.equal(s[1, 0], want[1][1, 0]) and s[1, 1].isnan()
+    nan = c.float().isnan()
+    assert nan[3, 5] and nan[128:, 128:].all() and int(nan.sum()) == 1 + 128 * 128
+    assert torch.equal(ct.view(torch.uint8), c.view(torch.uint8).T) and torch.equal(st.view(torch.int32), s.view(torch.int32).T)
+
+
 def rows(g, n, k):
     x = torch.randn((n, k), generator=g, device=DEV)
     x = x * torch.exp2(torch.randint(-3, 4, (n, k // 128), generator=g, device=DEV).float()).repeat_interleave(128, dim=1)
@@ -127,6 +143,16 @@ def test_dense_rows(gpu, T, n, k, act):
     case(gpu, T, 0, 1, k, n, act, seed=T)
 
 
+@pytest.mark.parametrize("T,k,n,act", [(100, 7168, 512, "swiglu"), (300, 4096, 1032, "none"), (130, 7168, 4096, "swiglu"),
+                                       (1000, 2688, 1024, "silu"), (700, 4224, 4096, "geglu"), (65, 5248, 8, "none"),
+                                       (512, 7168, 2048, "swiglu"), (512, 7168, 2056, "gelu"), (1024, 4096, 2560, "none"),
+                                       (640, 256, 3392, "geglu"), (640, 256, 3400, "none")])
+def test_dense_rows_in_parts(gpu, T, k, n, act):
+    """Contractions cut into parts, some within a group of four blocks; and whole ones in
+    the tiles between."""
+    case(gpu, T, 0, 1, k, n, act, bias=True, residual=True, seed=T)
+
+
 @pytest.mark.parametrize("n,act", [(8, "none"), (24, "none"), (64, "swiglu"), (136, "silu"), (192, "geglu"),
                                    (320, "swiglu"), (1000, "none")])
 @pytest.mark.parametrize("T,E", [(3, 0), (100, 0), (300, 4), (2000, 2)])
@@ -148,6 +174,13 @@ def test_ragged_experts(gpu, A):
     idx = torch.cat([torch.full((c,), e, dtype=torch.int64) for e, c in enumerate(counts)])
     idx = idx[torch.randperm(len(idx), generator=torch.Generator().manual_seed(A))].unsqueeze(1).to(DEV)
     case(gpu, len(idx), len(counts), 1, 640, 4416, "swiglu", A=A, idx=idx, seed=A)
+
+
+@pytest.mark.parametrize("E,T", [(32, 1600), (16, 1200), (8, 900)])
+@pytest.mark.parametrize("act", ["none", "swiglu"])
+def test_rows_per_expert(gpu, E, T, act):
+    """About 100, 150 and 225 rows an expert of many columns: tiles of 128, 192 and 256 rows."""
+    case(gpu, T, E, 2, 896, 4096, act, seed=E, residual=True)
 
 
 def test_fixed_capacity(gpu):

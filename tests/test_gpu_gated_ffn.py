@@ -45,9 +45,12 @@ def test_forward_odd_sizes(gpu, T, H, inter):
     check(gpu, T, H, inter)
 
 
-@pytest.mark.parametrize("H,inter", [(2048, 2048)])
-def test_forward_many_rows(gpu, H, inter):
-    check(gpu, 2100, H, inter)
+# products whole and in parts in tiles of each size
+@pytest.mark.parametrize("T,H,inter", [(100, 4096, 256), (512, 4096, 1024), (512, 2048, 4096), (640, 128, 1696),
+                                       (640, 3392, 64), (1024, 2048, 1280), (1024, 2560, 2048), (2100, 3584, 72),
+                                       (2100, 2048, 2048)])
+def test_forward_tiles(gpu, T, H, inter):
+    check(gpu, T, H, inter)
 
 
 def check_backward(gpu, T, H, inter, act, seed=0):
@@ -87,6 +90,15 @@ def test_backward_odd_sizes(gpu, T, H, inter):
 
 def test_backward_many_rows(gpu):
     check_backward(gpu, 2500, 4096, 1536, "swiglu")
+
+
+# sizes whose products take every pair of tiles: weight gradients in 128 x 128 tiles,
+# in runs of rows, in 256 x 256 tiles; dx whole and in parts of each tile
+@pytest.mark.parametrize("T,H,inter", [(700, 2048, 1024), (1500, 4096, 512), (1100, 512, 2048), (600, 4096, 2048),
+                                       (5000, 256, 512), (3000, 1024, 264), (2000, 136, 1400),
+                                       (1024, 2560, 1024), (4096, 1792, 64), (4096, 128, 1792)])
+def test_backward_tiles(gpu, T, H, inter):
+    check_backward(gpu, T, H, inter, "geglu")
 
 
 @pytest.mark.parametrize("rows", [4000, 9000])
@@ -148,6 +160,29 @@ def test_one_gradient_to_add_to(gpu):
     a = gpu.ep_gated_ffn_backward(dout, x, z, w1, w2)
     b = gpu.ep_gated_ffn_backward(dout, x, z, w1, w2, accumulate=(None, torch.ones_like(a[2])))
     assert torch.equal(a[1], b[1]) and not torch.equal(a[2], b[2])
+
+
+def test_weight_gradients_alone(gpu):
+    """Without dx (the C entry point's NULL)."""
+    announce("gated ffn, no dx")
+    import ctypes
+
+    from combine_ep_get_layout_amd import _abi
+    lib = _abi.load()
+    V = ctypes.c_void_p
+    for T, H, inter in ((20, 64, 32), (900, 256, 512), (2500, 4096, 1536)):
+        x, w1, w2, dout, g = make(T, H, inter, 6)
+        z = torch.randn((T, 2 * inter), generator=g, device=DEV).to(BF16)
+        want = gpu.ep_gated_ffn_backward(dout, x, z, w1, w2)
+        d1, d2 = torch.zeros_like(want[1]), torch.zeros_like(want[2])
+        n = lib.ep_gated_ffn_workspace_bytes(T, H, inter, 1)
+        ws = torch.empty(n, dtype=torch.uint8, device=DEV)
+        p = [V(t.data_ptr()) for t in (dout, x, z, w1, w2, ws, d1, d2)]
+        rc = lib.ep_gated_ffn_backward(p[0], p[1], p[2], T, H, inter, p[3], p[4], _abi.EP_ACT_SWIGLU, None, None,
+                                       p[5], n, None, p[6], p[7], 0, V(torch.cuda.current_stream().cuda_stream))
+        assert rc == 0
+        torch.cuda.synchronize()
+        assert torch.equal(d1, want[1]) and torch.equal(d2, want[2])
 
 
 def test_rows_do_not_mix(gpu):
