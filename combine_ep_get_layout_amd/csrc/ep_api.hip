@@ -749,6 +749,10 @@ int ep_cast_fp8_blocks(const void *w, int32_t num, int32_t n, int32_t k, uint8_t
     return to_status(ep::launch_cast_blocks(a, (hipStream_t)stream));
 }
 
+// The kernels count a segment's rows in 32 bits, up to a tile (256) or a ring's steps
+// (five of 64 rows) behind the last one.
+constexpr int64_t kMaxDenseRows = ((int64_t)1 << 31) - 1024;
+
 // The one segment of dense rows.
 static void dense_rows(int64_t num_rows, ep::SegmentRows *seg) {
     *seg = {};
@@ -757,7 +761,7 @@ static void dense_rows(int64_t num_rows, ep::SegmentRows *seg) {
 }
 
 size_t ep_block_linear_workspace_bytes(int64_t num_rows, int32_t n, int32_t k) {
-    if (num_rows < 0 || num_rows >= ((int64_t)1 << 31) || n < 8 || n > EP_MAX_HIDDEN ||
+    if (num_rows < 0 || num_rows > kMaxDenseRows || n < 8 || n > EP_MAX_HIDDEN ||
         k < ep::kFp8Group || k > EP_MAX_HIDDEN)
         return 0;
     return ep::block_linear_sums_bytes(num_rows, n, k);
@@ -773,7 +777,7 @@ int ep_block_linear(const void *x, const float *x_scales, const void *w, const f
         const int rc = segment_checks(p, layout, num_rows, &a.seg);
         if (rc != EP_OK) return rc;
     } else {
-        if (num_rows < 0 || num_rows >= ((int64_t)1 << 31)) return EP_ERR_INVALID_ARG;
+        if (num_rows < 0 || num_rows > kMaxDenseRows) return EP_ERR_INVALID_ARG;
         dense_rows(num_rows, &a.seg);
     }
     if (!is_act(act) || n < 8 || n % (ep::act_gated(act) ? 64 : 8) != 0) return EP_ERR_INVALID_ARG;
@@ -810,7 +814,7 @@ static size_t ffn_part(int64_t num_tokens, int64_t columns) {
 
 size_t ep_gated_ffn_workspace_bytes(int64_t num_tokens, int32_t hidden, int32_t inter,
                                     int backward) {
-    if (num_tokens < 0 || num_tokens >= ((int64_t)1 << 31) || hidden < 8 ||
+    if (num_tokens < 0 || num_tokens > kMaxDenseRows || hidden < 8 ||
         hidden > EP_MAX_HIDDEN || inter < 8 || inter > EP_MAX_HIDDEN / 2 ||
         (backward != 0 && backward != 1))
         return 0;
@@ -819,7 +823,7 @@ size_t ep_gated_ffn_workspace_bytes(int64_t num_tokens, int32_t hidden, int32_t 
 }
 
 static int ffn_checks(int64_t num_tokens, int32_t hidden, int32_t inter, int act) {
-    if (num_tokens < 0 || num_tokens >= ((int64_t)1 << 31)) return EP_ERR_INVALID_ARG;
+    if (num_tokens < 0 || num_tokens > kMaxDenseRows) return EP_ERR_INVALID_ARG;
     if (hidden < 8 || hidden % 8 != 0 || inter < 8 || inter % 8 != 0) return EP_ERR_INVALID_ARG;
     if (act != EP_ACT_SWIGLU && act != EP_ACT_GEGLU) return EP_ERR_INVALID_ARG;
     if (hidden > EP_MAX_HIDDEN || inter > EP_MAX_HIDDEN / 2 || (int64_t)hidden * inter * 4 >= kMaxBuffer)

@@ -624,7 +624,8 @@ size_t ep_block_linear_workspace_bytes(int64_t num_rows, int32_t n, int32_t k);
  * data gradient is the same call on gradient rows cast to 8 bits and the codes_t of
  * the weights.  Two calls on the same inputs give the same bits; a row's result does
  * not depend on the others' values, but with another number of rows its sums may be
- * formed in another order.  Errors: EP_ERR_INVALID_ARG; EP_ERR_WORKSPACE;
+ * formed in another order.  Errors: EP_ERR_INVALID_ARG (more than 2^31 - 1024 dense
+ * rows among them); EP_ERR_WORKSPACE;
  * EP_ERR_UNSUPPORTED (k or n above EP_MAX_HIDDEN, a matrix of 2^31 - 4096 bytes or
  * more). */
 int ep_block_linear(const void *x, const float *x_scales, const void *w, const float *w_scales,
@@ -656,7 +657,7 @@ size_t ep_gated_ffn_workspace_bytes(int64_t num_tokens, int32_t hidden, int32_t 
  * fp32; z, h and out are rounded to bf16 (h is formed from the sums, not from the
  * rounded z).  Two calls on the same inputs give the same bits; with another number
  * of rows, or with z, sums may be formed in another order.  Errors:
- * EP_ERR_INVALID_ARG (T < 0 or 2^31 and more among them), EP_ERR_WORKSPACE,
+ * EP_ERR_INVALID_ARG (T < 0 or above 2^31 - 1024 among them), EP_ERR_WORKSPACE,
  * EP_ERR_UNSUPPORTED (H or 2 I above EP_MAX_HIDDEN, a matrix of 2^31 - 4096 bytes
  * or more). */
 int ep_gated_ffn(const void *x, int64_t num_tokens, int32_t hidden, int32_t inter, const void *w1,

@@ -115,6 +115,22 @@ def test_workspaces():
     assert g(-1, 64, 128) == g(100, 0, 128) == g(100, 64, 0) == g(1 << 31, 64, 128) == 0
 
 
+# the kernels' 32-bit counts of rows run up to a tile and a ring of steps behind the last
+MOST = (1 << 31) - 1024
+
+
+def test_rows_that_would_pass_the_kernels_counts():
+    for rows in (MOST + 1, (1 << 31) - 1):
+        assert linear(rows=rows, nb=1 << 60) == INV
+        assert ffn(T=rows, nb=1 << 60) == INV
+        assert ffn_backward(T=rows, nb=1 << 60) == INV
+        assert _abi.load().ep_gated_ffn_workspace_bytes(rows, 8, 8, 0) == 0
+        assert _abi.load().ep_block_linear_workspace_bytes(rows, 64, 8192) == 0
+    # taken up to there (refused here for its workspace alone, so nothing is launched)
+    assert ffn(T=MOST, nb=0) == ffn_backward(T=MOST, nb=0) == WS
+    assert _abi.load().ep_gated_ffn_workspace_bytes(MOST, 8, 8, 1) >= 6 * MOST * 8
+
+
 def test_binding_refuses():
     import torch
 
