@@ -291,3 +291,19 @@ def test_binding_checks(gpu):
     with pytest.raises(gpu.EpError):                       # halves of 48
         w96, _ = gpu.ep_cast_fp8_blocks(weights(g, (96, 256)))
         gpu.ep_block_linear(x, w96, activation="swiglu")
+
+
+def test_offsets_past_32_bits(gpu):
+    """4.4 million dense rows of 512 codes: rows around byte 2^31 of x and 2^31 and 2^32 of
+    out, the first and the last ones."""
+    T, k, n = 4_400_000, 512, 512
+    announce("block linear", T, n, k)
+    g = torch.Generator(device=DEV).manual_seed(6)
+    x = torch.empty(T, k, device=DEV, dtype=torch.bfloat16).normal_(generator=g).to(torch.float8_e4m3fn)
+    xs = torch.rand(T, k // 128, generator=g, device=DEV) + 0.5
+    w, _ = gpu.ep_cast_fp8_blocks(torch.randn(n, k, generator=g, device=DEV).to(torch.bfloat16))
+    out = gpu.ep_block_linear((x, xs), w)
+    at = torch.cat([torch.arange(b - 40, b + 40, device=DEV) for b in (40, 1 << 21, 1 << 22, T - 40)])
+    some = (x.view(torch.uint8)[at].view(torch.float8_e4m3fn), xs[at])
+    for rows, y, dy in bref.block_linear(some, w, None, "none", None, [(None, 0, len(at))]):
+        ref.assert_near(out[at][rows], y, dy)

@@ -231,3 +231,30 @@ def test_binding_checks(gpu):
                 lambda: gpu.ep_gated_ffn_backward(r, x, z, w1, w2, out=(r, None, w2))):
         with pytest.raises(ValueError):
             bad()
+
+
+def test_offsets_past_32_bits(gpu):
+    """4.4 million rows of 1024 bytes: rows around byte 2^31 and 2^32 of x, dout, out and
+    dx, the first and the last ones.  The other rows' dout is zero, so that the weight
+    gradients are those of these rows."""
+    T, H, inter = 4_400_000, 512, 64
+    announce("gated ffn", T, H, inter)
+    g = torch.Generator(device=DEV).manual_seed(5)
+    n = lambda *s: torch.empty(s, device=DEV, dtype=BF16).normal_(generator=g)  # noqa: E731
+    x, w1, w2 = n(T, H), (n(2 * inter, H) * H ** -0.5), (n(H, inter) * inter ** -0.5)
+    at = torch.cat([torch.arange(b - 40, b + 40, device=DEV) for b in (40, 1 << 21, 1 << 22, T - 40)])
+    dout = torch.zeros(T, H, device=DEV, dtype=BF16)
+    dout[at] = n(len(at), H)
+    out, z = gpu.ep_gated_ffn(x, w1, w2, save=True)
+    zv, dz, want, err = bref.ffn(x[at], w1, w2, "swiglu", None)
+    ref.assert_near(out[at], want, err, what="out")
+    ref.assert_near(z[at], zv, dz, what="z")
+    del out
+    got = gpu.ep_gated_ffn_backward(dout, x, z, w1, w2)
+    want = bref.ffn_backward(dout[at], x[at], z[at], w1, w2, "swiglu")
+    for name, v, (y, e), h in zip(("dx", "dw1", "dw2"), (got[0][at], *got[1:]), want,
+                                  (ref.BF16_HALF, ref.U, ref.U)):
+        ref.assert_near(v, y, e, h, name)
+    live = torch.zeros(T, device=DEV, dtype=torch.bool)
+    live[at] = True
+    assert not (got[0] != 0).any(dim=1)[~live].any()
