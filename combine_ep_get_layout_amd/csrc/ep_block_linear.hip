@@ -102,9 +102,11 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void block_linear_kernel(BlockK p)
         if ((s & 3) == 0 || (MODE == kSums && s == begin)) {
             const uint32_t base = slds0 + (s >> 2 & 1) * kScales + wave * 256;
             const int s4 = s & ~3;
+            // (all in the lane's offset, see dma4: a group behind the last one may
+            // begin past the whole buffer)
             const uint32_t past = s4 + sk >= groups ? kOutOfRange : 0;
-            for (int i = 0; i < SL; ++i) dma4(xsb, base + i * kWaves * 256, soff[i] | past, s4 * 4);
-            dma4(wsb, base + kXScales, wsoff | past, s4 * 4);
+            for (int i = 0; i < SL; ++i) dma4(xsb, base + i * kWaves * 256, (soff[i] + s4 * 4) | past);
+            dma4(wsb, base + kXScales, (wsoff + s4 * 4) | past);
         }
     };
     // Copies behind the last step go on from empty buffers (they write zeros), so that

@@ -188,15 +188,17 @@ __device__ __forceinline__ void dma16_of4(ep_i32x4 &rsrc, uint32_t lds, uint32_t
     }
 }
 
-// 64 lanes x 4 bytes, in lane order.
-__device__ __forceinline__ void dma4(const ep_i32x4 &rsrc, uint32_t lds, uint32_t voff, uint32_t soff) {
+// 64 lanes x 4 bytes, in lane order.  Without a scalar offset: a buffer's range check
+// subtracts it from the size, and one past a small buffer would wrap, so that even
+// lanes at kOutOfRange were read.
+__device__ __forceinline__ void dma4(const ep_i32x4 &rsrc, uint32_t lds, uint32_t voff) {
     ep_i32x4 r;
     for (int i = 0; i < 4; ++i) r[i] = wave_uniform(rsrc[i]);
     asm volatile(
         "s_nop 4\n\t"
-        "buffer_load_dword %0, %1, %2 offen lds"
+        "buffer_load_dword %0, %1, 0 offen lds"
         :
-        : "v"(voff), "s"(r), "s"(wave_uniform((int)soff)), "{m0}"(wave_uniform((int)lds)));
+        : "v"(voff), "s"(r), "{m0}"(wave_uniform((int)lds)));
 }
 
 // 64 lanes x 1 byte, one dword of LDS each (the byte, zero extended).
