@@ -764,7 +764,7 @@ size_t ep_block_linear_workspace_bytes(int64_t num_rows, int32_t n, int32_t k) {
     if (num_rows < 0 || num_rows > kMaxDenseRows || n < 8 || n > EP_MAX_HIDDEN ||
         k < ep::kFp8Group || k > EP_MAX_HIDDEN)
         return 0;
-    return ep::block_linear_sums_bytes(num_rows, n, k);
+    return ep::block_linear_sums_most(num_rows, n, k);
 }
 
 int ep_block_linear(const void *x, const float *x_scales, const void *w, const float *w_scales,
@@ -812,14 +812,24 @@ static size_t ffn_part(int64_t num_tokens, int64_t columns) {
     return ((size_t)num_tokens * columns * 2 + 255) / 256 * 256;
 }
 
+static size_t ffn_rows(int64_t num_tokens, int32_t inter, int backward) {
+    return ffn_part(num_tokens, inter) + (backward ? ffn_part(num_tokens, 2 * (int64_t)inter) : 0) + 256;
+}
+
+// What a call uses: the query's bytes hold for fewer tokens too, so they may be more.
+static size_t ffn_used(int64_t num_tokens, int32_t hidden, int32_t inter, int backward) {
+    return ffn_rows(num_tokens, inter, backward) +
+           ep::gated_ffn_sums_bytes(num_tokens, hidden, inter, backward == 1);
+}
+
 size_t ep_gated_ffn_workspace_bytes(int64_t num_tokens, int32_t hidden, int32_t inter,
                                     int backward) {
     if (num_tokens < 0 || num_tokens > kMaxDenseRows || hidden < 8 ||
         hidden > EP_MAX_HIDDEN || inter < 8 || inter > EP_MAX_HIDDEN / 2 ||
         (backward != 0 && backward != 1))
         return 0;
-    return ffn_part(num_tokens, inter) + (backward ? ffn_part(num_tokens, 2 * (int64_t)inter) : 0) +
-           ep::gated_ffn_sums_bytes(num_tokens, hidden, inter, backward == 1) + 256;
+    return ffn_rows(num_tokens, inter, backward) +
+           ep::gated_ffn_sums_most(num_tokens, hidden, inter, backward == 1);
 }
 
 static int ffn_checks(int64_t num_tokens, int32_t hidden, int32_t inter, int act) {
@@ -841,7 +851,7 @@ int ep_gated_ffn(const void *x, int64_t num_tokens, int32_t hidden, int32_t inte
         !aligned16(out) || !aligned16(residual) || !aligned16(z))
         return EP_ERR_INVALID_ARG;
     if (!workspace || !aligned16(workspace) ||
-        workspace_bytes < ep_gated_ffn_workspace_bytes(num_tokens, hidden, inter, 0))
+        workspace_bytes < ffn_used(num_tokens, hidden, inter, 0))
         return EP_ERR_WORKSPACE;
     ep::FfnArgs a = {};
     a.x = x;
@@ -874,7 +884,7 @@ int ep_gated_ffn_backward(const void *dout, const void *x, const void *z, int64_
             !aligned16(w1) || !w2 || !aligned16(w2) || !aligned16(dx))
             return EP_ERR_INVALID_ARG;
         if (!workspace || !aligned16(workspace) ||
-            workspace_bytes < ep_gated_ffn_workspace_bytes(num_tokens, hidden, inter, 1))
+            workspace_bytes < ffn_used(num_tokens, hidden, inter, 1))
             return EP_ERR_WORKSPACE;
     }
     ep::FfnBackwardArgs a = {};

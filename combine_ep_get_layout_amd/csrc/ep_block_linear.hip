@@ -300,6 +300,10 @@ size_t block_linear_sums_bytes(int64_t rows, int n, int k) {
     return few_rows(rows, k) ? 0 : sums_bytes(plan_of(rows, n, k), rows, n);
 }
 
+size_t block_linear_sums_most(int64_t rows, int n, int k) {
+    return few_rows(rows, k) ? 0 : sums_most(rows, n, k / kFp8Group);
+}
+
 hipError_t launch_block_linear(const BlockLinearArgs &a, hipStream_t stream) {
     if (!a.seg.offsets && few_rows(a.seg.num_rows, a.k)) {
         FewRowsArgs f = {};

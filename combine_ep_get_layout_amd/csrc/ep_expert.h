@@ -126,8 +126,10 @@ struct BlockLinearArgs {
     int act;                     // EP_ACT_*
 };
 
-// Bytes that a product of dense rows needs for the sums of its parts.
+// Bytes that a product of dense rows needs for the sums of its parts, and the most
+// that any number of rows up to `rows` needs.
 size_t block_linear_sums_bytes(int64_t rows, int n, int k);
+size_t block_linear_sums_most(int64_t rows, int n, int k);
 
 hipError_t launch_block_linear(const BlockLinearArgs &a, hipStream_t stream);
 
@@ -155,8 +157,10 @@ struct FfnArgs {
     int hidden, inter, act;
 };
 
-// Bytes that the products of a pass need for the sums of their parts.
+// Bytes that the products of a pass need for the sums of their parts, and the most
+// that any number of rows up to `rows` needs.
 size_t gated_ffn_sums_bytes(int64_t rows, int hidden, int inter, bool backward);
+size_t gated_ffn_sums_most(int64_t rows, int hidden, int inter, bool backward);
 
 hipError_t launch_gated_ffn(const FfnArgs &a, hipStream_t stream);
 

@@ -140,6 +140,16 @@ __global__ __launch_bounds__(256) void wgrad_finish_kernel(WgradSums a) {
 // 5 us for their launch and 4 bytes an element and run, written and read, at 4 TB/s.
 struct PairPlan { int edge, parts; int64_t each; };
 
+constexpr int kRuns[] = {1, 2, 3, 4, 6, 8};
+
+// Runs of `each` rows, if `rows` rows are cut into `parts` of them (0: they are not):
+// of 256 rows at least, and sums of 256 MB at most.
+int64_t run_of(int64_t rows, int parts, double elements) {
+    if (parts == 1) return rows;
+    const int64_t each = ((rows + parts - 1) / parts + kRows - 1) / kRows * kRows;
+    return each < 256 || parts * elements > 64e6 ? 0 : each;
+}
+
 PairPlan pair_plan(int64_t rows, int n0, int k0, int n1, int k1) {
     const double elements = (double)n0 * k0 + (double)n1 * k1;
     PairPlan best = {kT, 1, rows};
@@ -147,9 +157,9 @@ PairPlan pair_plan(int64_t rows, int n0, int k0, int n1, int k1) {
     for (const int T : {kT, kWT}) {
         auto tiles = [&](int n, int k) { return (int64_t)((n + T - 1) / T) * ((k + T - 1) / T); };
         const int64_t all = tiles(n0, k0) + tiles(n1, k1);
-        for (const int parts : {1, 2, 3, 4, 6, 8}) {
-            const int64_t each = parts == 1 ? rows : ((rows + parts - 1) / parts + kRows - 1) / kRows * kRows;
-            if (parts > 1 && (each < 256 || (rows + each - 1) / each != parts || parts * elements > 64e6)) continue;
+        for (const int parts : kRuns) {
+            const int64_t each = run_of(rows, parts, elements);
+            if (parts > 1 && (each == 0 || (rows + each - 1) / each != parts)) continue;
             const int64_t total = all * parts, round = T == kWT ? 256 : 512;
             const double steps = (double)((each + kRows - 1) / kRows);
             const double step = T == kWT ? 1.55 : total <= 256 ? 1.0 : 1.6;
@@ -228,6 +238,17 @@ size_t gated_ffn_sums_bytes(int64_t rows, int hidden, int inter, bool backward) 
     const PairPlan p = pair_plan(rows, 2 * inter, hidden, hidden, inter);
     const size_t weights = p.parts > 1 ? (size_t)p.parts * 3 * hidden * inter * 4 : 0;
     return std::max(of(inter, hidden), of(hidden, 2 * inter) + weights);
+}
+
+size_t gated_ffn_sums_most(int64_t rows, int hidden, int inter, bool backward) {
+    const auto of = [&](int n, int k) { return sums_most(rows, n, (k + kStep - 1) / kStep); };
+    if (!backward) return std::max(of(2 * inter, hidden), of(hidden, inter));
+    // (a run grows with the rows, so what cuts fewer rows cuts these)
+    const double elements = 3.0 * hidden * inter;
+    int parts = 0;
+    for (const int p : kRuns)
+        if (p > 1 && run_of(rows, p, elements) > 0) parts = p;
+    return std::max(of(inter, hidden), of(hidden, 2 * inter) + (size_t)parts * 3 * hidden * inter * 4);
 }
 
 hipError_t launch_gated_ffn(const FfnArgs &a, hipStream_t stream) {

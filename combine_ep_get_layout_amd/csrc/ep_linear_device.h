@@ -948,6 +948,15 @@ inline size_t sums_bytes(const DensePlan &p, int64_t rows, int n) {
     return p.parts > 1 ? (size_t)p.parts * rows * n * 4 : 0;
 }
 
+// The most that they are for up to `rows` rows, which does not fall as the rows grow:
+// no contraction of `steps` is cut into more parts than this, and the parts' tiles
+// are at most 400, of 128 x 128 sums or fewer.
+inline size_t sums_most(int64_t rows, int n, int steps) {
+    const int parts = std::min(8, steps / 4);
+    if (parts < 2 || steps - (steps + parts - 1) / parts < 14) return 0;
+    return (size_t)std::min<int64_t>(parts * rows * n, 400 * 128 * 128) * 4;
+}
+
 // The rows of a tile and the columns of out that it covers.
 struct RowTile { int rows, cols; };
 

@@ -595,8 +595,10 @@ int ep_moe_decode(const void *x, const int64_t *topk_idx, const float *topk_weig
 int ep_cast_fp8_blocks(const void *w, int32_t num, int32_t n, int32_t k, uint8_t *codes,
                        float *scales, uint8_t *codes_t, float *scales_t, void *stream);
 
-/* Bytes of device workspace a product of dense rows needs (host call; 0: none, or
- * sizes it does not take).  With a layout none is needed. */
+/* Bytes of device workspace that products of up to num_rows dense rows need (host
+ * call; 0: none, or sizes they do not take).  It does not fall as the rows grow, so
+ * one workspace serves a program's largest batch and its smaller ones.  With a
+ * layout none is needed. */
 size_t ep_block_linear_workspace_bytes(int64_t num_rows, int32_t n, int32_t k);
 
 /* ep_block_linear - the matrix product with these scales and its epilogue: with
@@ -637,8 +639,8 @@ int ep_block_linear(const void *x, const float *x_scales, const void *w, const f
  * output, or that of the routed experts, is the other's bias or residual):
  *   z = x W1^T = [gate | up],  h = f(gate) * up,  out = h W2^T + residual. */
 
-/* Bytes of device workspace of the block's two calls (host call), or 0 for sizes
- * they do not take. */
+/* Bytes of device workspace of the block's two calls for up to num_tokens tokens (host
+ * call), or 0 for sizes they do not take.  It does not fall as the tokens grow. */
 size_t ep_gated_ffn_workspace_bytes(int64_t num_tokens, int32_t hidden, int32_t inter,
                                     int backward);
 
