@@ -760,9 +760,17 @@ static void dense_rows(int64_t num_rows, ep::SegmentRows *seg) {
     seg->num_rows = seg->pairs = seg->each = num_rows;
 }
 
+// A product's sizes; a gated activation takes multiples of 64 columns alone.
+static int block_linear_checks(int32_t n, int32_t k, bool gated) {
+    if (n < 8 || n % (gated ? 64 : 8) != 0) return EP_ERR_INVALID_ARG;
+    if (k < ep::kFp8Group || k % ep::kFp8Group != 0) return EP_ERR_INVALID_ARG;
+    if (n > EP_MAX_HIDDEN || k > EP_MAX_HIDDEN || (int64_t)n * k >= kMaxBuffer)
+        return EP_ERR_UNSUPPORTED;
+    return EP_OK;
+}
+
 size_t ep_block_linear_workspace_bytes(int64_t num_rows, int32_t n, int32_t k) {
-    if (num_rows < 0 || num_rows > kMaxDenseRows || n < 8 || n > EP_MAX_HIDDEN ||
-        k < ep::kFp8Group || k > EP_MAX_HIDDEN)
+    if (num_rows < 0 || num_rows > kMaxDenseRows || block_linear_checks(n, k, false) != EP_OK)
         return 0;
     return ep::block_linear_sums_most(num_rows, n, k);
 }
@@ -780,10 +788,9 @@ int ep_block_linear(const void *x, const float *x_scales, const void *w, const f
         if (num_rows < 0 || num_rows > kMaxDenseRows) return EP_ERR_INVALID_ARG;
         dense_rows(num_rows, &a.seg);
     }
-    if (!is_act(act) || n < 8 || n % (ep::act_gated(act) ? 64 : 8) != 0) return EP_ERR_INVALID_ARG;
-    if (k < ep::kFp8Group || k % ep::kFp8Group != 0) return EP_ERR_INVALID_ARG;
-    if (n > EP_MAX_HIDDEN || k > EP_MAX_HIDDEN || (int64_t)n * k >= kMaxBuffer)
-        return EP_ERR_UNSUPPORTED;
+    if (!is_act(act)) return EP_ERR_INVALID_ARG;
+    const int sizes = block_linear_checks(n, k, ep::act_gated(act));
+    if (sizes != EP_OK) return sizes;
     if (a.seg.pairs == 0 || num_rows == 0) return EP_OK;
     if (!x || !aligned16(x) || !w || !aligned16(w) || !out || !aligned16(out))
         return EP_ERR_INVALID_ARG;
@@ -822,16 +829,6 @@ static size_t ffn_used(int64_t num_tokens, int32_t hidden, int32_t inter, int ba
            ep::gated_ffn_sums_bytes(num_tokens, hidden, inter, backward == 1);
 }
 
-size_t ep_gated_ffn_workspace_bytes(int64_t num_tokens, int32_t hidden, int32_t inter,
-                                    int backward) {
-    if (num_tokens < 0 || num_tokens > kMaxDenseRows || hidden < 8 ||
-        hidden > EP_MAX_HIDDEN || inter < 8 || inter > EP_MAX_HIDDEN / 2 ||
-        (backward != 0 && backward != 1))
-        return 0;
-    return ffn_rows(num_tokens, inter, backward) +
-           ep::gated_ffn_sums_most(num_tokens, hidden, inter, backward == 1);
-}
-
 static int ffn_checks(int64_t num_tokens, int32_t hidden, int32_t inter, int act) {
     if (num_tokens < 0 || num_tokens > kMaxDenseRows) return EP_ERR_INVALID_ARG;
     if (hidden < 8 || hidden % 8 != 0 || inter < 8 || inter % 8 != 0) return EP_ERR_INVALID_ARG;
@@ -839,6 +836,14 @@ static int ffn_checks(int64_t num_tokens, int32_t hidden, int32_t inter, int act
     if (hidden > EP_MAX_HIDDEN || inter > EP_MAX_HIDDEN / 2 || (int64_t)hidden * inter * 4 >= kMaxBuffer)
         return EP_ERR_UNSUPPORTED;
     return EP_OK;
+}
+
+size_t ep_gated_ffn_workspace_bytes(int64_t num_tokens, int32_t hidden, int32_t inter,
+                                    int backward) {
+    if (ffn_checks(num_tokens, hidden, inter, EP_ACT_SWIGLU) != EP_OK || (backward != 0 && backward != 1))
+        return 0;
+    return ffn_rows(num_tokens, inter, backward) +
+           ep::gated_ffn_sums_most(num_tokens, hidden, inter, backward == 1);
 }
 
 int ep_gated_ffn(const void *x, int64_t num_tokens, int32_t hidden, int32_t inter, const void *w1,

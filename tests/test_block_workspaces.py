@@ -25,3 +25,16 @@ def test_block_does_not_ask_more_for_fewer_tokens(hidden, inter, backward):
     room = 256 * (1 + backward) + 256 + 26_214_400 + 256_000_000 * backward
     for r, b in zip(ROWS, got):
         assert 0 <= b - 2 * r * inter * (3 if backward else 1) <= room
+
+
+@pytest.mark.parametrize("n,k", [(12, 7168), (4096, 7168 + 64), (4, 7168), (4096, 64), (1 << 20, 1 << 11),
+                                 ((1 << 20) + 8, 1024), (8, (1 << 20) + 128)])
+def test_product_asks_nothing_for_sizes_it_refuses(n, k):
+    assert _abi.load().ep_block_linear_workspace_bytes(333, n, k) == 0
+
+
+@pytest.mark.parametrize("hidden,inter", [(12, 8), (8, 12), (4, 8), (8, 4), (1 << 15, 1 << 14), ((1 << 20) + 8, 8),
+                                          (8, (1 << 19) + 8)])
+def test_block_asks_nothing_for_sizes_it_refuses(hidden, inter):
+    f = _abi.load().ep_gated_ffn_workspace_bytes
+    assert f(333, hidden, inter, 0) == f(333, hidden, inter, 1) == 0
