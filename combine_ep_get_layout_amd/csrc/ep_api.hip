@@ -732,7 +732,7 @@ int ep_cast_fp8_blocks(const void *w, int32_t num, int32_t n, int32_t k, uint8_t
         return EP_ERR_INVALID_ARG;
     if (n > EP_MAX_HIDDEN || k > EP_MAX_HIDDEN) return EP_ERR_UNSUPPORTED;
     const int64_t blocks = (int64_t)((n + 127) / 128) * ((k + 127) / 128);
-    if (blocks * num > 0x7fffffff) return EP_ERR_UNSUPPORTED;
+    if (!ep::launchable(blocks * num, 256)) return EP_ERR_UNSUPPORTED;    // a workgroup a block
     if (num == 0) return EP_OK;
     if (!w || !aligned16(w) || (!codes && !codes_t) || !aligned8(codes) || !aligned8(codes_t) ||
         !aligned4(scales) || !aligned4(scales_t))

@@ -269,7 +269,7 @@ hipError_t launch_tiles(BlockK &k, bool gated, int parts, hipStream_t stream) {
     const int per = gated ? WN * 32 : WN * 64;
     k.l.col_tiles = (k.l.m + per - 1) / per;
     const int64_t grid = grid_of(k.l.seg, k.l.col_tiles, BM);
-    if (grid > 0x7fffffff) return hipErrorInvalidConfiguration;
+    if (!launchable(grid, 64 * WN * WM)) return hipErrorInvalidConfiguration;
     const dim3 g((unsigned)grid, parts), t(64 * WN * WM);
     if (gated) block_linear_kernel<BM, WM, WN, NS, true, MODE><<<g, t, 0, stream>>>(k);
     else block_linear_kernel<BM, WM, WN, NS, false, MODE><<<g, t, 0, stream>>>(k);

@@ -94,7 +94,7 @@ __global__ __launch_bounds__(256) void cast_blocks_kernel(CastBlocksArgs a) {
 
 hipError_t launch_cast_blocks(const CastBlocksArgs &a, hipStream_t stream) {
     const int64_t grid = (int64_t)a.num * ((a.n + kB - 1) / kB) * ((a.k + kB - 1) / kB);
-    if (grid > 0x7fffffff) return hipErrorInvalidConfiguration;
+    if (!launchable(grid, 256)) return hipErrorInvalidConfiguration;
     const dim3 g((unsigned)grid), t(256);
     if (a.codes_t) cast_blocks_kernel<true><<<g, t, 0, stream>>>(a);
     else cast_blocks_kernel<false><<<g, t, 0, stream>>>(a);

@@ -81,6 +81,9 @@ struct ActBackwardArgs {
 
 hipError_t launch_act_backward(const ActBackwardArgs &a, hipStream_t stream);
 
+// Whether HIP launches so many workgroups: fewer than 2^32 threads.
+inline bool launchable(int64_t grid, int threads) { return grid <= 0xffffffff / threads; }
+
 // The activation function of an EP_ACT_* (0 none, 1 silu, 2 gelu).
 inline int act_kind(int act) {
     return act == EP_ACT_SILU || act == EP_ACT_SWIGLU ? 1

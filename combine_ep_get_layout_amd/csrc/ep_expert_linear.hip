@@ -8,7 +8,7 @@ namespace {
 
 hipError_t launch_wide(const LinearArgs &a, const LinearK &k, bool gated, hipStream_t stream) {
     const int64_t grid = grid_of(a.seg, k.col_tiles, 256);
-    if (grid > 0x7fffffff) return hipErrorInvalidConfiguration;
+    if (!launchable(grid, 256)) return hipErrorInvalidConfiguration;
     const dim3 g((unsigned)grid), t(256);
     if (a.fp8 && a.ckpt) {
         if (gated) expert_linear_wide_kernel<kFp8Exact, false, true><<<g, t, 0, stream>>>(k);
@@ -29,7 +29,7 @@ hipError_t launch_wide(const LinearArgs &a, const LinearK &k, bool gated, hipStr
 template <int BM, int WM, int WN, int NS>
 hipError_t launch_bm(const LinearArgs &a, const LinearK &k, bool gated, hipStream_t stream) {
     const int64_t grid = grid_of(a.seg, k.col_tiles, BM);
-    if (grid > 0x7fffffff) return hipErrorInvalidConfiguration;
+    if (!launchable(grid, 64 * WN * WM)) return hipErrorInvalidConfiguration;
     const dim3 g((unsigned)grid), t(64 * WN * WM);
     if (a.fp8 && a.ckpt) {
         if (gated) expert_linear_kernel<BM, WM, WN, NS, kFp8Exact, false, true><<<g, t, 0, stream>>>(k);

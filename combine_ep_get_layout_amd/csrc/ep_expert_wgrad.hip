@@ -31,7 +31,7 @@ hipError_t launch_expert_wgrad(const WgradArgs &a, hipStream_t stream) {
     const int T = wide ? kWT : kT;
     const WgradK k = kernel_args(a, T);
     const int64_t grid = grid_of(k);
-    if (grid > 0x7fffffff) return hipErrorInvalidConfiguration;
+    if (!launchable(grid, 256)) return hipErrorInvalidConfiguration;
     const dim3 g((unsigned)grid), t(256);
     if (wide) {
         if (a.fp8) {

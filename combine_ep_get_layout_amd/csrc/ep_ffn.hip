@@ -37,7 +37,7 @@ hipError_t launch_tiles(LinearK &k, int parts, hipStream_t stream) {
     const int per = GATED ? WN * 32 : WN * 64;
     k.col_tiles = (k.m + per - 1) / per;
     const int64_t grid = grid_of(k.seg, k.col_tiles, BM);
-    if (grid > 0x7fffffff) return hipErrorInvalidConfiguration;
+    if (!launchable(grid, 64 * WM * WN)) return hipErrorInvalidConfiguration;
     expert_linear_kernel<BM, WM, WN, NS, kBf16, WT, GATED, MODE>
         <<<dim3((unsigned)grid, parts), 64 * WM * WN, 0, stream>>>(k);
     return hipGetLastError();
@@ -52,7 +52,7 @@ hipError_t product(LinearK k, int64_t rows, float *sums, hipStream_t stream) {
         const int per = GATED ? kBN / 2 : kBN;
         k.col_tiles = (k.m + per - 1) / per;
         const int64_t grid = grid_of(k.seg, k.col_tiles, 256);
-        if (grid > 0x7fffffff) return hipErrorInvalidConfiguration;
+        if (!launchable(grid, 256)) return hipErrorInvalidConfiguration;
         expert_linear_wide_kernel<kBf16, WT, GATED, MODE><<<dim3((unsigned)grid), 256, 0, stream>>>(k);
         return hipGetLastError();
     }
@@ -345,7 +345,9 @@ hipError_t launch_gated_ffn_backward(const FfnBackwardArgs &a, hipStream_t strea
     const bool with_dx = a.dx && a.rows > 0, wide = plan.edge == kWT;
     const bool together = with_dx && wide == (dx.rows == 256);
     const int64_t grid = together ? w_blocks + (int64_t)p.x_blocks * dx.parts : w_blocks;
-    if (grid > 0x7fffffff || (int64_t)p.x.col_tiles * (a.rows / dx.rows + 1) > 0x7fffffff) return hipErrorInvalidConfiguration;
+    // (x_blocks, in 32 bits, too)
+    if (!launchable(grid, 256) || !launchable((int64_t)p.x.col_tiles * (a.rows / dx.rows + 1), 256))
+        return hipErrorInvalidConfiguration;
     const dim3 g((unsigned)grid), t(256);
     if (!together) {
         if (wide) wgrad_wide_pair_kernel<<<g, t, 0, stream>>>(p.w);

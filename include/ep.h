@@ -591,7 +591,7 @@ int ep_moe_decode(const void *x, const int64_t *topk_idx, const float *topk_weig
  * and keeps to itself; a block that holds an infinity has a NaN scale and NaN codes.
  * codes_t holds the same codes and scales transposed.  EP_ERR_INVALID_ARG (num < 0,
  * sizes, pointers; neither pair); EP_ERR_UNSUPPORTED (n or k above EP_MAX_HIDDEN,
- * 2^31 blocks or more). */
+ * 2^24 blocks or more). */
 int ep_cast_fp8_blocks(const void *w, int32_t num, int32_t n, int32_t k, uint8_t *codes,
                        float *scales, uint8_t *codes_t, float *scales_t, void *stream);
 
