@@ -12,10 +12,12 @@
 // lie in ordinary registers, so eight waves of 64 columns x 128 rows share a tile of
 // 256 x 256, not four of 128 x 128.
 //
-// Bound by the matrix instructions under the power limit: 32768 rows, 7168 to 4096 with
-// swiglu 0.80 to 0.84 ms (2.3 to 2.4 PFLOP/s, 1.7 to 1.8 GHz; without the scales' instructions
-// 0.68 to 0.77, and what saves cycles costs clock), 2048 to 7168 0.47 ms (2.0: 7 of a
-// tile's 34 us are its ends).
+// 8 experts of 4000 or 4096 rows each, 7168 to 4096 with swiglu, 0.88 ms (2.1 to 2.2
+// PFLOP/s; one matrix for 32768 dense rows 0.82, 2.35), 2048 to 7168 0.53 to 0.54 (1.8;
+// dense 0.48, 2.0).  A round of 256 tiles takes 106 to 111 and 36 to 38 us, and a partial
+// one as long as a full one: with one row more than 4096 an expert 0.96 and 0.56 ms.  The
+// matrix instructions run in 52% and 42% of the cycles; without the scales' instructions
+// the dense product took 0.68 to 0.77 ms.
 //
 // The weights are the instruction's first operand: a lane's values are consecutive
 // columns of one row, with one row scale, and a wave's 64 columns lie in one block

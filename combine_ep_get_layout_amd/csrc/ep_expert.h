@@ -92,9 +92,16 @@ inline int act_kind(int act) {
 inline bool act_gated(int act) { return act == EP_ACT_SWIGLU || act == EP_ACT_GEGLU; }
 
 // Dense rows, at most kFewRows of them.  Taken up to 16 rows, and for more while
-// they have few bytes, since every workgroup reads them: 7168 to 4096, gated, bf16, 24
-// rows 18.9 us, in tiles and parts 18.2, 64 rows 34 and 21; 2048 to 7168 32 rows 13.7
-// and 12.4; but 1024 to 4096, gated, 64 rows 7.5 and 9.2.
+// they have few bytes, since every workgroup reads them.  Both sides, us here and in
+// tiles, whole or in parts:
+//   bf16  7168 to 4096, gated, 24 rows 18.9 and 18.2, 64 rows 34 and 21; 2048 to 7168
+//         32 rows 13.7 and 12.4; but 1024 to 4096, gated, 64 rows 7.5 and 9.2
+//   e4m3  7168 to 4096, gated, 16 rows 10.7 and 15.6, 32 rows 15.2 and 16.2, 48 rows
+//         21 and 17; 4096 to 4096 32 rows 10.1 and 13.0; 1024 to 4096, gated, 64 rows
+//         6.5 and 7.5
+// (The limit in bytes was chosen for bf16.  In e4m3 it is too high for many columns of
+// short rows, 2048 to 7168 32 rows 10.3 and 9.8, 64 rows 16.2 and 10.0, and a little
+// low for 24 and 32 rows of 7168.)
 constexpr int kFewRows = 64;
 inline bool few_rows(int64_t rows, int64_t row_bytes) {
     return rows <= 16 || (rows <= kFewRows && rows * row_bytes <= 128 * 1024);

@@ -12,8 +12,10 @@
 // Many small workgroups hide the latency better than deep rings: four waves with two
 // units each, where eight waves with eight units took (back to back) 13.6 us for one
 // row of 7168 to 4096, gated, in bf16, these take 11.0 (5.3 TB/s); 13.9 and 7.2 for
-// 2048 to 7168; e4m3 9.7 and 8.1, 12.5 and 5.2.  Bound by reading the weights up to about
-// 8 rows, then by reading x: 16 rows 15.0, 64 rows 34 us.
+// 2048 to 7168; e4m3 9.7 and 8.1, 12.5 and 5.2.  (Eight waves with one unit each 10.7 and
+// 7.7, e4m3 7.4 and 5.5: better for the long contraction alone.)  Up to about 8 rows bound
+// by reading the weights, in e4m3 of 7168 channels at 3.6 TB/s by a wave's seven round
+// trips to memory; then by reading x: 16 rows 15.0, 64 rows 34 us.
 #include "ep_expert_device.h"
 
 namespace ep {

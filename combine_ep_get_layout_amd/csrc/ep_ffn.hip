@@ -10,7 +10,7 @@
 // type that the matrix instructions of these products take.
 //
 // 16384 tokens 7168/2048, back to back on one card: forward 1.02 to 1.06 ms (1.36 to
-// 1.41 PFLOP/s; a library product reaches 1.54), backward 2.26 to 2.34 (1.23 to 1.28), bound by
+// 1.41 PFLOP/s; a library product reaches 1.54), backward 2.23 to 2.34 (1.23 to 1.29), bound by
 // the matrix instructions under the power limit.
 #include "ep_linear_device.h"
 #include "ep_wgrad_device.h"
@@ -143,7 +143,8 @@ struct PairPlan { int edge, parts; int64_t each; };
 constexpr int kRuns[] = {1, 2, 3, 4, 6, 8};
 
 // Runs of `each` rows, if `rows` rows are cut into `parts` of them (0: they are not):
-// of 256 rows at least, and sums of 256 MB at most.
+// of 256 rows at least, and with sums of 256 MB at most (bounds of the choice and of
+// the workspace, whose other sides are not measured).
 int64_t run_of(int64_t rows, int parts, double elements) {
     if (parts == 1) return rows;
     const int64_t each = ((rows + parts - 1) / parts + kRows - 1) / kRows * kRows;

@@ -929,6 +929,23 @@ hipError_t launch_finish(const LinearK &k, int parts, hipStream_t stream) {
 // Parts: as many as make 400 workgroups of the tiles (two run on a compute unit), at
 // most 8 (more only move more sums) of at least 4 steps, where that saves 14 steps of
 // 0.3 to 0.6 us: the second launch takes 3 to 5 us, and 2.5 us of the host.
+//
+// The limits were chosen by these figures, of bf16 rows.  e4m3 rows, whose steps have
+// 128 channels, go by the same ones; us, with the other sides:
+//   256 x 256   1500 rows, 2048 to 7168 (168 tiles) 32, in 128 x 128 tiles 39; but 1000
+//               rows (112 tiles) 31 and 24; 2000 rows, 7168 to 4096, gated (128) 81 and 68
+//   64 x 64     whole: 333 rows, 2048 to 2048, gated, 10.0, in 64 x 128 tiles 12.4; in
+//               parts: 128 rows, 7168 to 4096, gated, 20, in 64 x 128 tiles and parts 22,
+//               whole 21.7
+//   128 x 128   700 rows, 2048 to 7168, 22.4, in 64 x 128 tiles 25.6; but 333 rows (168
+//               tiles) 19 and 16; 700 rows, 7168 to 4096, gated, 2 parts: 45, in 64 x 128
+//               tiles 48, those whole 39
+//   64 x 128    in parts: 333 rows, 7168 to 4096, gated, 31, in 128 x 128 tiles 32, whole
+//               30; but 1000 rows, 4096 to 1024, 20.6, in 64 x 64 tiles, whole, 15.3
+//
+// Not looked at is how full the columns of a tile are: 32768 e4m3 rows of 7168 to 128 (128
+// half empty tiles) take 86 us, in 64 x 128 tiles 47; 16384 rows to 264 82, in 128 x 128
+// tiles 60; to 520 84 and 109.
 struct DensePlan { int rows, cols, parts, split; };
 
 inline DensePlan dense_plan(int64_t rows, int n, int steps, bool transposed) {

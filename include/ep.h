@@ -622,14 +622,15 @@ size_t ep_block_linear_workspace_bytes(int64_t num_rows, int32_t n, int32_t k);
  *              dense rows (scratch of this call), else unused.
  *   out        device bf16 [num_rows, m], 16-byte aligned.
  * A block's sum is the fp8 instruction's (fp32; it cuts products below 2^-13 of
- * the largest of their 8 channels); the blocks are scaled and added in fp32.  The
- * data gradient is the same call on gradient rows cast to 8 bits and the codes_t of
- * the weights.  Two calls on the same inputs give the same bits; a row's result does
- * not depend on the others' values, but with another number of rows its sums may be
- * formed in another order.  Errors: EP_ERR_INVALID_ARG (more than 2^31 - 1024 dense
- * rows among them); EP_ERR_WORKSPACE;
- * EP_ERR_UNSUPPORTED (k or n above EP_MAX_HIDDEN, a matrix of 2^31 - 4096 bytes or
- * more). */
+ * the largest of their 8 channels); the blocks are scaled, by the fp32 product of
+ * their two scales (one outside fp32's normal range loses digits, or is infinite),
+ * and added in fp32.  The data gradient is the same call on gradient rows cast to 8
+ * bits and the codes_t of the weights.  Two calls on the same inputs give the same
+ * bits; a row's result does not depend on the others' values, but with another
+ * number of rows its sums may be formed in another order.  Errors:
+ * EP_ERR_INVALID_ARG (more than 2^31 - 1024 dense rows among them);
+ * EP_ERR_WORKSPACE; EP_ERR_UNSUPPORTED (k or n above EP_MAX_HIDDEN, a matrix of
+ * 2^31 - 4096 bytes or more). */
 int ep_block_linear(const void *x, const float *x_scales, const void *w, const float *w_scales,
                     int32_t n, int32_t k, const void *bias, int act, const void *residual,
                     const ep_layout_params *params, const ep_layout *layout, int64_t num_rows,
